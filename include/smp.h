@@ -363,6 +363,47 @@ smp_status smp_beam_topk(const void* logits, const double* beam_scores, int32_t 
                          void* stream);
 
 /*
+ * smp_spec_verify_probs -- the check of drafted tokens against the target's
+ * probabilities, with random numbers that the caller supplies.  The rule is
+ * smp_spec_verify's ("Decoding & Speculative Sampling", section 39.4, eqs.
+ * 39.3 and 39.4) on probabilities instead of logits: draft x at position i is
+ * kept when u_i q_i(x) < p_i(x); at the first rejection j the replacement
+ * follows max(0, p_j - q_j) (p_j where that is zero everywhere); if all are
+ * kept a bonus token follows the next target row.  The draw is a race of
+ * exponential variables: with e_i independent and exponentially distributed,
+ * the index of the largest w_i / e_i has the distribution w_i / sum w.  So no
+ * normaliser is needed, and with products, differences and quotients rounded
+ * once to binary32 the tokens do not depend on any order of summation: equal
+ * quotients keep the lower id.
+ *
+ *   p           device, [batch, k+1, vocab] contiguous, dtype elements:
+ *               target probabilities (a row's common factor matters to the
+ *               accept test and the difference, not to the draw).
+ *   q           device, [batch, k, vocab] contiguous, same dtype: draft
+ *               probabilities, or NULL for drafts proposed with certainty
+ *               (q_i is 1 at the draft and 0 elsewhere).
+ *   draft_ids   device, [batch, k] int32 (NULL when k = 0).
+ *   draft_lens  device, [batch] int32 in 0 .. k, the drafts that each row
+ *               really has (the bonus row is then row draft_lens[b]), or NULL
+ *               for k.
+ *   uniforms    device, [batch, k] float in [0, 1) (NULL when k = 0).
+ *   noise       device, [batch, vocab] float, exponential variables > 0.
+ *   batch 0 .. 2^20;  k 0 .. SMP_MAX_DRAFT;  vocab 1 .. SMP_MAX_VOCAB.
+ *   out_accepted_len  device, [batch] int32: accepted drafts (-1: error).
+ *   out_ids     device, [batch, k+1] int32: the accepted drafts, the
+ *               replacement or bonus token, then -1.
+ *   status      device int32 or NULL, as for smp_sample.
+ * A row with a draft id outside [0, vocab) or a length outside 0 .. k is an
+ * error row (SMP_ROW_BAD_DRAFT), and so is one whose target row has no
+ * positive probability to draw from (SMP_ROW_NONFINITE).  NaN probabilities
+ * reject their draft and are never drawn.
+ */
+smp_status smp_spec_verify_probs(const void* p, const void* q, const int32_t* draft_ids, const int32_t* draft_lens,
+                                 int32_t batch, int32_t k, int32_t vocab, smp_dtype dtype, const float* uniforms,
+                                 const float* noise, int32_t* out_accepted_len, int32_t* out_ids, int32_t* status,
+                                 void* stream);
+
+/*
  * Size of the device array that smp_spec_verify_static uses as its workspace
  * (1 MiB: enough for batch * (2k+1) <= 32768, e.g. 1024 rows with k = 15).
  */

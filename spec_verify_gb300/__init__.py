@@ -6,4 +6,4 @@ The compute lives in libsmp.so (C ABI: include/smp.h), built in-tree by
 PyTorch tensors; `spec_verify_gb300.workloads` makes seeded synthetic inputs.
 """
 
-__all__ = ["binding", "build", "workloads"]
+__all__ = ["binding", "build", "cache", "workloads"]

@@ -23,12 +23,16 @@ ROW_BAD_PARAMS = 1
 ROW_NONFINITE = 2
 ROW_TIMEOUT = 4
 ROW_BAD_DRAFT = 8
+ROW_BAD_LENGTH = 16
+ROW_NO_CAPACITY = 32
+ROW_BAD_BLOCK = 64
 
-# Symbols declared in include/smp.h.
+# Symbols declared in include/smp.h and include/smp_cache.h.
 EXPORTS = ("smp_sample", "smp_filter_debug", "smp_sample_processed", "smp_sample_rows", "smp_logit_prepass",
            "smp_beam_topk_workspace_bytes", "smp_beam_topk", "smp_spec_verify_workspace_bytes",
            "smp_spec_verify", "smp_spec_verify_params", "smp_spec_verify_rows", "smp_spec_verify_static",
-           "smp_status_string", "smp_last_cuda_error", "smp_abi_version")
+           "smp_spec_verify_probs", "smp_block_plan", "smp_qk_norm_rope", "smp_cache_append",
+           "smp_cache_attention_workspace_bytes", "smp_cache_attention", "smp_status_string", "smp_last_cuda_error", "smp_abi_version")
 
 STATIC_VERIFY_SCRATCH_BYTES = 1 << 20
 
@@ -83,6 +87,22 @@ def load():
     lib.smp_spec_verify_rows.restype = i32
     lib.smp_spec_verify_static.argtypes = [vp, vp, vp, i32, i32, i32, i32, u64, u64, vp, vp, vp, vp]
     lib.smp_spec_verify_static.restype = i32
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    lib.smp_spec_verify_probs.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.smp_spec_verify_probs.restype = i32
+    lib.smp_block_plan.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp,
+                                   vp, vp]
+    lib.smp_block_plan.restype = i32
+    lib.smp_qk_norm_rope.argtypes = [vp, vp, i32, i32, i32, i32, i64, i64, i32, vp, vp, f32, vp, i32, i32, i32, vp,
+                                     vp, vp, i64, i64, vp, vp]
+    lib.smp_qk_norm_rope.restype = i32
+    lib.smp_cache_append.argtypes = [vp, vp, vp, i32, i64, i64, i32, vp, vp, vp]
+    lib.smp_cache_append.restype = i32
+    lib.smp_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.smp_cache_attention_workspace_bytes.restype = sz
+    lib.smp_cache_attention.argtypes = [vp, vp, i32, i32, i64, i32, vp, vp, i32, vp, i32, f32, i32, vp, i64, vp, vp,
+                                        vp, sz, vp]
+    lib.smp_cache_attention.restype = i32
     lib.smp_status_string.argtypes = [i32]
     lib.smp_status_string.restype = ctypes.c_char_p
     lib.smp_last_cuda_error.argtypes = []
@@ -398,3 +418,40 @@ def beam_topk(logits, beam_scores, width=None, workspace=None, out_parent=None, 
                              _ptr(out_parent), _ptr(out_token), _ptr(out_score), _ptr(status), _ptr(workspace),
                              workspace.numel(), _stream(stream)))
     return out_parent, out_token, out_score, status
+
+
+def spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens=None, out_accepted=None, out_ids=None, status=None,
+                      stream=None):
+    """smp_spec_verify_probs on probabilities p [B, K+1, V] and q [B, K, V]
+    (float32/bfloat16; q None: drafts proposed with certainty), draft ids
+    [B, K] (int32), uniforms [B, K] and exponential noise [B, V] (float32);
+    draft_lens: int32 [B], the drafts each row really has, or None for K.
+    status: an int32 [1] tensor for the SMP_ROW_* flags, or None (no status
+    word).  Returns (accepted_len int32 [B], ids int32 [B, K+1])."""
+    torch = _torch()
+    lib = load()
+    if p.dim() != 3 or noise.dim() != 2 or draft_ids.dim() != 2:
+        raise SmpError("expected p [B, K+1, V], draft_ids [B, K], noise [B, V]")
+    batch, k1, vocab = p.shape
+    k = k1 - 1
+    if (q is not None and (q.shape != (batch, k, vocab) or q.dtype != p.dtype)) or noise.shape != (batch, vocab) or \
+            draft_ids.shape != (batch, k) or uniforms.shape != (batch, k):
+        raise SmpError("shape mismatch between p, q, draft_ids, uniforms and noise")
+    if draft_ids.dtype != torch.int32 or uniforms.dtype != torch.float32 or noise.dtype != torch.float32:
+        raise SmpError("draft_ids must be int32, uniforms and noise float32")
+    if draft_lens is not None and (draft_lens.shape != (batch,) or draft_lens.dtype != torch.int32):
+        raise SmpError("draft_lens must be an int32 [B] CUDA tensor")
+    if out_accepted is None:
+        out_accepted = torch.empty(batch, dtype=torch.int32, device=p.device)
+    if out_ids is None:
+        out_ids = torch.empty(batch, k1, dtype=torch.int32, device=p.device)
+    if out_accepted.shape != (batch,) or out_ids.shape != (batch, k1) or out_accepted.dtype != torch.int32 or \
+            out_ids.dtype != torch.int32:
+        raise SmpError("out_accepted must be int32 [B] and out_ids int32 [B, K+1]")
+    for t in (p, q, draft_ids, uniforms, noise, draft_lens, out_accepted, out_ids, status):
+        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+            raise SmpError("expected contiguous CUDA tensors")
+    _check(lib.smp_spec_verify_probs(_ptr(p), _ptr(q), _ptr(draft_ids), _ptr(draft_lens), batch, k, vocab,
+                                     _dtype_code(p), _ptr(uniforms), _ptr(noise), _ptr(out_accepted), _ptr(out_ids),
+                                     _ptr(status), _stream(stream)))
+    return out_accepted, out_ids

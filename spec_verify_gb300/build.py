@@ -21,8 +21,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsmp.so")
 
-SOURCES = ["api.cu", "sample.cu", "verify.cu", "prepass.cu", "beam.cu"]
-HEADERS = ["common.cuh", "row_ops.cuh", "select.cuh", "general.cuh", "launch.h", "exp_table.h", "tma.cuh", "general_bf16.cuh"]
+SOURCES = ["api.cu", "sample.cu", "verify.cu", "prepass.cu", "beam.cu", "verify_probs.cu", "block_plan.cu",
+           "norm_rope.cu", "cache_append.cu", "cache_attention.cu"]
+HEADERS = ["common.cuh", "row_ops.cuh", "select.cuh", "general.cuh", "launch.h", "exp_table.h", "tma.cuh", "general_bf16.cuh",
+           "cache.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -41,7 +43,7 @@ def nvcc():
 
 def _newest_input():
     paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    paths.append(os.path.join(INCLUDE, "smp.h"))
+    paths += [os.path.join(INCLUDE, f) for f in ("smp.h", "smp_cache.h")]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 

@@ -1,0 +1,232 @@
+// Block tables and slot maps of one step, from request lengths.
+//
+// Mathematics: with n_b the blocks that request b lacks, its first new block
+// is entry head + sum_{c<b} n_c of the free list and its first token is
+// sum_{c<b} add_c: two exclusive prefix sums, after which every token's
+// place follows from its own request alone.
+//
+// Bound: 16 bytes written per token (position, request, slot) and the latency
+// of one launch for small steps.  Tokens, not requests, are split over the
+// CTAs, since one prompt can be longer than all other requests together.
+// Every CTA repeats the prefix sums over all requests (12 bytes each, from
+// L2) instead of waiting for another kernel or CTA, keeps those that meet its
+// own tokens in shared memory, and finds each token's request by a running
+// maximum over the marks that the requests' first tokens leave.
+#include <cuda_runtime.h>
+
+#include "cache.cuh"
+#include "launch.h"
+#include "smp.h"
+
+namespace smp {
+
+constexpr int kPlanTokensPerThread = 4;
+constexpr int kPlanTokens = kThreads * kPlanTokensPerThread;   // per CTA
+
+struct PlanArgs {
+  const int32_t* lens;
+  const int32_t* add;
+  const int32_t* held;
+  int batch;
+  const int32_t* free_blocks;
+  int free_count;
+  const int32_t* free_head;
+  int32_t* table;
+  int stride;
+  int shift;        // log2(block_size)
+  int num_blocks;
+  int max_tokens;
+  int32_t* out_lens;
+  int32_t* out_held;
+  int32_t* out_head;
+  int32_t* out_start;
+  int32_t* out_position;
+  int32_t* out_request;
+  int64_t* out_slot;
+  int32_t* status;
+};
+
+// What a token needs to know of its request.
+struct PlanRequest {
+  int request;
+  int first;      // the request's first token in the step
+  int len;        // tokens held before the step
+  int held;       // blocks held before the step
+  int fresh;      // index into free_blocks of the request's first new block
+};
+
+// Sum over the threads before this one; `total` gets the sum over all.
+__device__ __forceinline__ uint64_t block_exclusive_u64(uint64_t v, uint64_t* scratch, uint64_t& total) {
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  const uint64_t inc = warp_inclusive_scan<uint64_t>(v);
+  cta_sync();
+  if (lane == 31) scratch[warp] = inc;
+  cta_sync();
+  uint64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(kThreads) block_plan_kernel(const PlanArgs a) {
+  __shared__ PlanRequest req[kPlanTokens];   // at the local index of the request's first token here
+  __shared__ int16_t mark[kPlanTokens];      // that index, or -1
+  __shared__ uint64_t scratch[kWarps];
+  __shared__ int warp_last[kWarps];
+  allow_dependent_launch();
+  grid_dependency_wait();
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int64_t t0 = int64_t(blockIdx.x) * kPlanTokens, t1 = t0 + kPlanTokens;
+  const int64_t head = *a.free_head;
+  const int64_t avail = head >= 0 && head <= a.free_count ? a.free_count - head : 0;
+  const int round = (1 << a.shift) - 1;
+  int flags = head >= 0 && head <= a.free_count ? 0 : kRowBadLength;
+#pragma unroll
+  for (int i = 0; i < kPlanTokensPerThread; ++i) mark[i * kThreads + tid] = -1;
+
+  // Prefix sums over the requests.  Sums wanted so far decide who is served;
+  // both kinds grow with b, so the served requests that add anything are the
+  // first ones.
+  int64_t tokens = 0, blocks = 0;               // wanted by the requests before this chunk
+  int64_t served_tokens = 0, served_blocks = 0; // of the served ones before this chunk
+  for (int base = 0; base < a.batch; base += kThreads) {
+    const int b = base + tid;
+    int len = 0, add = 0, held = 0;
+    int64_t want = 0, need = 0;
+    bool valid = true;
+    if (b < a.batch) {
+      len = a.lens[b], add = a.add[b], held = a.held[b];
+      const int64_t after = int64_t(len) + add;
+      need = (after + round) >> a.shift;
+      valid = len >= 0 && add >= 0 && after <= 0x7FFFFFFF && held <= a.stride && need <= a.stride &&
+              ((int64_t(len) + round) >> a.shift) <= held;
+      if (!valid) flags |= kRowBadLength;
+      need = need > held ? need - held : 0;
+      want = valid ? add : 0;
+      need = want ? need : 0;
+    }
+    uint64_t chunk_tokens, chunk_blocks;
+    const int64_t before_t = tokens + int64_t(block_exclusive_u64(uint64_t(want), scratch, chunk_tokens));
+    const int64_t before_b = blocks + int64_t(block_exclusive_u64(uint64_t(need), scratch, chunk_blocks));
+    tokens += int64_t(chunk_tokens);
+    blocks += int64_t(chunk_blocks);
+    const bool fits = before_t + want <= a.max_tokens && before_b + need <= avail;
+    const bool served = want > 0 && fits;
+    if (want > 0 && !fits) flags |= kRowNoCapacity;
+    uint64_t got_tokens, got_blocks;
+    const int64_t start = served_tokens + int64_t(block_exclusive_u64(served ? uint64_t(want) : 0, scratch, got_tokens));
+    block_exclusive_u64(served ? uint64_t(need) : 0, scratch, got_blocks);
+    served_tokens += int64_t(got_tokens);
+    served_blocks += int64_t(got_blocks);
+    if (b < a.batch) {
+      if ((base / kThreads) % int(gridDim.x) == int(blockIdx.x)) {
+        a.out_lens[b] = served ? len + add : len;
+        a.out_held[b] = served ? held + int(need) : held;
+        a.out_start[b] = int(start);
+      }
+      if (served && start < t1 && start + want > t0) {
+        const int at = int(start > t0 ? start - t0 : 0);
+        mark[at] = int16_t(at);
+        req[at] = {b, int(start), len, held, int(head + before_b)};
+      }
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.out_start[a.batch] = int(served_tokens);
+    *a.out_head = int(head + served_blocks);
+  }
+  cta_sync();
+
+  // The running maximum of the marks is each token's request.
+  int owner[kPlanTokensPerThread], run = -1;
+#pragma unroll
+  for (int i = 0; i < kPlanTokensPerThread; ++i) {
+    run = max(run, int(mark[tid * kPlanTokensPerThread + i]));
+    owner[i] = run;
+  }
+  int before = run;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before = max(before, o);
+  }
+  if (lane == 31) warp_last[warp] = before;
+  before = __shfl_up_sync(~0u, before, 1);
+  if (lane == 0) before = -1;
+  cta_sync();
+  for (int w = 0; w < warp; ++w) before = max(before, warp_last[w]);
+
+  for (int i = 0; i < kPlanTokensPerThread; ++i) {
+    const int64_t t = t0 + tid * kPlanTokensPerThread + i;
+    if (t >= a.max_tokens) break;
+    int position = -1, request = -1;
+    int64_t slot = -1;
+    if (t < served_tokens) {
+      const PlanRequest& r = req[max(owner[i], before)];
+      position = r.len + int(t - r.first);
+      request = r.request;
+      const int block = position >> a.shift;
+      const int64_t entry = int64_t(request) * a.stride + block;
+      const int id = block < r.held ? a.table[entry] : a.free_blocks[r.fresh + block - r.held];
+      if (id >= 0 && id < a.num_blocks) slot = (int64_t(id) << a.shift) + (position & round);
+      else flags |= kRowBadBlock;
+      if (block >= r.held && (position & round) == 0) a.table[entry] = id;
+    }
+    a.out_position[t] = position;
+    a.out_request[t] = request;
+    a.out_slot[t] = slot;
+  }
+  if (flags && a.status) atomicOr(a.status, flags);
+}
+
+}  // namespace smp
+
+extern "C" smp_status smp_block_plan(const int32_t* lens, const int32_t* add, const int32_t* held, int32_t batch,
+                                     const int32_t* free_blocks, int32_t free_count, const int32_t* free_head,
+                                     int32_t* block_table, int32_t table_stride, int32_t block_size,
+                                     int32_t num_blocks, int32_t max_tokens, int32_t* out_lens, int32_t* out_held,
+                                     int32_t* out_free_head, int32_t* out_start, int32_t* out_position,
+                                     int32_t* out_request, int64_t* out_slot, int32_t* status, void* stream) {
+  using namespace smp;
+  if (batch < 0 || batch > (1 << 24) || free_count < 0 || table_stride < 0 || num_blocks <= 0 || max_tokens < 0)
+    return SMP_ERR_INVALID_ARG;
+  if (block_size < 16 || block_size > 256 || (block_size & (block_size - 1))) return SMP_ERR_INVALID_ARG;
+  if (!free_head || !out_free_head || !out_start) return SMP_ERR_INVALID_ARG;
+  if (batch > 0 && (!lens || !add || !held || !out_lens || !out_held || (table_stride > 0 && !block_table)))
+    return SMP_ERR_INVALID_ARG;
+  if (free_count > 0 && !free_blocks) return SMP_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!out_position || !out_request || !out_slot)) return SMP_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(add), static_cast<const void*>(held),
+                        static_cast<const void*>(free_blocks), static_cast<const void*>(free_head),
+                        static_cast<const void*>(block_table), static_cast<const void*>(out_lens),
+                        static_cast<const void*>(out_held), static_cast<const void*>(out_free_head),
+                        static_cast<const void*>(out_start), static_cast<const void*>(out_position),
+                        static_cast<const void*>(out_request), static_cast<const void*>(status)})
+    if (misaligned(p, 4)) return SMP_ERR_INVALID_ARG;
+  if (misaligned(out_slot, 8)) return SMP_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status) {
+    const smp_status rc = clear_status(status, st);
+    if (rc != SMP_OK) return rc;
+  }
+  PlanArgs a{};
+  a.lens = lens, a.add = add, a.held = held, a.batch = batch;
+  a.free_blocks = free_blocks, a.free_count = free_count, a.free_head = free_head;
+  a.table = block_table, a.stride = table_stride, a.num_blocks = num_blocks;
+  for (a.shift = 0; (1 << a.shift) < block_size;) ++a.shift;
+  a.max_tokens = max_tokens;
+  a.out_lens = out_lens, a.out_held = out_held, a.out_head = out_free_head, a.out_start = out_start;
+  a.out_position = out_position, a.out_request = out_request, a.out_slot = out_slot;
+  a.status = status;
+  LaunchShape ls;
+  ls.pdl = true;
+  const int64_t ctas = (int64_t(max_tokens) + kPlanTokens - 1) / kPlanTokens;
+  const cudaError_t err = launch_cluster(reinterpret_cast<const void*>(&block_plan_kernel),
+                                         dim3(unsigned(ctas > 0 ? ctas : 1)), dim3(kThreads), ls, st, &a);
+  if (err != cudaSuccess) return fail_cuda(err);
+  return SMP_OK;
+}
