@@ -67,6 +67,8 @@ extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q,
   a.joins = static_cast<int4*>(workspace);
   a.partial = reinterpret_cast<float*>(a.joins + device_sms(dev) * kAttnCtasPerSm);
   a.min_share = 8;
+  a.q_vector = !misaligned(q, 16) && q_stride * int64_t(elem) % 16 == 0;
+  a.out_vector = !misaligned(out, 4 * elem) && out_stride % 4 == 0;
   // the tile shape follows the average request; longer ones take several row tiles
   const int64_t rows = (int64_t(tokens) + batch - 1) / batch * a.group;
   const bool e4m3 = cache->type == SMP_CACHE_E4M3, split = dtype == SMP_F32;

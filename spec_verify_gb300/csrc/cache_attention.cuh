@@ -3,14 +3,14 @@
 //
 // Mathematics.  For the rows of one key head (its queries times the query
 // heads that share it) and tiles of keys:
-//   S^T = K Q^T,  P = 2^(S c - m + 3),  O^T += V^T P^T,  l += sum P
-// with c = scale * log2(e) * (the block's key scale) and m a row reference
-// that is only raised when a score passes it by more than 8 (then O and l are
-// multiplied by 2^(m_old - m_new)), so P stays below 2^11.  A block's value
-// scale multiplies P, relative to the largest one met so far (at most 16 times
-// that before O is rescaled), so the products' second factor stays below 2^15
-// and fits 16-bit floats, whose smallest step is then 2^-35 of the largest
-// weight's: far below the 11-bit rounding of the weights that matter.
+//   S^T = K Q^T,  P = 2^(S c - m),  l += sum P,  O^T += V^T (P v u)
+// with c = scale * log2(e) * (the block's key scale), v the block's value
+// scale, and two references per row that move only when they must: m, raised
+// when a score passes it by more than 2^11 (then O and l are multiplied by
+// 2^(m_old - m_new)), and u, a power of two, lowered when a weight P v u would
+// pass 2^15, the range of 16-bit floats.  Both leave the largest weights far
+// above the smallest normal 16-bit float, so the weights that matter keep all
+// 11 bits whatever the scales of the blocks; l is summed from binary32 P.
 //
 // Both products run on the tensor cores with the cache as the 16-row operand
 // (tokens, then head elements) and the query rows as the 8-wide one, so one
@@ -44,9 +44,11 @@ namespace smp {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnUnitCost = 3;        // a unit's fixed cost, in tiles
-constexpr float kShift = 3.0f;          // P = 2^(s - m + 3)
-constexpr float kRaise = 8.0f;          // m follows a score only past this
-constexpr float kVRaise = 16.0f;        // the value scale's reference likewise
+constexpr float kShift = 3.0f;          // a new reference m puts the row's largest score at 2^3
+constexpr float kRaise = 11.0f;         // and is replaced once a score passes 2^11
+constexpr uint32_t kWeightLimit = 0x7800u;       // 2^15 as a 16-bit float: u is lowered past it
+constexpr int kWeightExp = 8;                    // a new u puts the largest weight in [2^8, 2^9)
+constexpr int kMaxUExp = 60;                     // u <= 2^60 and v <= 2^66, so that v u is finite
 
 struct AttnArgs {
   const uint8_t* k;
@@ -70,7 +72,7 @@ struct AttnArgs {
   int32_t* status;
   float* partial;           // [CTA][2][rows][dim_padded + 2]
   int4* joins;              // [CTA]: request, row tile, key head, parts of the unit that begins there (0: none)
-  int row_groups;           // warps per team
+  bool q_vector, out_vector;   // queries and results take 16-byte (results: 4-element) accesses
   int min_share;            // smallest share of a CTA, in tiles
 };
 
@@ -118,6 +120,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return w;
 }
 
+__device__ __forceinline__ void store4(uint16_t* p, const float (&x)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
 // What pack_f16 left out, as 16-bit floats.
 __device__ __forceinline__ uint32_t rest_f16(uint32_t packed, float lo, float hi) {
   float a, b;
@@ -142,6 +151,44 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) 
   }
 }
 
+// The larger of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
+// Pairs of binary32 numbers in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+  return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+  return y;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -159,6 +206,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
   return v;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // 16 bytes global to shared, or zeros where !live (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 16 : 0;
@@ -176,7 +226,7 @@ __device__ __forceinline__ void copies_wait() {
 
 // ---------------------------------------------------------------- shapes
 
-template <int kDP, int kNT, bool kSplit>
+template <int kDP, int kNT, int kRG, bool kSplit>
 struct AttnShape {
   static constexpr int kTile = kDP == 256 ? 16 : 32;             // tokens per tile
   static constexpr int kMT = kTile / 16;                         // 16-token row tiles of a tile
@@ -184,47 +234,41 @@ struct AttnShape {
   static constexpr int kSteps = kDP / 16;                        // products of depth 16 over the head
   static constexpr int kDT = kDP / 16;                           // 16-row tiles of V^T
   static constexpr int kStage = 2 * kTile * kDP;                 // bytes of one ring stage (keys, then values)
+  static constexpr int kTeams = kAttnWarps / kRG;
   static constexpr int kWarpRows = 8 * kNT;
+  static constexpr int kRows = kWarpRows * kRG;                  // rows of a unit's row tile
   static constexpr int kParts = kSplit ? 2 : 1;
   static constexpr bool kQReg = kNT * kSteps * 2 * kParts <= 32; // query fragments in registers
   static constexpr int kOPitch = kDP + 4;                        // floats of a row when teams are joined
   // stages of a team's ring: 96, 80 or 64 KB per CTA for teams of 1, 2 or 4 warps, whose queries take up to 8, 16
   // or 32 KB
-  static constexpr int depth(int row_groups) {
-    return (kDP == 64 ? 2 : 1) * (row_groups == 4 ? 8 : row_groups == 2 ? 5 : 3);
-  }
-  static int ring_bytes(int row_groups) {
-    const int ring = kAttnWarps / row_groups * depth(row_groups) * kStage;
-    const int join = kAttnWarps * kWarpRows * kOPitch * 4;
-    return ring > join ? ring : join;
-  }
-  static int query_bytes(int row_groups) { return kQReg ? 0 : row_groups * kNT * kSteps * kParts * 32 * 8; }
-  static constexpr int kMaxStages = (kDP == 64 ? 2 : 1) * 12;    // most stages of all teams' rings
-  // scales and flags of every stage, then the rows' (m, l) of each warp
-  static constexpr int kMetaBytes = kMaxStages * kMT * 12 + 3 * kAttnWarps * kWarpRows * 4;
-  static int smem(int row_groups) { return ring_bytes(row_groups) + query_bytes(row_groups) + kMetaBytes; }
+  static constexpr int kDepth = (kDP == 64 ? 2 : 1) * (kRG == 4 ? 8 : kRG == 2 ? 5 : 3);
+  static constexpr int kRing = kTeams * kDepth * kStage;
+  static constexpr int kJoin = kAttnWarps * kWarpRows * kOPitch * 4;
+  static constexpr int kRingBytes = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kQueryBytes = kQReg ? 0 : kRows / 8 * kSteps * kParts * 32 * 8;
+  // per stage: kMT key scales, kMT value scales, kMT flags; then (m, l, weight) of every warp's rows
+  static constexpr int kScaleBytes = kTeams * kDepth * kMT * 12;
+  static constexpr int kSmem = kRingBytes + kQueryBytes + kScaleBytes + 3 * kAttnWarps * kWarpRows * 4;
 };
 
 // ---------------------------------------------------------------- main kernel
 
-template <int kDP, int kNT, int kType, bool kSplit>
-__global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnArgs a, const int ring_bytes,
-                                                                    const int query_bytes) {
-  using S = AttnShape<kDP, kNT, kSplit>;
+template <int kDP, int kNT, int kRG, int kType, bool kSplit>
+__global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnArgs a) {
+  using S = AttnShape<kDP, kNT, kRG, kSplit>;
   using T = typename std::conditional<kSplit, float, uint16_t>::type;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scan[kAttnWarps + 1];
   __shared__ int64_t found[2];
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rgs = a.row_groups, teams = kAttnWarps / rgs, team = warp / rgs, rg = warp % rgs;
-  const int rows = S::kWarpRows * rgs;                  // rows of a unit's row tile
-  const int depth = S::depth(rgs);                      // stages of this team's ring
+  constexpr int teams = S::kTeams, rows = S::kRows, depth = S::kDepth, ring_bytes = S::kRingBytes;
+  const int team = warp / kRG, rg = warp % kRG;
   const uint32_t ring = smem_addr(smem) + uint32_t(team * depth) * S::kStage;
-  uint8_t* const meta = smem + ring_bytes + query_bytes;
-  // per team and stage: kMT key scales, kMT value scales, kMT flags
+  uint8_t* const meta = smem + ring_bytes + S::kQueryBytes;
   float* const meta_scale = reinterpret_cast<float*>(meta) + team * depth * S::kMT * 3;
-  float* const row_m = reinterpret_cast<float*>(meta + S::kMaxStages * S::kMT * 12);   // [warp][row]
+  float* const row_m = reinterpret_cast<float*>(meta + S::kScaleBytes);       // [warp][row]
   float* const row_l = row_m + kAttnWarps * S::kWarpRows;
   float* const row_w = row_l + kAttnWarps * S::kWarpRows;
 
@@ -302,13 +346,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
   int64_t pos = mine - found[1] - unit * cost;
   int rt = int(unit / a.kv_heads), head = int(unit - int64_t(rt) * a.kv_heads);
 
-  const int my_chunk = S::kChunks == 4 ? lane & 3 : S::kChunks == 8 ? lane & 7 : lane & 15;
-  constexpr int kRowsPerCopy = 32 / S::kChunks;              // rows that one copy instruction covers
-  constexpr int kCopies = 2 * S::kTile / kRowsPerCopy;       // copy instructions of a stage, over the team's warps
-  const int my_row = lane / S::kChunks;
+  // A stage's copies: one instruction covers kRowsPerCopy rows, keys first; the warps of a team take turns.
+  constexpr int kRowsPerCopy = 32 / S::kChunks, kCopies = 2 * S::kTile / kRowsPerCopy, kHalf = kCopies / 2;
+  constexpr int kPerMT = kHalf / S::kMT;                     // copies of 16 tokens' keys
+  constexpr int kSwizzles = 8 / kRowsPerCopy / kRG > 1 ? 8 / kRowsPerCopy / kRG : 1;
+  const int my_chunk = lane % S::kChunks, my_row = lane / S::kChunks;
   // chunk c of row r lies at chunk c ^ swizzle(r): 16-byte reads of keys (8 rows, 4 chunks) and of values (8 rows two
   // apart, 2 chunks) then meet every bank once
   auto swizzle = [](int r) { return kDP == 64 ? (r >> 1) & 3 : (r & 6) ^ ((r & 1) << 2); };
+  uint32_t lane_dst[kSwizzles];
+#pragma unroll
+  for (int i = 0; i < kSwizzles; ++i)
+    lane_dst[i] = uint32_t((rg * kRowsPerCopy + my_row) * kDP +
+                           ((my_chunk ^ swizzle((i * kRG + rg) * kRowsPerCopy + my_row)) * 16));
+  const int lane_src = ((rg % kPerMT) * kRowsPerCopy + my_row) * kDP + my_chunk * 16;
 
   while (at < end) {
     const int64_t take = min(cost - pos, end - at);
@@ -338,52 +389,72 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
       return id;
     };
     int ids = load_ids(0), ids_next = load_ids(kPer);
-    auto issue = [&](int k) {
-      if (k < iters) {
-        if (k > 0 && k % kPer == 0) {
+    int in_k = 0, in_slot = 0, in_id = 0, in_token = (tile_lo + team) * S::kTile;
+    const int64_t head_at = (int64_t(head) << a.shift) * a.dim, block_size_all = (int64_t(a.kv_heads) << a.shift) * a.dim;
+    auto issue = [&]() {
+      if (in_k < iters) {
+        if (in_id == 32) {
+          in_id = 0;
           ids = ids_next;
-          ids_next = load_ids(k + kPer);
+          ids_next = load_ids(in_k + kPer);
         }
-        const int slot = k % depth, token0 = (tile_lo + team + k * teams) * S::kTile;
-        const uint32_t dst = ring + uint32_t(slot) * S::kStage;
-        const uint8_t* src[2][S::kMT];
-        bool ok[S::kMT];
+        const uint32_t dst = ring + uint32_t(in_slot) * S::kStage;
+        int64_t off[S::kMT];
+        bool ok[S::kMT], full = in_token + S::kTile <= len && a.dim == kDP;
 #pragma unroll
         for (int mt = 0; mt < S::kMT; ++mt) {
-          const int id = __shfl_sync(~0u, ids, (k % kPer) * S::kMT + mt);
+          const int id = __shfl_sync(~0u, ids, in_id + mt);
           ok[mt] = id >= 0;
-          const int64_t bh = int64_t(max(id, 0)) * a.kv_heads + head;
-          const int64_t off = ((bh << a.shift) + ((token0 + 16 * mt) & ((1 << a.shift) - 1))) * a.dim;
-          src[0][mt] = a.k + off;
-          src[1][mt] = a.v + off;
-          if (rg == 0 && lane < 2) {
-            float* m = meta_scale + slot * S::kMT * 3 + lane * S::kMT + mt;
-            copy4(smem_addr(m), (lane ? a.v_scale : a.k_scale) + bh, ok[mt]);
-            if (lane == 0) reinterpret_cast<int*>(m)[2 * S::kMT] = ok[mt];
+          full &= ok[mt];
+          off[mt] = int64_t(max(id, 0)) * block_size_all + head_at + ((in_token + 16 * mt) & ((1 << a.shift) - 1)) * a.dim;
+        }
+        if (rg == 0) {
+          const int id = __shfl_sync(~0u, ids, in_id + lane % S::kMT);
+          if (lane < 2 * S::kMT) {
+            float* m = meta_scale + in_slot * S::kMT * 3 + lane;
+            copy4(smem_addr(m), (lane < S::kMT ? a.k_scale : a.v_scale) + int64_t(max(id, 0)) * a.kv_heads + head, id >= 0);
+            if (lane < S::kMT) reinterpret_cast<int*>(m)[2 * S::kMT] = id >= 0;
           }
         }
+        if (full) {
+          // every chunk of every row: a lane's offsets are constants but for kSwizzles of them
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          if ((i & (rgs - 1)) != rg) continue;
-          constexpr int kHalf = kCopies / 2;
-          const int row = (i % kHalf) * kRowsPerCopy + my_row;      // within the tile
-          constexpr int kPerMT = kHalf / S::kMT;
-          const int mt = (i % kHalf) / kPerMT;
-          if (my_chunk * 16 < a.dim)
-            copy16(dst + uint32_t((i / kHalf) * S::kTile * kDP + row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
-                   src[i / kHalf][mt] + (row % 16) * a.dim + my_chunk * 16, ok[mt] && token0 + row < len);
+          for (int j = 0; j < kCopies / kRG; ++j) {
+            const int jj = j * kRG % kHalf;                            // + rg: the copy's place in its half
+            const bool second = kRG > kPerMT ? rg >= kPerMT : jj >= kPerMT;
+            copy16(dst + uint32_t((j * kRG / kHalf) * S::kTile * kDP + jj * kRowsPerCopy * kDP) +
+                       lane_dst[jj / kRG % kSwizzles],
+                   (j * kRG / kHalf ? a.v : a.k) + (second ? off[S::kMT - 1] : off[0]) + lane_src +
+                       (jj % kPerMT) * kRowsPerCopy * kDP);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCopies / kRG; ++j) {
+            const int jj = j * kRG % kHalf + rg, row = jj * kRowsPerCopy + my_row;
+            const bool second = jj >= kPerMT;
+            if (my_chunk * 16 < a.dim)
+              copy16(dst + uint32_t((j * kRG / kHalf) * S::kTile * kDP + row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
+                     (j * kRG / kHalf ? a.v : a.k) + (second ? off[S::kMT - 1] : off[0]) + (row % 16) * a.dim +
+                         my_chunk * 16,
+                     (second ? ok[S::kMT - 1] : ok[0]) && in_token + row < len);
+          }
         }
+        ++in_k;
+        in_id += S::kMT;
+        in_token += teams * S::kTile;
+        in_slot = in_slot + 1 == depth ? 0 : in_slot + 1;
       }
       copies_commit();
     };
-    for (int k = 0; k < depth - 1; ++k) issue(k);
+    for (int k = 0; k < depth - 1; ++k) issue();
 
     // ---- query fragments: lane (g, t) holds the 16-element chunks t + 4 h of row g of each row tile
-    uint32_t qreg[S::kQReg ? kNT : 1][S::kQReg ? S::kSteps : 1][S::kParts][2];
+    constexpr int kQ4 = S::kSteps * S::kParts / 2;             // 16-byte pieces of a row tile's fragments per lane
+    uint32_t qreg[S::kQReg ? kNT : 1][S::kQReg ? S::kSteps * S::kParts * 2 : 1];
     float factor[kNT][2];
     int see[kNT][2];                     // last visible position of columns 2t, 2t + 1
     {
-      uint2* const qs = reinterpret_cast<uint2*>(smem + ring_bytes) + rg * kNT * S::kSteps * S::kParts * 32;
+      uint4* const qs = reinterpret_cast<uint4*>(smem + ring_bytes) + rg * kNT * kQ4 * 32;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         const int row = rg * S::kWarpRows + nt * 8 + g;
@@ -391,14 +462,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         const int64_t gr = r0 + row;
         const int token = req.first + int(gr / a.group), qh = head * a.group + int(gr % a.group);
         const T* q = static_cast<const T*>(a.q) + (ok ? token * a.q_stride + int64_t(qh) * a.dim : 0);
-        float top = 0.0f;
         float x[S::kSteps][4];
 #pragma unroll
         for (int h = 0; h < kDP / 64; ++h) {
           const int d = (t + 4 * h) * 16;
+          if (ok && d < a.dim && a.q_vector) {
+            float y[8];
+            load8(q + d, y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[h * 4 + e / 4][e % 4] = ok && d < a.dim ? load1(q + d + e) : 0.0f;
+            for (int e = 0; e < 8; ++e) x[h * 4 + e / 4][e % 4] = y[e];
+            load8(q + d + 8, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[h * 4 + 2 + e / 4][e % 4] = y[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[h * 4 + e / 4][e % 4] = ok && d < a.dim ? load1(q + d + e) : 0.0f;
+          }
         }
+        float top = 0.0f;
 #pragma unroll
         for (int s = 0; s < S::kSteps; ++s)
 #pragma unroll
@@ -411,24 +492,26 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         const float down = __uint_as_float(uint32_t(254 - up_exp) << 23) * a.scale;
         factor[nt][0] = __shfl_sync(~0u, down, 8 * t);
         factor[nt][1] = __shfl_sync(~0u, down, 8 * t + 4);
+        uint32_t f[S::kSteps * S::kParts * 2];                 // per step: two words, with kSplit the two rests
 #pragma unroll
         for (int s = 0; s < S::kSteps; ++s) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[s][e] *= up;
-          uint32_t f[S::kParts][2] = {{pack_f16(x[s][0], x[s][1]), pack_f16(x[s][2], x[s][3])}};
+          uint32_t* const fs = f + s * S::kParts * 2;
+          fs[0] = pack_f16(x[s][0], x[s][1]);
+          fs[1] = pack_f16(x[s][2], x[s][3]);
           if (kSplit) {
-            f[S::kParts - 1][0] = rest_f16(f[0][0], x[s][0], x[s][1]);
-            f[S::kParts - 1][1] = rest_f16(f[0][1], x[s][2], x[s][3]);
+            fs[S::kParts * 2 - 2] = rest_f16(fs[0], x[s][0], x[s][1]);
+            fs[S::kParts * 2 - 1] = rest_f16(fs[1], x[s][2], x[s][3]);
           }
+        }
+        if (S::kQReg) {
 #pragma unroll
-          for (int p = 0; p < S::kParts; ++p) {
-            if (S::kQReg) {
-              qreg[S::kQReg ? nt : 0][S::kQReg ? s : 0][p][0] = f[p][0];
-              qreg[S::kQReg ? nt : 0][S::kQReg ? s : 0][p][1] = f[p][1];
-            } else if (team == 0) {
-              qs[((nt * S::kSteps + s) * S::kParts + p) * 32 + lane] = make_uint2(f[p][0], f[p][1]);
-            }
-          }
+          for (int i = 0; i < S::kSteps * S::kParts * 2; ++i) qreg[S::kQReg ? nt : 0][S::kQReg ? i : 0] = f[i];
+        } else if (team == 0) {
+#pragma unroll
+          for (int i = 0; i < kQ4; ++i)
+            qs[(nt * kQ4 + i) * 32 + lane] = make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -438,28 +521,32 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
       }
     }
     if (!S::kQReg) __syncthreads();
-    const uint32_t q_at = smem_addr(smem + ring_bytes) + uint32_t(rg * kNT * S::kSteps * S::kParts * 32 + lane) * 8;
+    const uint32_t q_at = smem_addr(smem + ring_bytes) + uint32_t(rg * kNT * kQ4 * 32 + lane) * 16;
 
     float o[kNT][S::kDT][4];
-    float m[kNT][2], l[kNT][2], v_ref = 0.0f;
+    float l[kNT][2], m[kNT][2], u[kNT][2];
+    uint32_t set_m = 0;                          // rows (2 nt + c) whose reference is set; m = 0, u = 1 before
+    constexpr uint32_t kAllSet = (1u << (2 * kNT)) - 1;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[nt][c] = -INFINITY, l[nt][c] = 0.0f;
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = 0.0f, u[nt][c] = 1.0f, l[nt][c] = 0.0f;
+        if (rg * S::kWarpRows + nt * 8 + 2 * t + c >= live_rows) set_m |= 1u << (2 * nt + c);   // unused: never awaited
+      }
 #pragma unroll
       for (int d = 0; d < S::kDT; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.0f;
     }
 
+    uint32_t set_u = set_m;
+    int slot = 0, token0 = (tile_lo + team) * S::kTile;
     for (int k = 0; k < iters; ++k) {
-      if (rgs == 1) copies_wait<S::depth(1) - 2>();
-      else if (rgs == 2) copies_wait<S::depth(2) - 2>();
-      else copies_wait<S::depth(4) - 2>();
-      if (rgs == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(rgs * 32) : "memory");
-      issue(k + depth - 1);
-      const int slot = k % depth, token0 = (tile_lo + team + k * teams) * S::kTile;
+      copies_wait<depth - 2>();
+      if (kRG == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kRG * 32) : "memory");
+      issue();
       const uint32_t kst = ring + uint32_t(slot) * S::kStage, vst = kst + S::kTile * kDP;
       const float* sc = meta_scale + slot * S::kMT * 3;
 
@@ -473,7 +560,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
           for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
 #pragma unroll
       for (int h = 0; h < kDP / 64; ++h) {
-        uint4 w[S::kMT][2];
+        uint4 w[S::kMT][2], q_two[kNT];
 #pragma unroll
         for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
@@ -488,36 +575,38 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
             unpack4<kType>(reinterpret_cast<const uint32_t*>(&w[mt][1])[i], f[mt][1], f[mt][3]);
           }
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+          for (int nt = 0; nt < kNT; ++nt) {
+            uint32_t q[S::kParts * 2];
+            if (S::kQReg) {
 #pragma unroll
-            for (int p = 0; p < S::kParts; ++p) {
-              uint32_t b0, b1;
-              if (S::kQReg) {
-                b0 = qreg[S::kQReg ? nt : 0][S::kQReg ? h * 4 + i : 0][p][0];
-                b1 = qreg[S::kQReg ? nt : 0][S::kQReg ? h * 4 + i : 0][p][1];
-              } else {
-                const uint2 q2 = lds64(q_at + uint32_t((nt * S::kSteps + h * 4 + i) * S::kParts + p) * 256);
-                b0 = q2.x, b1 = q2.y;
-              }
-#pragma unroll
-              for (int mt = 0; mt < S::kMT; ++mt) mma_f16(s[mt][nt], f[mt], b0, b1);
+              for (int p = 0; p < S::kParts * 2; ++p)
+                q[p] = qreg[S::kQReg ? nt : 0][S::kQReg ? (h * 4 + i) * S::kParts * 2 + p : 0];
+            } else if (kSplit) {
+              const uint4 x = lds128(q_at + uint32_t(nt * kQ4 + h * 4 + i) * 512);
+              q[0] = x.x, q[1] = x.y, q[S::kParts * 2 - 2] = x.z, q[S::kParts * 2 - 1] = x.w;
+            } else {
+              if (i % 2 == 0) q_two[nt] = lds128(q_at + uint32_t(nt * kQ4 + (h * 4 + i) / 2) * 512);
+              q[0] = i % 2 ? q_two[nt].z : q_two[nt].x, q[1] = i % 2 ? q_two[nt].w : q_two[nt].y;
             }
+#pragma unroll
+            for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+              for (int mt = 0; mt < S::kMT; ++mt) mma_f16(s[mt][nt], f[mt], q[2 * p], q[2 * p + 1]);
+          }
         }
       }
 
-      // ---- scale, mask, raise the references
-      float v_scale[S::kMT], v_top = 0.0f;
+      // ---- exponents: s = S c - m, masked; m raised where one passes the limit
       bool edge = token0 + S::kTile - 1 > p_first || (a.window > 0 && token0 <= p_last - a.window);
 #pragma unroll
       for (int mt = 0; mt < S::kMT; ++mt) {
-        const float ks = sc[mt];
-        v_scale[mt] = sc[S::kMT + mt];
-        v_top = fmaxf(v_top, v_scale[mt]);
         edge |= !reinterpret_cast<const int*>(sc)[2 * S::kMT + mt];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          const float c0 = ks * factor[nt][0], c1 = ks * factor[nt][1];
-          s[mt][nt][0] *= c0, s[mt][nt][1] *= c1, s[mt][nt][2] *= c0, s[mt][nt][3] *= c1;
+          const uint64_t c = mul2(pair(sc[mt], sc[mt]), pair(factor[nt][0], factor[nt][1]));
+          const uint64_t less = pair(-m[nt][0], -m[nt][1]);
+          unpair(fma2(pair(s[mt][nt][0], s[mt][nt][1]), c, less), s[mt][nt][0], s[mt][nt][1]);
+          unpair(fma2(pair(s[mt][nt][2], s[mt][nt][3]), c, less), s[mt][nt][2], s[mt][nt][3]);
         }
       }
       auto visible = [&](int mt, int nt, int e) {
@@ -533,19 +622,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
             for (int e = 0; e < 4; ++e)
               if (!visible(mt, nt, e)) s[mt][nt][e] = -INFINITY;
       }
-      bool raise = v_top > kVRaise * v_ref;
+      float largest = s[0][0][0];
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int mt = 1; mt < S::kMT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]));
-          raise |= x > m[nt][c] + kRaise;
-        }
-      if (__any_sync(~0u, raise)) {
-        const float v_new = fmaxf(v_ref, v_top), beta = v_new > 0.0f ? v_ref / v_new : 1.0f;
-        v_ref = v_new;
+          for (int c = 0; c < 2; ++c) largest = max3(largest, s[mt][nt][c], s[mt][nt][c + 2]);
+      if (__any_sync(~0u, largest > kRaise || set_m != kAllSet)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
           float alpha[2];
@@ -556,11 +640,17 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
             for (int mt = 1; mt < S::kMT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-            const float top = fmaxf(m[nt][c], x);
-            alpha[c] = m[nt][c] == -INFINITY ? 0.0f : exp2_approx(m[nt][c] - top);
-            m[nt][c] = top;
-            l[nt][c] *= alpha[c];
-            alpha[c] *= beta;
+            const uint32_t bit = 1u << (2 * nt + c);
+            alpha[c] = 1.0f;
+            if ((set_m & bit) ? x > kShift : x > -INFINITY) {
+              const float up = x - kShift;
+              if (set_m & bit) alpha[c] = exp2_approx(-up);
+              set_m |= bit;
+              m[nt][c] += up;
+              l[nt][c] *= alpha[c];
+#pragma unroll
+              for (int mt = 0; mt < S::kMT; ++mt) s[mt][nt][c] -= up, s[mt][nt][c + 2] -= up;
+            }
           }
 #pragma unroll
           for (int d = 0; d < S::kDT; ++d) {
@@ -569,29 +659,76 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         }
       }
 
-      // ---- P, transposed into the right operand of V^T P^T
-      uint32_t pf[S::kMT][kNT][S::kParts][2];
+      // ---- weights P v u as 16-bit floats; u lowered where one passes the limit
+      float v_scale[S::kMT];
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt) {
-        const float rel = v_ref > 0.0f ? v_scale[mt] / v_ref : 0.0f;
+      for (int mt = 0; mt < S::kMT; ++mt) v_scale[mt] = fminf(sc[S::kMT + mt], 0x1p66f);
+      uint32_t pf[S::kMT][kNT][S::kParts][2];
+      uint32_t packed_max = 0;
+      auto weigh = [&]() {
+#pragma unroll
+        for (int mt = 0; mt < S::kMT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            const uint64_t vu = mul2(pair(v_scale[mt], v_scale[mt]), pair(u[nt][0], u[nt][1]));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float p0, p1;
+              unpair(mul2(pair(s[mt][nt][half * 2], s[mt][nt][half * 2 + 1]), vu), p0, p1);
+              pf[mt][nt][0][half] = pack_f16(p0, p1);
+              if (kSplit) pf[mt][nt][S::kParts - 1][half] = rest_f16(pf[mt][nt][0][half], p0, p1);
+              packed_max = max_f16x2(packed_max, pf[mt][nt][0][half]);
+            }
+          }
+      };
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        uint64_t sum = pair(l[nt][0], l[nt][1]);
+#pragma unroll
+        for (int mt = 0; mt < S::kMT; ++mt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = exp2_approx(s[mt][nt][e]);
+          sum = add2(sum, add2(pair(s[mt][nt][0], s[mt][nt][1]), pair(s[mt][nt][2], s[mt][nt][3])));
+        }
+        unpair(sum, l[nt][0], l[nt][1]);
+      }
+      weigh();
+      if (__any_sync(~0u, (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || set_u != kAllSet)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          float p[4];
+          float beta[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float ref = m[nt][e % 2] == -INFINITY ? 0.0f : m[nt][e % 2] - kShift;
-            p[e] = exp2_approx(s[mt][nt][e] - ref);
-            l[nt][e % 2] += p[e];
-            p[e] *= rel;
+          for (int c = 0; c < 2; ++c) {
+            float x = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < S::kMT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) * v_scale[mt]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+            const uint32_t bit = 1u << (2 * nt + c);
+            beta[c] = 1.0f;
+            const int exp = min(kWeightExp + 127 - int(__float_as_uint(x) >> 23), kMaxUExp);
+            const float lower = __uint_as_float(uint32_t(max(exp, -126) + 127) << 23);
+            if (x > 0.0f && (!(set_u & bit) || lower < u[nt][c])) {
+              if (set_u & bit) beta[c] = lower / u[nt][c];
+              u[nt][c] = lower;
+              set_u |= bit;
+            }
           }
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t hi = pack_f16(p[half * 2], p[half * 2 + 1]);
-            pf[mt][nt][0][half] = transpose8(hi);
-            if (kSplit) pf[mt][nt][S::kParts - 1][half] = transpose8(rest_f16(hi, p[half * 2], p[half * 2 + 1]));
+          for (int d = 0; d < S::kDT; ++d) {
+            o[nt][d][0] *= beta[0], o[nt][d][1] *= beta[1], o[nt][d][2] *= beta[0], o[nt][d][3] *= beta[1];
           }
         }
+        weigh();
       }
+#pragma unroll
+      for (int mt = 0; mt < S::kMT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) pf[mt][nt][p][half] = transpose8(pf[mt][nt][p][half]);
 
       // ---- O^T += V^T P^T: lane (g, t) reads elements of tokens 2t, 2t+1, 2t+8, 2t+9; row g of tile d is element
       // 16 g + 2 d (8 g + 2 d of 64), row g + 8 the next one
@@ -681,6 +818,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
                 for (int p = 0; p < S::kParts; ++p) mma_f16(o[nt][d], f, pf[mt][nt][p][0], pf[mt][nt][p][1]);
             }
         }
+      slot = slot + 1 == depth ? 0 : slot + 1;
+      token0 += teams * S::kTile;
     }
     copies_wait<0>();
 
@@ -692,22 +831,24 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], d);
         if (g == 0) {
-          row_m[warp * S::kWarpRows + nt * 8 + 2 * t + c] = m[nt][c];
+          row_m[warp * S::kWarpRows + nt * 8 + 2 * t + c] = set_m >> (2 * nt + c) & 1 ? m[nt][c] : -INFINITY;
           row_l[warp * S::kWarpRows + nt * 8 + 2 * t + c] = l[nt][c];
         }
       }
     __syncthreads();                              // every team is done with the ring
     float* const join = reinterpret_cast<float*>(smem) + warp * S::kWarpRows * S::kOPitch;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
+    for (int nt = 0; nt < kNT; ++nt) {
+      const float back[2] = {1.0f / u[nt][0], 1.0f / u[nt][1]};
 #pragma unroll
       for (int d = 0; d < S::kDT; ++d)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int e = kDP == 64 ? 8 * g + 2 * d : (d / 8) * 128 + 16 * g + 2 * (d % 8);
           *reinterpret_cast<float2*>(join + (nt * 8 + 2 * t + c) * S::kOPitch + e) =
-              make_float2(o[nt][d][c] * v_ref, o[nt][d][c + 2] * v_ref);
+              make_float2(o[nt][d][c] * back[c], o[nt][d][c + 2] * back[c]);
         }
+    }
     // each warp's weight in its row, and the rows' joined (m, l) in the first team's place
     for (int r = tid; r < rows; r += kAttnThreads) {
       float top = -INFINITY, all = 0.0f;
@@ -742,8 +883,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
                  (int64_t(head) * a.group + gr % a.group) * a.dim;
         const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
         if (d < a.dim) {
+          if (a.out_vector) {
+            store4(out + d, y);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) store1(out + d + e, y[e]);
+            for (int e = 0; e < 4; ++e) store1(out + d + e, y[e]);
+          }
         }
       } else {
         *reinterpret_cast<float4*>(part + r * kDP + d) = x;
@@ -756,7 +901,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
       } else if (a.lse) {
         const int64_t gr = r0 + r;
         a.lse[(req.first + gr / a.group) * a.q_heads + int64_t(head) * a.group + gr % a.group] =
-            row_l[r] == 0.0f ? -INFINITY : (row_m[r] - kShift + log2f(row_l[r])) * 0.6931471805599453f;
+            row_l[r] == 0.0f ? -INFINITY : (row_m[r] + log2f(row_l[r])) * 0.6931471805599453f;
       }
     }
     if (!whole && pos == 0 && tid == 0)
@@ -839,28 +984,21 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, c
     for (int e = 0; e < kPer; ++e) store1(out + e, x[e] * inv);
   }
   if (lane == 0 && a.lse)
-    a.lse[token * a.q_heads + qh] = all == 0.0f ? -INFINITY : (top - kShift + log2f(all)) * 0.6931471805599453f;
+    a.lse[token * a.q_heads + qh] = all == 0.0f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- launch
 
 constexpr int kAttnCtasPerSm = 2;
 
-// Row tiles of 8 per warp and warps per team for `rows` rows per key head.
-struct AttnRows {
-  int nt, rg;
-};
-
-template <int kDP, int kNT, int kType, bool kSplit>
-cudaError_t attn_launch_shape(AttnArgs a, int row_groups, int dev, cudaStream_t st) {
-  using S = AttnShape<kDP, kNT, kSplit>;
-  a.row_groups = row_groups;
+template <int kDP, int kNT, int kRG, int kType, bool kSplit>
+cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
+  using S = AttnShape<kDP, kNT, kRG, kSplit>;
   LaunchShape ls;
-  ls.smem = size_t(S::smem(row_groups));
+  ls.smem = size_t(S::kSmem);
   // one wave: as many CTAs as fit at once (228 KB of shared memory per SM, 1 KB of it reserved per CTA)
-  const int grid = device_sms(dev) * (2 * (ls.smem + 1024) <= 228 * 1024 ? kAttnCtasPerSm : 1);
-  const void* kernel = reinterpret_cast<const void*>(&attention_kernel<kDP, kNT, kType, kSplit>);
-  cudaError_t err = prepare_kernel(kernel, dev, ls);
+  const int grid = device_sms(dev) * (2 * (S::kSmem + 1280) <= 228 * 1024 ? kAttnCtasPerSm : 1);
+  cudaError_t err = prepare_kernel(reinterpret_cast<const void*>(&attention_kernel<kDP, kNT, kRG, kType, kSplit>), dev, ls);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
@@ -872,49 +1010,44 @@ cudaError_t attn_launch_shape(AttnArgs a, int row_groups, int dev, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kNT, kType, kSplit>, a, S::ring_bytes(row_groups),
-                           S::query_bytes(row_groups));
+  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kNT, kRG, kType, kSplit>, a);
   if (err != cudaSuccess) return err;
-  const int rows = S::kWarpRows * row_groups;
-  cfg.gridDim = dim3(unsigned(grid), unsigned(rows / 8));
+  cfg.gridDim = dim3(unsigned(grid), unsigned(S::kRows / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, rows);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, S::kRows);
 }
 
+// The smallest row tile that holds `rows` rows of a key head: more row tiles
+// of 8 per warp while the registers hold their sums (they share the codes'
+// conversion), then more warps per team.
 template <int kType, bool kSplit, int kDP>
-cudaError_t attn_launch_dim(const AttnArgs& a, AttnRows r, int dev, cudaStream_t st) {
-  if (r.nt == 1) return attn_launch_shape<kDP, 1, kType, kSplit>(a, r.rg, dev, st);
+cudaError_t attn_launch_dim(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {
+  if (rows <= 8) return attn_launch_shape<kDP, 1, 1, kType, kSplit>(a, dev, st);
+  if (rows <= 16) return attn_launch_shape<kDP, 2, 1, kType, kSplit>(a, dev, st);
   if constexpr (kSplit || kDP == 256) {
-    return attn_launch_shape<kDP, 2, kType, kSplit>(a, r.rg, dev, st);
+    if (rows <= 32) return attn_launch_shape<kDP, 2, 2, kType, kSplit>(a, dev, st);
+    return attn_launch_shape<kDP, 2, 4, kType, kSplit>(a, dev, st);
   } else {
-    if (r.nt == 2) return attn_launch_shape<kDP, 2, kType, kSplit>(a, r.rg, dev, st);
-    if (r.nt == 3) return attn_launch_shape<kDP, 3, kType, kSplit>(a, r.rg, dev, st);
-    return attn_launch_shape<kDP, 4, kType, kSplit>(a, r.rg, dev, st);
+    if (rows <= 24) return attn_launch_shape<kDP, 3, 1, kType, kSplit>(a, dev, st);
+    if (rows <= 32) return attn_launch_shape<kDP, 4, 1, kType, kSplit>(a, dev, st);
+    if (rows <= 48) return attn_launch_shape<kDP, 3, 2, kType, kSplit>(a, dev, st);
+    if (rows <= 64) return attn_launch_shape<kDP, 4, 2, kType, kSplit>(a, dev, st);
+    if (rows <= 96) return attn_launch_shape<kDP, 3, 4, kType, kSplit>(a, dev, st);
+    return attn_launch_shape<kDP, 4, 4, kType, kSplit>(a, dev, st);
   }
-}
-
-// The smallest row tile that holds `rows` rows: more row tiles per warp while
-// the registers hold their sums, then more warps per team.
-inline AttnRows attn_rows(int64_t rows, bool narrow) {
-  const int most = narrow ? 2 : 4;
-  for (int rg = 1; rg <= 4; rg *= 2)
-    for (int nt = rg == 1 ? 1 : most / 2 + 1; nt <= most; ++nt)
-      if (rows <= 8 * nt * rg) return {nt, rg};
-  return {most, 4};
 }
 
 // One translation unit per cache and query type defines its own.
 template <int kType, bool kSplit>
 cudaError_t attn_launch(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st);
 
-#define SMP_ATTENTION_INSTANCE(TYPE, SPLIT)                                                                \
-  template <>                                                                                              \
-  cudaError_t attn_launch<TYPE, SPLIT>(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {       \
-    const AttnRows r = attn_rows(rows, SPLIT || a.dim > 128);                                              \
-    if (a.dim <= 64) return attn_launch_dim<TYPE, SPLIT, 64>(a, r, dev, st);                              \
-    if (a.dim <= 128) return attn_launch_dim<TYPE, SPLIT, 128>(a, r, dev, st);                            \
-    return attn_launch_dim<TYPE, SPLIT, 256>(a, r, dev, st);                                              \
+#define SMP_ATTENTION_INSTANCE(TYPE, SPLIT)                                                          \
+  template <>                                                                                        \
+  cudaError_t attn_launch<TYPE, SPLIT>(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {  \
+    if (a.dim <= 64) return attn_launch_dim<TYPE, SPLIT, 64>(a, rows, dev, st);                      \
+    if (a.dim <= 128) return attn_launch_dim<TYPE, SPLIT, 128>(a, rows, dev, st);                    \
+    return attn_launch_dim<TYPE, SPLIT, 256>(a, rows, dev, st);                                      \
   }
 
 template <>
