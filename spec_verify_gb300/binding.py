@@ -40,6 +40,7 @@ STATIC_VERIFY_SCRATCH_BYTES = 1 << 20
 VERIFY_LAUNCHES = 2
 
 _lib = None
+_step = None
 
 
 class SmpError(RuntimeError):
@@ -111,6 +112,27 @@ def load():
     lib.smp_abi_version.restype = i32
     _lib = lib
     return lib
+
+
+def step_module():
+    """The native marshalling of the cached step (csrc/step_binding.cpp)."""
+    global _step
+    if _step is None:
+        import importlib.machinery
+        import importlib.util
+
+        _torch()                       # its libraries are the extension's
+        load()
+        path = _build.STEP_LIB
+        if not os.path.exists(path):
+            raise SmpError(f"smp_step_binding.so is not built ({path}); run "
+                           "`python -m spec_verify_gb300.build` or __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("smp_step_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("smp_step_binding", loader))
+        loader.exec_module(module)
+        module.set_error(SmpError)
+        _step = module
+    return _step
 
 
 def _check(code):
@@ -428,30 +450,11 @@ def spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens=None, out_acc
     draft_lens: int32 [B], the drafts each row really has, or None for K.
     status: an int32 [1] tensor for the SMP_ROW_* flags, or None (no status
     word).  Returns (accepted_len int32 [B], ids int32 [B, K+1])."""
-    torch = _torch()
-    lib = load()
-    if p.dim() != 3 or noise.dim() != 2 or draft_ids.dim() != 2:
-        raise SmpError("expected p [B, K+1, V], draft_ids [B, K], noise [B, V]")
-    batch, k1, vocab = p.shape
-    k = k1 - 1
-    if (q is not None and (q.shape != (batch, k, vocab) or q.dtype != p.dtype)) or noise.shape != (batch, vocab) or \
-            draft_ids.shape != (batch, k) or uniforms.shape != (batch, k):
-        raise SmpError("shape mismatch between p, q, draft_ids, uniforms and noise")
-    if draft_ids.dtype != torch.int32 or uniforms.dtype != torch.float32 or noise.dtype != torch.float32:
-        raise SmpError("draft_ids must be int32, uniforms and noise float32")
-    if draft_lens is not None and (draft_lens.shape != (batch,) or draft_lens.dtype != torch.int32):
-        raise SmpError("draft_lens must be an int32 [B] CUDA tensor")
+    native = step_module()
     if out_accepted is None:
-        out_accepted = torch.empty(batch, dtype=torch.int32, device=p.device)
+        out_accepted = _torch().empty(p.shape[0], dtype=_torch().int32, device=p.device)
     if out_ids is None:
-        out_ids = torch.empty(batch, k1, dtype=torch.int32, device=p.device)
-    if out_accepted.shape != (batch,) or out_ids.shape != (batch, k1) or out_accepted.dtype != torch.int32 or \
-            out_ids.dtype != torch.int32:
-        raise SmpError("out_accepted must be int32 [B] and out_ids int32 [B, K+1]")
-    for t in (p, q, draft_ids, uniforms, noise, draft_lens, out_accepted, out_ids, status):
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise SmpError("expected contiguous CUDA tensors")
-    _check(lib.smp_spec_verify_probs(_ptr(p), _ptr(q), _ptr(draft_ids), _ptr(draft_lens), batch, k, vocab,
-                                     _dtype_code(p), _ptr(uniforms), _ptr(noise), _ptr(out_accepted), _ptr(out_ids),
-                                     _ptr(status), _stream(stream)))
+        out_ids = _torch().empty(p.shape[:2], dtype=_torch().int32, device=p.device)
+    native.spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens, out_accepted, out_ids, status,
+                             None if stream is None else stream.cuda_stream)
     return out_accepted, out_ids

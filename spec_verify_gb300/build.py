@@ -4,7 +4,9 @@
     python -m spec_verify_gb300.build --force  # from scratch
 
 Translation units compile in parallel; the library links the CUDA runtime
-statically, so it loads next to any PyTorch build.
+statically, so it loads next to any PyTorch build.  The native marshalling of
+the cached step (csrc/step_binding.cpp) is a separate extension module, built
+against the PyTorch that is installed.
 """
 
 import argparse
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libsmp.so")
+STEP_SOURCE = os.path.join(CSRC, "step_binding.cpp")
+STEP_LIB = os.path.join(BUILD, "smp_step_binding.so")
 
 SOURCES = ["api.cu", "sample.cu", "verify.cu", "prepass.cu", "beam.cu", "verify_probs.cu", "block_plan.cu",
            "norm_rope.cu", "cache_append.cu", "cache_attention.cu", "attention_e4m3_bf16.cu",
@@ -45,12 +50,13 @@ def nvcc():
 def _newest_input():
     paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
     paths += [os.path.join(INCLUDE, f) for f in ("smp.h", "smp_cache.h")]
-    paths.append(os.path.abspath(__file__))
+    paths += [os.path.abspath(__file__), STEP_SOURCE]
     return max(os.path.getmtime(p) for p in paths)
 
 
 def up_to_date():
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input()
+    newest = _newest_input()
+    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, STEP_LIB))
 
 
 def _compile(src, extra):
@@ -62,6 +68,34 @@ def _compile(src, extra):
     return obj, res.stderr
 
 
+def _compile_step():
+    """Object file of the extension module, against the installed PyTorch."""
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD, "step_binding.o")
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+    cmd = ["g++", "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-DTORCH_API_INCLUDE_EXTENSION_H",
+           *[f"-isystem{p}" if p != INCLUDE else f"-I{p}" for p in includes], "-c", STEP_SOURCE, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {STEP_SOURCE}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_step(obj):
+    from torch.utils import cpp_extension
+
+    tmp = STEP_LIB + ".tmp"
+    libs = [p for p in cpp_extension.library_paths() if os.path.isdir(p)]
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{BUILD}", "-lsmp", "-Wl,-rpath,$ORIGIN",
+           *[f"-L{p}" for p in libs], *[f"-Wl,-rpath,{p}" for p in libs],
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, STEP_LIB)
+
+
 def build(force=False, verbose=False, extra=()):
     """Compile every CUDA source and link libsmp.so; returns the library path."""
     if not force and up_to_date():
@@ -70,7 +104,8 @@ def build(force=False, verbose=False, extra=()):
     extra = list(extra)
     if verbose:
         extra += ["-Xptxas", "-v"]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        step = pool.submit(_compile_step)
         results = list(pool.map(lambda s: _compile(s, extra), SOURCES))
     if verbose:
         for (_, log), src in zip(results, SOURCES):
@@ -82,6 +117,7 @@ def build(force=False, verbose=False, extra=()):
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_step(step.result())
     return LIB
 
 

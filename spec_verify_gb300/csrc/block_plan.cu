@@ -43,6 +43,7 @@ struct PlanArgs {
   int32_t* out_position;
   int32_t* out_request;
   int64_t* out_slot;
+  bool vector;      // the per-token outputs take 16-byte stores
   int32_t* status;
 };
 
@@ -55,27 +56,29 @@ struct PlanRequest {
   int fresh;      // index into free_blocks of the request's first new block
 };
 
-// Sum over the threads before this one; `total` gets the sum over all.
-__device__ __forceinline__ uint64_t block_exclusive_u64(uint64_t v, uint64_t* scratch, uint64_t& total) {
+// Sums of x and y over the threads before this one; x_all and y_all get the
+// sums over all threads.
+__device__ __forceinline__ void block_exclusive2(uint64_t& x, uint64_t& y, uint64_t (*scratch)[2], uint64_t& x_all,
+                                                 uint64_t& y_all) {
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  const uint64_t inc = warp_inclusive_scan<uint64_t>(v);
-  cta_sync();
-  if (lane == 31) scratch[warp] = inc;
-  cta_sync();
-  uint64_t before = 0;
-  total = 0;
+  const uint64_t xi = warp_inclusive_scan<uint64_t>(x), yi = warp_inclusive_scan<uint64_t>(y);
+  __syncthreads();
+  if (lane == 31) scratch[warp][0] = xi, scratch[warp][1] = yi;
+  __syncthreads();
+  uint64_t xb = 0, yb = 0;
+  x_all = y_all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+    if (w < warp) xb += scratch[w][0], yb += scratch[w][1];
+    x_all += scratch[w][0], y_all += scratch[w][1];
   }
-  return before + inc - v;
+  x = xb + xi - x, y = yb + yi - y;
 }
 
 __global__ void __launch_bounds__(kThreads) block_plan_kernel(const PlanArgs a) {
   __shared__ PlanRequest req[kPlanTokens];   // at the local index of the request's first token here
   __shared__ int16_t mark[kPlanTokens];      // that index, or -1
-  __shared__ uint64_t scratch[kWarps];
+  __shared__ uint64_t scratch[kWarps][2];
   __shared__ int warp_last[kWarps];
   allow_dependent_launch();
   grid_dependency_wait();
@@ -109,19 +112,24 @@ __global__ void __launch_bounds__(kThreads) block_plan_kernel(const PlanArgs a) 
       want = valid ? add : 0;
       need = want ? need : 0;
     }
-    uint64_t chunk_tokens, chunk_blocks;
-    const int64_t before_t = tokens + int64_t(block_exclusive_u64(uint64_t(want), scratch, chunk_tokens));
-    const int64_t before_b = blocks + int64_t(block_exclusive_u64(uint64_t(need), scratch, chunk_blocks));
+    uint64_t chunk_tokens, chunk_blocks, t_before = uint64_t(want), b_before = uint64_t(need);
+    block_exclusive2(t_before, b_before, scratch, chunk_tokens, chunk_blocks);
+    const int64_t before_t = tokens + int64_t(t_before), before_b = blocks + int64_t(b_before);
     tokens += int64_t(chunk_tokens);
     blocks += int64_t(chunk_blocks);
     const bool fits = before_t + want <= a.max_tokens && before_b + need <= avail;
     const bool served = want > 0 && fits;
     if (want > 0 && !fits) flags |= kRowNoCapacity;
-    uint64_t got_tokens, got_blocks;
-    const int64_t start = served_tokens + int64_t(block_exclusive_u64(served ? uint64_t(want) : 0, scratch, got_tokens));
-    block_exclusive_u64(served ? uint64_t(need) : 0, scratch, got_blocks);
-    served_tokens += int64_t(got_tokens);
-    served_blocks += int64_t(got_blocks);
+    int64_t start = before_t;
+    if (tokens <= a.max_tokens && blocks <= avail) {           // all of them so far
+      served_tokens = tokens, served_blocks = blocks;
+    } else {
+      uint64_t got_tokens, got_blocks, t_served = served ? uint64_t(want) : 0, b_served = served ? uint64_t(need) : 0;
+      block_exclusive2(t_served, b_served, scratch, got_tokens, got_blocks);
+      start = served_tokens + int64_t(t_served);
+      served_tokens += int64_t(got_tokens);
+      served_blocks += int64_t(got_blocks);
+    }
     if (b < a.batch) {
       if ((base / kThreads) % int(gridDim.x) == int(blockIdx.x)) {
         a.out_lens[b] = served ? len + add : len;
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) block_plan_kernel(const PlanArgs a) 
     a.out_start[a.batch] = int(served_tokens);
     *a.out_head = int(head + served_blocks);
   }
-  cta_sync();
+  __syncthreads();
 
   // The running maximum of the marks is each token's request.
   int owner[kPlanTokensPerThread], run = -1;
@@ -157,28 +165,42 @@ __global__ void __launch_bounds__(kThreads) block_plan_kernel(const PlanArgs a) 
   if (lane == 31) warp_last[warp] = before;
   before = __shfl_up_sync(~0u, before, 1);
   if (lane == 0) before = -1;
-  cta_sync();
+  __syncthreads();
   for (int w = 0; w < warp; ++w) before = max(before, warp_last[w]);
 
+  int position[kPlanTokensPerThread], request[kPlanTokensPerThread];
+  int64_t slot[kPlanTokensPerThread];
+  const int64_t first = t0 + tid * kPlanTokensPerThread;
+#pragma unroll
   for (int i = 0; i < kPlanTokensPerThread; ++i) {
-    const int64_t t = t0 + tid * kPlanTokensPerThread + i;
-    if (t >= a.max_tokens) break;
-    int position = -1, request = -1;
-    int64_t slot = -1;
+    const int64_t t = first + i;
+    position[i] = request[i] = -1;
+    slot[i] = -1;
     if (t < served_tokens) {
       const PlanRequest& r = req[max(owner[i], before)];
-      position = r.len + int(t - r.first);
-      request = r.request;
-      const int block = position >> a.shift;
-      const int64_t entry = int64_t(request) * a.stride + block;
+      position[i] = r.len + int(t - r.first);
+      request[i] = r.request;
+      const int block = position[i] >> a.shift;
+      const int64_t entry = int64_t(request[i]) * a.stride + block;
       const int id = block < r.held ? a.table[entry] : a.free_blocks[r.fresh + block - r.held];
-      if (id >= 0 && id < a.num_blocks) slot = (int64_t(id) << a.shift) + (position & round);
+      if (id >= 0 && id < a.num_blocks) slot[i] = (int64_t(id) << a.shift) + (position[i] & round);
       else flags |= kRowBadBlock;
-      if (block >= r.held && (position & round) == 0) a.table[entry] = id;
+      if (block >= r.held && (position[i] & round) == 0) a.table[entry] = id;
     }
-    a.out_position[t] = position;
-    a.out_request[t] = request;
-    a.out_slot[t] = slot;
+  }
+  if (a.vector && first + kPlanTokensPerThread <= a.max_tokens) {
+    *reinterpret_cast<int4*>(a.out_position + first) = make_int4(position[0], position[1], position[2], position[3]);
+    *reinterpret_cast<int4*>(a.out_request + first) = make_int4(request[0], request[1], request[2], request[3]);
+    reinterpret_cast<longlong2*>(a.out_slot + first)[0] = make_longlong2(slot[0], slot[1]);
+    reinterpret_cast<longlong2*>(a.out_slot + first)[1] = make_longlong2(slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPlanTokensPerThread; ++i) {
+      if (first + i >= a.max_tokens) break;
+      a.out_position[first + i] = position[i];
+      a.out_request[first + i] = request[i];
+      a.out_slot[first + i] = slot[i];
+    }
   }
   if (flags && a.status) atomicOr(a.status, flags);
 }
@@ -221,6 +243,7 @@ extern "C" smp_status smp_block_plan(const int32_t* lens, const int32_t* add, co
   a.max_tokens = max_tokens;
   a.out_lens = out_lens, a.out_held = out_held, a.out_head = out_free_head, a.out_start = out_start;
   a.out_position = out_position, a.out_request = out_request, a.out_slot = out_slot;
+  a.vector = !misaligned(out_position, 16) && !misaligned(out_request, 16) && !misaligned(out_slot, 16);
   a.status = status;
   LaunchShape ls;
   ls.pdl = true;

@@ -9,8 +9,8 @@
 // Bound: HBM, two bytes read (bf16) and one written per element.  The work
 // item is a run (the step's tokens inside one block) of one head, of k or of
 // v: one CTA holds it in registers between the maximum and the encoding.
-// Runs are found from the slots themselves: a CTA looks at kSpan consecutive
-// tokens and handles the runs that begin there.
+// Runs are found from the slots themselves: a CTA looks at a span of up to 32
+// consecutive tokens, one per lane, and handles the runs that begin there.
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
@@ -19,14 +19,16 @@
 
 namespace smp {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
 constexpr int kMinScaleExp = -100;
 
 struct AppendArgs {
-  uint8_t* codes[2];
-  float* scale[2];
-  const void* x[2];
-  int64_t stride[2];
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  const void *new_k, *new_v;
+  int64_t k_stride, v_stride;
+  bool k_vector, v_vector;       // rows of k / v take 16-byte loads
+  int span;                      // tokens a CTA looks at, 1 .. 32
   int tokens, heads, dim, shift;
   int64_t slots_end;             // num_blocks << shift
   const int64_t* slots;
@@ -53,14 +55,15 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return uint32_t(lo) | uint32_t(hi) << 16;
   }
+  // adding 1.5 * 2^23 rounds to an integer whose low byte is the code
   const float v[4] = {a, b, c, d};
-  uint32_t w = 0;
+  uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int q = v[i] != v[i] ? 0 : __float2int_rn(fminf(fmaxf(v[i], -127.0f), 127.0f));
-    w |= uint32_t(q & 0xFF) << (8 * i);
+    const float x = v[i] != v[i] ? 0.0f : fminf(fmaxf(v[i], -127.0f), 127.0f);
+    q[i] = __float_as_uint(__fadd_rn(x, 12582912.0f));
   }
-  return w;
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
 template <int kType>
@@ -118,22 +121,33 @@ __device__ __forceinline__ void load_eight(const T* p, bool vector, float (&x)[8
 // run; longer runs are read again.
 constexpr int kKept = 4;
 
+// One tensor's side of the call: k or v.
+template <typename T>
+struct AppendSide {
+  uint8_t* codes;
+  float* scale;
+  const T* x;
+  int64_t stride;
+  bool vector;
+};
+
 template <typename T, int kType>
-__device__ __forceinline__ void append_run(const AppendArgs& a, int which, int head, int token, int count,
-                                           int64_t slot, bool vector, float* scratch, int& flags) {
+__device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide<T>& side, int head, int64_t token,
+                                           int count, int64_t slot, float* scratch, int& flags) {
   const int tid = int(threadIdx.x), per_row = a.dim / 8, vectors = count * per_row;
   const int64_t block = slot >> a.shift;
   const int offset = int(slot & ((1 << a.shift) - 1));
-  const T* x = static_cast<const T*>(a.x[which]) + int64_t(head) * a.dim;
-  const int64_t stride = a.stride[which];
-  uint8_t* codes = a.codes[which] + ((block * a.heads + head) << a.shift) * a.dim;
-  float* scale = a.scale[which] + block * a.heads + head;
+  uint8_t* codes = side.codes + ((block * a.heads + head) << a.shift) * a.dim;
+  float* scale = side.scale + block * a.heads + head;
   const float old = offset ? *scale : 0.0f;
 
+  // vector v = tid + i * kAppendThreads is piece v % per_row of row v / per_row
+  const int row0 = tid / per_row, piece0 = tid - row0 * per_row;
+  const int step_row = kAppendThreads / per_row, step_piece = kAppendThreads - step_row * per_row;
+  const T* x = side.x + token * side.stride + int64_t(head) * a.dim;
   float kept[kKept][8];
   float amax = 0.0f;
   bool odd = false;
-  auto row_of = [&](int v) { return x + (token + v / per_row) * stride + v % per_row * 8; };
   auto look = [&](const float (&y)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -142,17 +156,25 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int which, int h
       else odd = true;
     }
   };
+  int row = row0, piece = piece0;
+  auto advance = [&] {
+    row += step_row;
+    piece += step_piece;
+    if (piece >= per_row) piece -= per_row, ++row;
+  };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    const int v = tid + i * kAppendThreads;
-    if (v < vectors) load_eight(row_of(v), vector, kept[i]);
+    if (tid + i * kAppendThreads < vectors) load_eight(x + row * side.stride + piece * 8, side.vector, kept[i]);
+    advance();
   }
+  const int more_row = row, more_piece = piece;
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
     if (tid + i * kAppendThreads < vectors) look(kept[i]);
   for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
     float y[8];
-    load_eight(row_of(v), vector, y);
+    load_eight(x + row * side.stride + piece * 8, side.vector, y);
+    advance();
     look(y);
   }
   if (odd) flags |= kRowNonFinite;
@@ -183,55 +205,56 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, int which, int h
     const int v = tid + i * kAppendThreads;
     if (v < vectors) out[v] = encode8<kType>(kept[i], s, inverse);
   }
+  row = more_row, piece = more_piece;
   for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
     float y[8];
-    load_eight(row_of(v), vector, y);
+    load_eight(x + row * side.stride + piece * 8, side.vector, y);
+    advance();
     out[v] = encode8<kType>(y, s, inverse);
   }
 }
 
-// Grid: (spans of kSpan tokens, heads, k or v).
-template <typename T, int kType, int kSpan>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a, const bool vector_k,
-                                                                      const bool vector_v) {
+// Grid: (spans of tokens, heads, k or v).
+template <typename T, int kType>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
   __shared__ float scratch[kAppendThreads / 32];
   allow_dependent_launch();
   grid_dependency_wait();
-  const int which = int(blockIdx.z), head = int(blockIdx.y);
-  const int64_t first = int64_t(blockIdx.x) * kSpan;
-  const int last = int(first + kSpan < a.tokens ? first + kSpan : a.tokens);
-  int flags = 0;
-  auto usable = [&](int64_t s) { return s >= 0 && s < a.slots_end; };
+  const int head = int(blockIdx.y), lane = int(threadIdx.x) & 31;
+  const AppendSide<T> side =
+      blockIdx.z ? AppendSide<T>{a.v, a.v_scale, static_cast<const T*>(a.new_v), a.v_stride, a.v_vector}
+                 : AppendSide<T>{a.k, a.k_scale, static_cast<const T*>(a.new_k), a.k_stride, a.k_vector};
+  const int64_t first = int64_t(blockIdx.x) * a.span, mine = first + lane;
   const int64_t inside = (1 << a.shift) - 1;
-  for (int t = int(first); t < last; ++t) {
-    const int64_t slot = a.slots[t];
-    if (!usable(slot)) {
-      if (slot >= 0) flags |= kRowBadLength;
-      continue;
-    }
-    // a run goes on while the slots follow one another and the block does not end
-    if (t > 0 && (slot & inside) != 0 && a.slots[t - 1] == slot - 1) continue;
-    const int most = int(inside + 1 - (slot & inside));
+  int flags = 0;
+  // every warp looks at the whole span, a token per lane; a run goes on while
+  // the slots follow one another and the block does not end
+  int64_t slot = -1;
+  if (lane < a.span && mine < a.tokens) slot = a.slots[mine];
+  if (slot >= a.slots_end) slot = -1, flags |= kRowBadLength;
+  const bool follows = slot >= 0 && mine > 0 && (slot & inside) != 0 && a.slots[mine - 1] == slot - 1;
+  unsigned starts = __ballot_sync(~0u, slot >= 0 && !follows);
+  while (starts) {
+    const int at = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const int64_t run = __shfl_sync(~0u, slot, at);
+    const int most = int(inside + 1 - (run & inside));
     int count = 1;
-    for (bool more = true; more && count < most;) {     // 32 slots at a time, the same in every warp
-      const int i = count + (int(threadIdx.x) & 31);
-      const bool follows = i < most && t + int64_t(i) < a.tokens && a.slots[t + int64_t(i)] == slot + i;
-      const unsigned broken = ~__ballot_sync(~0u, follows);
+    for (bool more = true; more && count < most;) {
+      const int64_t i = first + at + count + lane;
+      const bool on = count + lane < most && i < a.tokens && a.slots[i] == run + count + lane;
+      const unsigned broken = ~__ballot_sync(~0u, on);
       more = broken == 0;
       count += more ? 32 : __ffs(broken) - 1;
     }
-    append_run<T, kType>(a, which, head, t, count, slot, which ? vector_v : vector_k, scratch, flags);
+    append_run<T, kType>(a, side, head, first + at, count, run, scratch, flags);
   }
   if (flags && a.status) atomicOr(a.status, flags);
 }
 
 template <typename T, int kType>
 static smp_status launch_append(const AppendArgs& a, cudaStream_t st) {
-  bool vector[2];
-  for (int w = 0; w < 2; ++w)
-    vector[w] = !misaligned(a.x[w], 16) && a.stride[w] * int64_t(sizeof(T)) % 16 == 0;
-  constexpr int kSpan = 4;
-  const int64_t spans = (int64_t(a.tokens) + kSpan - 1) / kSpan;
+  const int64_t spans = (int64_t(a.tokens) + a.span - 1) / a.span;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(spans), unsigned(a.heads), 2);
   cfg.blockDim = dim3(kAppendThreads);
@@ -241,7 +264,7 @@ static smp_status launch_append(const AppendArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, cache_append_kernel<T, kType, kSpan>, a, vector[0], vector[1]);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, cache_append_kernel<T, kType>, a);
   return err == cudaSuccess ? SMP_OK : fail_cuda(err);
 }
 
@@ -267,15 +290,22 @@ extern "C" smp_status smp_cache_append(const smp_cache* cache, const void* k, co
   }
   if (tokens == 0) return SMP_OK;
   AppendArgs a{};
-  a.codes[0] = static_cast<uint8_t*>(cache->k), a.codes[1] = static_cast<uint8_t*>(cache->v);
-  a.scale[0] = cache->k_scale, a.scale[1] = cache->v_scale;
-  a.x[0] = k, a.x[1] = v;
-  a.stride[0] = k_stride, a.stride[1] = v_stride;
+  a.k = static_cast<uint8_t*>(cache->k), a.v = static_cast<uint8_t*>(cache->v);
+  a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+  a.new_k = k, a.new_v = v;
+  a.k_stride = k_stride, a.v_stride = v_stride;
+  a.k_vector = !misaligned(k, 16) && k_stride * int64_t(elem) % 16 == 0;
+  a.v_vector = !misaligned(v, 16) && v_stride * int64_t(elem) % 16 == 0;
   a.tokens = tokens, a.heads = cache->kv_heads, a.dim = cache->head_dim;
   for (a.shift = 0; (1 << a.shift) < cache->block_size;) ++a.shift;
   a.slots_end = int64_t(cache->num_blocks) << a.shift;
   a.slots = slots;
   a.status = status;
+  // spans as long as leaves every SM some 16 CTAs: a CTA without a run start only costs its launch
+  const int dev = current_device();
+  if (dev < 0) return fail_cuda(cudaGetLastError());
+  const int64_t fill = int64_t(tokens) * a.heads * 2 / (int64_t(device_sms(dev)) * 16);
+  a.span = int(fill < 1 ? 1 : fill > 32 ? 32 : fill);
   const bool e4m3 = cache->type == SMP_CACHE_E4M3;
   if (dtype == SMP_F32)
     return e4m3 ? launch_append<float, SMP_CACHE_E4M3>(a, st) : launch_append<float, SMP_CACHE_I8>(a, st);

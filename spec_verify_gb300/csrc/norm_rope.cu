@@ -67,34 +67,29 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
   float w[8], c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 1.0f, c[i] = 1.0f, s[i] = 0.0f;
-  if (a.weight[which] && live) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = a.weight[which][l * 8 + i];
-  }
+  if (a.weight[which] && live) load8(a.weight[which] + l * 8, w);
   // Per element: y' = y c + partner s, with the sign of its side in s.
   const int half = a.rotary / 2;
   int partner = l;
   bool bad = position >= a.table_rows && a.rotary > 0;
   if (!bad && l * 8 < a.rotary) {
     const float* row = a.table + int64_t(position) * a.rotary;
-    if (a.interleaved) {
+    if (a.interleaved) {               // half is a multiple of 4: a lane rotates or not
+      const float4 cs = reinterpret_cast<const float4*>(row)[l], sn = reinterpret_cast<const float4*>(row + half)[l];
+      const float c4[4] = {cs.x, cs.y, cs.z, cs.w}, s4[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int j = l * 4 + i / 2;
-        if (j < half) {
-          c[i] = row[j];
-          s[i] = i % 2 ? row[half + j] : -row[half + j];
-        }
+        c[i] = c4[i / 2];
+        s[i] = i % 2 ? s4[i / 2] : -s4[i / 2];
       }
     } else {                           // half is a multiple of 8: a lane is on one side
       const bool upper = l * 8 >= half;
       const int j = l * 8 - (upper ? half : 0);
       partner = upper ? l - half / 8 : l + half / 8;
+      load8(row + j, c);
+      load8(row + half + j, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = row[j + i];
-        s[i] = upper ? row[half + j + i] : -row[half + j + i];
-      }
+      for (int i = 0; i < 8; ++i) s[i] = upper ? s[i] : -s[i];
     }
   }
 #pragma unroll
@@ -111,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float other = a.interleaved ? y[h][i ^ 1] : __shfl_sync(group, y[h][i], partner, kLanes);
-      z[i] = l * 8 + i < a.rotary ? fmaf(y[h][i], c[i], other * s[i]) : y[h][i];
+      z[i] = l * 8 < a.rotary ? fmaf(y[h][i], c[i], other * s[i]) : y[h][i];
     }
     if (live && h < heads) store8(out + h * a.dim, z);
   }
@@ -186,7 +181,8 @@ static cudaError_t launch_lanes(const NormRopeArgs& a, cudaStream_t st) {
 
 template <typename T>
 static smp_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t st) {
-  bool vector = a.dim % 8 == 0 && (a.interleaved || (a.rotary / 2) % 8 == 0);
+  bool vector = a.dim % 8 == 0 && a.rotary % (a.interleaved ? 8 : 16) == 0 && !misaligned(a.table, 16) &&
+                !misaligned(a.weight[0], 16) && !misaligned(a.weight[1], 16);
   for (int w = 0; w < 2 && vector; ++w) {
     if (a.heads[w] == 0) continue;
     vector = !misaligned(a.x[w], 16) && !misaligned(a.out[w], 16) && a.stride[w] * int64_t(sizeof(T)) % 16 == 0 &&
@@ -194,7 +190,12 @@ static smp_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t st) {
   }
   cudaError_t err;
   if (vector) {
-    err = launch_lanes<T, 1>(a, st);
+    // four heads per group share the table row and the weights, and keep 64 (bf16) or 128 bytes per lane in flight;
+    // one head per group while that leaves SMs short of warps (16384 tokens of 40 heads of 128: see below)
+    const int dev = current_device();
+    if (dev < 0) return fail_cuda(cudaGetLastError());
+    const int64_t warps = int64_t(a.tokens) * (a.heads[0] + a.heads[1]) * (a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32) / 32;
+    err = warps >= int64_t(device_sms(dev)) * 128 ? launch_lanes<T, 4>(a, st) : launch_lanes<T, 1>(a, st);
   } else {
     LaunchShape ls;
     ls.pdl = true;

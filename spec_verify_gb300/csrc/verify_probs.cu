@@ -34,32 +34,118 @@ struct ProbsArgs {
   int32_t* status;
 };
 
-// The larger quotient wins, the lower id among equals; 0 is no candidate.
-__device__ __forceinline__ void race(uint64_t& best, float p, float q, float e, uint32_t id) {
-  const float w = __fsub_rn(p, q);
-  if (w > 0.0f) {
+// The best candidate so far of one thread, whose ids ascend: a larger quotient
+// replaces it, an equal one does not.
+struct Best {
+  float score = 0.0f;   // 0 is no candidate
+  int id = 0;
+};
+
+// The exact quotient is only formed where w / e can reach the best score:
+// best * e is off by at most 2^-24, so a w below it by 2^-20 cannot (products
+// too small for that bound are not trusted).
+__device__ __forceinline__ void race(Best& best, float p, float q, float e, int id) {
+  const float w = __fsub_rn(p, q), reach = best.score * e;
+  if (w > 0.0f && !(w < reach * (1.0f - 0x1p-20f) && reach > 1e-30f)) {
     const float score = __fdiv_rn(w, e);
-    if (score > 0.0f) {
-      const uint64_t key = pack_key_id(__float_as_uint(score), id);
-      best = key > best ? key : best;
-    }
+    if (score > best.score) best.score = score, best.id = id;
   }
 }
 
-// The best candidate of elements [lo, hi) of one row; q may be nullptr, and
-// `certain` is the id where it then counts as 1 (or -1).
+// 16 bytes of elements.
 template <typename T>
-__device__ __forceinline__ uint64_t race_slice(const T* p, const T* q, const float* e, int lo, int hi, int certain) {
-  uint64_t best = 0;
-  for (int i = lo + int(threadIdx.x); i < hi; i += kThreads) {
-    const float qv = q ? load1(q + i) : (i == certain ? 1.0f : 0.0f);
-    race(best, load1(p + i), qv, e[i], uint32_t(i));
+struct Piece;
+template <>
+struct Piece<float> {
+  static constexpr int kN = 4;
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+};
+template <>
+struct Piece<uint16_t> {
+  static constexpr int kN = 8;
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return i & 1 ? bf16_high(w) : bf16_low(w);
+  }
+};
+
+// The noise of one batch of a thread's pieces.
+template <typename T>
+struct NoiseBatch {
+  static constexpr int kN = Piece<T>::kN, kBatch = kN == 4 ? 2 : 1;
+  Piece<float> v[kBatch][kN / 4];
+  __device__ __forceinline__ void load(const float* e, int i0, int hi) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (i0 + u * kThreads * kN < hi) {
+#pragma unroll
+        for (int h = 0; h < kN / 4; ++h) v[u][h].load(e + i0 + u * kThreads * kN + 4 * h);
+      }
+  }
+};
+
+// The best candidate of elements [lo, hi) of one row; q may be nullptr, and
+// `certain` is the id where it then counts as 1 (or -1).  16-byte loads, all of
+// a batch issued before the first is used, where every row's address allows
+// them (vector: lo and hi are then multiples of a piece); else one element per
+// load, as many in flight.
+// The first batch of noise, which does not depend on the row chosen, comes in
+// `ev` when `have_noise`.
+template <typename T, bool kQ>
+__device__ __forceinline__ Best race_slice(const T* p, const T* q, const float* e, int lo, int hi, int certain,
+                                           bool vector, NoiseBatch<T>& ev, bool have_noise) {
+  Best best;
+  constexpr int kN = Piece<T>::kN, kBatch = NoiseBatch<T>::kBatch;
+  if (vector) {
+    for (int i0 = lo + int(threadIdx.x) * kN; i0 < hi; i0 += kBatch * kThreads * kN) {
+      Piece<T> pv[kBatch], qv[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads * kN;
+        if (i < hi) {
+          pv[u].load(p + i);
+          if (kQ) qv[u].load(q + i);
+        }
+      }
+      if (!have_noise) ev.load(e, i0, hi);
+      have_noise = false;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kThreads * kN;
+        if (i < hi) {
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            race(best, pv[u].at(j), kQ ? qv[u].at(j) : (i + j == certain ? 1.0f : 0.0f), ev.v[u][j / 4].at(j % 4), i + j);
+        }
+      }
+    }
+  } else {
+    constexpr int kSingles = 4;
+    for (int i0 = lo + int(threadIdx.x); i0 < hi; i0 += kSingles * kThreads) {
+      float pv[kSingles], qv[kSingles], ev[kSingles];
+#pragma unroll
+      for (int u = 0; u < kSingles; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i < hi) {
+          pv[u] = load1(p + i);
+          qv[u] = kQ ? load1(q + i) : (i == certain ? 1.0f : 0.0f);
+          ev[u] = e[i];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSingles; ++u)
+        if (i0 + u * kThreads < hi) race(best, pv[u], qv[u], ev[u], i0 + u * kThreads);
+    }
   }
   return best;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_probs_kernel(const ProbsArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_probs_kernel(const ProbsArgs a) {
   __shared__ uint64_t scratch[kWarps];
   __shared__ uint64_t mail[2][16];
   allow_dependent_launch();
@@ -71,6 +157,11 @@ __global__ void __launch_bounds__(kThreads) verify_probs_kernel(const ProbsArgs 
   const T* p = static_cast<const T*>(a.p) + int64_t(b) * (a.k + 1) * v;
   const T* q = a.q ? static_cast<const T*>(a.q) + int64_t(b) * a.k * v : nullptr;
   const float* e = a.noise + int64_t(b) * v;
+
+  const int lo = min(rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
+  const bool noise_fits = reinterpret_cast<uintptr_t>(e) % 16 == 0 && a.vocab % Piece<T>::kN == 0;
+  NoiseBatch<T> noise;
+  if (noise_fits) noise.load(e, lo + int(threadIdx.x) * Piece<T>::kN, hi);
 
   const int drafts = a.lens ? a.lens[b] : a.k;
   bool bad = drafts < 0 || drafts > a.k, reject = false;
@@ -93,12 +184,15 @@ __global__ void __launch_bounds__(kThreads) verify_probs_kernel(const ProbsArgs 
     const T* row = p + stop * v;
     const T* draft = replace && q ? q + stop * v : nullptr;
     const int certain = replace && !q ? __shfl_sync(~0u, id, stop) : -1;
-    const int lo = min(rank * a.slice, a.vocab), hi = min(lo + a.slice, a.vocab);
     for (int pass = 0; pass < 2; ++pass) {
       // pass 1 is reached when the difference is zero everywhere: the draw is from p itself
-      uint64_t mine = pass == 0 ? race_slice<T>(row, draft, e, lo, hi, certain)
-                                : race_slice<T>(row, nullptr, e, lo, hi, -1);
-      best = block_max_u64(mine, scratch);
+      const bool vector =
+          noise_fits && (reinterpret_cast<uintptr_t>(row) | reinterpret_cast<uintptr_t>(draft)) % 16 == 0;
+      const Best mine =
+          pass == 0 && draft
+              ? race_slice<T, true>(row, draft, e, lo, hi, -1, vector, noise, noise_fits)
+              : race_slice<T, false>(row, nullptr, e, lo, hi, pass == 0 ? certain : -1, vector, noise, noise_fits && pass == 0);
+      best = block_max_u64(mine.score > 0.0f ? pack_key_id(__float_as_uint(mine.score), uint32_t(mine.id)) : 0, scratch);
       if (ranks > 1) {
         if (int(threadIdx.x) < ranks) st_cluster_u64(map_rank(smem_addr(&mail[pass][rank]), threadIdx.x), best);
         hw_cluster_sync();
@@ -121,13 +215,14 @@ __global__ void __launch_bounds__(kThreads) verify_probs_kernel(const ProbsArgs 
   }
 }
 
-// CTAs per request: enough for every SM to hold eight, as long as a CTA keeps
-// 2048 elements; 16 only for batches that leave most SMs idle otherwise.
+// CTAs per request: as many as fit beside each other in one wave (four CTAs
+// per SM), while a CTA keeps 2000 elements.  256 rows of 128256: 61 us with 2
+// CTAs a row, 66 with 4 (a second, partial wave), 87 with 1; 32 rows of 32000:
+// 8.1 us with 8, 10.6 with 4, 9.9 with 16, so 16 are left to batches of few rows.
 static int probs_cluster(int batch, int vocab, int sms) {
   int c = 1;
-  while (c < 16 && int64_t(batch) * c * 2 <= int64_t(sms) * 8 && vocab / (2 * c) >= 2048) c *= 2;
-  if (c == 16 && int64_t(batch) * 8 >= sms) c = 8;
-  return c;
+  while (c < 16 && int64_t(batch) * c * 2 <= int64_t(sms) * 4 && vocab / (2 * c) >= 2000) c *= 2;
+  return c == 16 && int64_t(batch) * 8 >= sms ? 8 : c;
 }
 
 template <typename T>

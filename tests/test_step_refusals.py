@@ -46,10 +46,17 @@ def test_norm_rope(lib):
     assert call(lib.smp_qk_norm_rope, good, dtype=2) == 2
 
 
+class Cache(ctypes.Structure):
+    """smp_cache of include/smp_cache.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
 def a_cache(**change):
     fields = dict(k=0x1000, v=0x1000, ks=0x1000, vs=0x1000, n=8, h=2, bs=16, d=64, type=0)
     fields.update(change)
-    return ctypes.byref(cache._Cache(*fields.values()))
+    return ctypes.byref(Cache(*fields.values()))
 
 
 BAD_CACHES = [(dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1), (dict(vs=0), 1), (dict(n=0), 1), (dict(h=0), 1),
