@@ -7,8 +7,8 @@
 // (e4m3: exact down to the subnormals; i8: one rounding at the new scale).
 //
 // Bound: HBM, two bytes read (bf16) and one written per element.  The work
-// item is a run (the step's tokens inside one block) of one head, of k or of
-// v: one CTA holds it in registers between the maximum and the encoding.
+// item is a run (the step's tokens inside one block) of one head, k and v: one
+// CTA holds it in registers between the maximum and the encoding.
 // Runs are found from the slots themselves: a CTA looks at a span of up to 32
 // consecutive tokens, one per lane, and handles the runs that begin there.
 #include <cuda_runtime.h>
@@ -46,24 +46,33 @@ __device__ __forceinline__ float needed_scale(float amax) {
   return __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// Codes of four numbers already divided by the scale, the first in the low byte.
+// Four codes of x * inverse for finite x with |x * inverse| <= top, the first
+// in the low byte; the product is exact, so each code is rounded once.
 template <int kType>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inverse) {
   if (kType == SMP_CACHE_E4M3) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b * inverse), "f"(a * inverse));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d * inverse), "f"(c * inverse));
     return uint32_t(lo) | uint32_t(hi) << 16;
   }
   // adding 1.5 * 2^23 rounds to an integer whose low byte is the code
   const float v[4] = {a, b, c, d};
   uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = v[i] != v[i] ? 0.0f : fminf(fmaxf(v[i], -127.0f), 127.0f);
-    q[i] = __float_as_uint(__fadd_rn(x, 12582912.0f));
-  }
+  for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(__fmaf_rn(v[i], inverse, 12582912.0f));
   return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+
+// One code of any x: infinities take the largest code, NaN e4m3's NaN or 0.
+template <int kType>
+__device__ __forceinline__ uint32_t encode1(float x) {
+  if (kType == SMP_CACHE_E4M3) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(x));
+    return c & 0xFFu;
+  }
+  return x != x ? 0u : uint32_t(__float2int_rn(fminf(fmaxf(x, -127.0f), 127.0f))) & 0xFFu;
 }
 
 template <int kType>
@@ -97,29 +106,49 @@ __device__ __forceinline__ float product(float x, float y) {
   return to_odd(p, __fmaf_rn(x, y, -p));
 }
 
-// Eight codes of x / s.  The quotient is a product with the exact inverse of a
-// power of two; a block's scale that the caller set to something else divides.
+// Eight codes of x / s for finite x and a power of two s.
 template <int kType>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inverse) {
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = inverse != 0.0f ? __fmul_rn(x[i], inverse) : quotient(x[i], s);
-  return make_uint2(encode4<kType>(y[0], y[1], y[2], y[3]), encode4<kType>(y[4], y[5], y[6], y[7]));
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inverse) {
+  return make_uint2(encode4<kType>(x[0], x[1], x[2], x[3], inverse), encode4<kType>(x[4], x[5], x[6], x[7], inverse));
 }
 
-template <typename T>
-__device__ __forceinline__ void load_eight(const T* p, bool vector, float (&x)[8]) {
-  if (vector) {
-    load8(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = load1(p + i);
+// The rare forms are out of line and rolled: inlined, they made the kernel
+// miss its instruction cache (56 us against the figure at the kernel).
+
+// Eight codes of any x and any s.
+template <int kType>
+__device__ __noinline__ uint2 encode8_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                          float s) {
+  uint64_t out = 0;
+  for (int i = 0; i < 8; ++i) {
+    out |= uint64_t(encode1<kType>(quotient(x0, s))) << (8 * i);
+    x0 = x1, x1 = x2, x2 = x3, x3 = x4, x4 = x5, x5 = x6, x6 = x7;
+  }
+  return make_uint2(uint32_t(out), uint32_t(out >> 32));
+}
+
+// The `count` codes before a run, encoded again after the scale grew.
+template <int kType>
+__device__ __noinline__ void encode_again(uint8_t* codes, int count, float old, float s) {
+  const float ratio = __fdiv_rn(old, s);
+  for (int i = int(threadIdx.x); i < count / 4; i += kAppendThreads) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
+    const uint32_t c = *p;
+    uint32_t out = 0;
+    for (int j = 0; j < 32; j += 8) out |= encode1<kType>(product(decode1<kType>(uint8_t(c >> j)), ratio)) << j;
+    *p = out;
   }
 }
 
-// Vectors of eight elements that a thread keeps between the two sweeps of a
-// run; longer runs are read again.
-constexpr int kKept = 4;
+// The largest finite |x| of eight.
+template <typename T>
+__device__ __noinline__ float finite_top(Eight<T> e) {
+  float y[8], top = 0.0f;
+  e.get(y);
+  for (int i = 0; i < 8; ++i)
+    if (fabsf(y[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(y[i]));
+  return top;
+}
 
 // One tensor's side of the call: k or v.
 template <typename T>
@@ -131,29 +160,48 @@ struct AppendSide {
   bool vector;
 };
 
+// A run of one head, k and v together: their loads are all in flight before
+// the first is used, and one pair of barriers finds both maxima.
 template <typename T, int kType>
-__device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide<T>& side, int head, int64_t token,
-                                           int count, int64_t slot, float* scratch, int& flags) {
+__device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide<T> (&side)[2], int head,
+                                           int64_t token, int count, int64_t slot, float (*scratch)[2], int& flags) {
+  // vectors of eight elements that a thread keeps of each side between the two
+  // sweeps of a run; longer runs are read again
+  constexpr int kKept = Eight<T>::kInFlight / 2;
   const int tid = int(threadIdx.x), per_row = a.dim / 8, vectors = count * per_row;
   const int64_t block = slot >> a.shift;
   const int offset = int(slot & ((1 << a.shift) - 1));
-  uint8_t* codes = side.codes + ((block * a.heads + head) << a.shift) * a.dim;
-  float* scale = side.scale + block * a.heads + head;
-  const float old = offset ? *scale : 0.0f;
+  uint8_t* codes[2];
+  float* scale[2];
+  const T* x[2];
+  float old[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    codes[w] = side[w].codes + ((block * a.heads + head) << a.shift) * a.dim;
+    scale[w] = side[w].scale + block * a.heads + head;
+    x[w] = side[w].x + token * side[w].stride + int64_t(head) * a.dim;
+    old[w] = offset ? *scale[w] : 0.0f;
+  }
 
   // vector v = tid + i * kAppendThreads is piece v % per_row of row v / per_row
   const int row0 = tid / per_row, piece0 = tid - row0 * per_row;
   const int step_row = kAppendThreads / per_row, step_piece = kAppendThreads - step_row * per_row;
-  const T* x = side.x + token * side.stride + int64_t(head) * a.dim;
-  float kept[kKept][8];
-  float amax = 0.0f;
+  Eight<T> kept[2][kKept];
+  float amax[2] = {0.0f, 0.0f};
   bool odd = false;
-  auto look = [&](const float (&y)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fabsf(y[i]);
-      if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
-      else odd = true;
+  auto load = [&](int w, int row, int piece, Eight<T>& e) {
+    const T* p = x[w] + row * side[w].stride + piece * 8;
+    if (side[w].vector) e.load(p);
+    else e.load_any(p);
+  };
+  // binary32 bits order like the magnitudes, and those at or above infinity's show what is not finite
+  auto look = [&](const Eight<T>& e, float& top) {
+    const uint32_t bits = e.top();
+    if (bits >= 0x7F800000u) {
+      odd = true;
+      top = fmaxf(top, finite_top<T>(e));
+    } else {
+      top = fmaxf(top, __uint_as_float(bits));
     }
   };
   int row = row0, piece = piece0;
@@ -164,88 +212,103 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    if (tid + i * kAppendThreads < vectors) load_eight(x + row * side.stride + piece * 8, side.vector, kept[i]);
+    if (tid + i * kAppendThreads < vectors) load(0, row, piece, kept[0][i]), load(1, row, piece, kept[1][i]);
     advance();
   }
   const int more_row = row, more_piece = piece;
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
-    if (tid + i * kAppendThreads < vectors) look(kept[i]);
+    if (tid + i * kAppendThreads < vectors) look(kept[0][i], amax[0]), look(kept[1][i], amax[1]);
   for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
-    float y[8];
-    load_eight(x + row * side.stride + piece * 8, side.vector, y);
+    Eight<T> e[2];
+    load(0, row, piece, e[0]), load(1, row, piece, e[1]);
     advance();
-    look(y);
+    look(e[0], amax[0]), look(e[1], amax[1]);
   }
   if (odd) flags |= kRowNonFinite;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  __syncthreads();                       // also orders the load of `old` before the store below
-  if ((tid & 31) == 0) scratch[tid >> 5] = amax;
+  for (int o = 16; o; o >>= 1) {
+    amax[0] = fmaxf(amax[0], __shfl_xor_sync(~0u, amax[0], o));
+    amax[1] = fmaxf(amax[1], __shfl_xor_sync(~0u, amax[1], o));
+  }
+  __syncthreads();                       // also orders the loads of `old` before the stores below
+  if ((tid & 31) == 0) scratch[tid >> 5][0] = amax[0], scratch[tid >> 5][1] = amax[1];
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) amax = fmaxf(amax, scratch[w]);
+  for (int w = 0; w < kAppendThreads / 32; ++w)
+    amax[0] = fmaxf(amax[0], scratch[w][0]), amax[1] = fmaxf(amax[1], scratch[w][1]);
 
-  const float s = fmaxf(needed_scale<kType>(amax), old);
-  const float inverse = (__float_as_uint(s) & 0x7FFFFFu) == 0 ? __fdiv_rn(1.0f, s) : 0.0f;
-  if (tid == 0) *scale = s;
-  if (offset && s != old) {
-    const float ratio = __fdiv_rn(old, s);
-    for (int i = tid; i < offset * a.dim / 4; i += kAppendThreads) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
-      const uint32_t w = *p;
-      *p = encode4<kType>(product(decode1<kType>(uint8_t(w)), ratio), product(decode1<kType>(uint8_t(w >> 8)), ratio),
-                          product(decode1<kType>(uint8_t(w >> 16)), ratio),
-                          product(decode1<kType>(uint8_t(w >> 24)), ratio));
-    }
-  }
-  uint2* out = reinterpret_cast<uint2*>(codes + offset * a.dim);   // rows of a run are contiguous
 #pragma unroll
-  for (int i = 0; i < kKept; ++i) {
-    const int v = tid + i * kAppendThreads;
-    if (v < vectors) out[v] = encode8<kType>(kept[i], s, inverse);
-  }
-  row = more_row, piece = more_piece;
-  for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
-    float y[8];
-    load_eight(x + row * side.stride + piece * 8, side.vector, y);
-    advance();
-    out[v] = encode8<kType>(y, s, inverse);
+  for (int w = 0; w < 2; ++w) {
+    const float s = fmaxf(needed_scale<kType>(amax[w]), old[w]);
+    const float inverse = (__float_as_uint(s) & 0x7FFFFFu) == 0 ? __fdiv_rn(1.0f, s) : 0.0f;
+    if (tid == 0) *scale[w] = s;
+    if (offset && s != old[w]) encode_again<kType>(codes[w], offset * a.dim, old[w], s);
+    uint2* out = reinterpret_cast<uint2*>(codes[w] + offset * a.dim);   // rows of a run are contiguous
+    const bool plain = inverse != 0.0f && !odd;
+    auto encode = [&](const Eight<T>& e) {
+      float y[8];
+      e.get(y);
+      return plain ? encode8<kType>(y, inverse) : encode8_any<kType>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], s);
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const int v = tid + i * kAppendThreads;
+      if (v < vectors) out[v] = encode(kept[w][i]);
+    }
+    row = more_row, piece = more_piece;
+    for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
+      Eight<T> e;
+      load(w, row, piece, e);
+      advance();
+      out[v] = encode(e);
+    }
   }
 }
 
-// Grid: (spans of tokens, heads, k or v).
+// Grid: (spans of tokens, heads).
 template <typename T, int kType>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
-  __shared__ float scratch[kAppendThreads / 32];
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const AppendArgs a) {
+  __shared__ float scratch[kAppendThreads / 32][2];
   allow_dependent_launch();
   grid_dependency_wait();
   const int head = int(blockIdx.y), lane = int(threadIdx.x) & 31;
-  const AppendSide<T> side =
-      blockIdx.z ? AppendSide<T>{a.v, a.v_scale, static_cast<const T*>(a.new_v), a.v_stride, a.v_vector}
-                 : AppendSide<T>{a.k, a.k_scale, static_cast<const T*>(a.new_k), a.k_stride, a.k_vector};
-  const int64_t first = int64_t(blockIdx.x) * a.span, mine = first + lane;
+  const AppendSide<T> side[2] = {{a.k, a.k_scale, static_cast<const T*>(a.new_k), a.k_stride, a.k_vector},
+                                 {a.v, a.v_scale, static_cast<const T*>(a.new_v), a.v_stride, a.v_vector}};
+  const int64_t first = int64_t(blockIdx.x) * a.span;
   const int64_t inside = (1 << a.shift) - 1;
   int flags = 0;
-  // every warp looks at the whole span, a token per lane; a run goes on while
-  // the slots follow one another and the block does not end
-  int64_t slot = -1;
-  if (lane < a.span && mine < a.tokens) slot = a.slots[mine];
-  if (slot >= a.slots_end) slot = -1, flags |= kRowBadLength;
-  const bool follows = slot >= 0 && mine > 0 && (slot & inside) != 0 && a.slots[mine - 1] == slot - 1;
-  unsigned starts = __ballot_sync(~0u, slot >= 0 && !follows);
+  // Every warp looks at 64 tokens, two per lane: bit i of `on` says that token
+  // first + i goes on with the run of the one before it (the slots follow one
+  // another and the block has not ended).
+  int64_t slot[2];
+  unsigned goes_on[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t t = first + 32 * h + lane;
+    slot[h] = t < a.tokens ? a.slots[t] : -1;
+    const int64_t before = t > 0 && t < a.tokens ? a.slots[t - 1] : -1;
+    goes_on[h] = __ballot_sync(~0u, slot[h] > 0 && slot[h] < a.slots_end && (slot[h] & inside) != 0 && before == slot[h] - 1);
+  }
+  const uint64_t on = goes_on[0] | uint64_t(goes_on[1]) << 32;
+  if (lane < a.span && slot[0] >= a.slots_end) flags |= kRowBadLength;
+  unsigned starts = __ballot_sync(~0u, lane < a.span && slot[0] >= 0 && slot[0] < a.slots_end) & ~goes_on[0];
   while (starts) {
     const int at = __ffs(starts) - 1;
     starts &= starts - 1;
-    const int64_t run = __shfl_sync(~0u, slot, at);
-    const int most = int(inside + 1 - (run & inside));
-    int count = 1;
-    for (bool more = true; more && count < most;) {
-      const int64_t i = first + at + count + lane;
-      const bool on = count + lane < most && i < a.tokens && a.slots[i] == run + count + lane;
-      const unsigned broken = ~__ballot_sync(~0u, on);
-      more = broken == 0;
-      count += more ? 32 : __ffs(broken) - 1;
+    const int64_t run = __shfl_sync(~0u, slot[0], at);
+    const uint64_t after = ~(at == 63 ? 0 : on >> (at + 1));
+    int count = after ? __ffsll(int64_t(after)) : 64;            // 1 + the tokens that go on
+    if (at + count >= 64) {                                      // the run may leave the 64 tokens
+      count = 64 - at;
+      const int most = int(inside + 1 - (run & inside));
+      for (bool more = true; more && count < most;) {
+        const int64_t i = first + at + count + lane;
+        const bool next = count + lane < most && i < a.tokens && a.slots[i] == run + count + lane;
+        const unsigned broken = ~__ballot_sync(~0u, next);
+        more = broken == 0;
+        count += more ? 32 : __ffs(broken) - 1;
+      }
     }
     append_run<T, kType>(a, side, head, first + at, count, run, scratch, flags);
   }
@@ -256,7 +319,7 @@ template <typename T, int kType>
 static smp_status launch_append(const AppendArgs& a, cudaStream_t st) {
   const int64_t spans = (int64_t(a.tokens) + a.span - 1) / a.span;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(spans), unsigned(a.heads), 2);
+  cfg.gridDim = dim3(unsigned(spans), unsigned(a.heads));
   cfg.blockDim = dim3(kAppendThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -301,10 +364,10 @@ extern "C" smp_status smp_cache_append(const smp_cache* cache, const void* k, co
   a.slots_end = int64_t(cache->num_blocks) << a.shift;
   a.slots = slots;
   a.status = status;
-  // spans as long as leaves every SM some 16 CTAs: a CTA without a run start only costs its launch
+  // spans as long as leaves every SM some 8 CTAs: a CTA without a run start only costs its launch
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
-  const int64_t fill = int64_t(tokens) * a.heads * 2 / (int64_t(device_sms(dev)) * 16);
+  const int64_t fill = int64_t(tokens) * a.heads / (int64_t(device_sms(dev)) * 8);
   a.span = int(fill < 1 ? 1 : fill > 32 ? 32 : fill);
   const bool e4m3 = cache->type == SMP_CACHE_E4M3;
   if (dtype == SMP_F32)

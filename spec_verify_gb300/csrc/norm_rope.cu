@@ -36,16 +36,16 @@ struct NormRopeArgs {
 // Vector form: kLanes lanes per head, each with 8 elements; kHeads heads of one
 // token per group, all loaded before the first is used.
 template <typename T, int kLanes, int kHeads>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const NormRopeArgs a) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int per_token = a.chunks[0] + a.chunks[1];
-  const int64_t item = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
+  const uint32_t item = blockIdx.x * uint32_t(kThreads / kLanes) + threadIdx.x / kLanes;
   const int l = int(threadIdx.x) % kLanes;
-  const int token = int(item / per_token);
+  const int token = int(item / uint32_t(per_token));
   if (token >= a.tokens) return;      // whole groups leave together
   const unsigned group = kLanes == 32 ? ~0u : ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
-  int chunk = int(item - int64_t(token) * per_token);
+  int chunk = int(item - uint32_t(token) * uint32_t(per_token));
   const int which = chunk >= a.chunks[0];
   if (which) chunk -= a.chunks[0];
   const int position = a.positions[token];
@@ -54,15 +54,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
   const int h0 = chunk * kHeads, heads = min(kHeads, a.heads[which] - h0);
   const T* x = static_cast<const T*>(a.x[which]) + token * a.stride[which] + int64_t(h0) * a.dim + l * 8;
   T* out = static_cast<T*>(a.out[which]) + token * a.out_stride[which] + int64_t(h0) * a.dim + l * 8;
-  float y[kHeads][8];
+  Eight<T> raw[kHeads];                // as loaded: all heads are in flight before the first is used
 #pragma unroll
   for (int h = 0; h < kHeads; ++h) {
-    if (live && h < heads) {
-      load8(x + h * a.dim, y[h]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[h][i] = 0.0f;
-    }
+    raw[h].clear();
+    if (live && h < heads) raw[h].load(x + h * a.dim);
   }
   float w[8], c[8], s[8];
 #pragma unroll
@@ -92,21 +88,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
       for (int i = 0; i < 8; ++i) s[i] = upper ? s[i] : -s[i];
     }
   }
+  const float per_element = 1.0f / float(a.dim);
 #pragma unroll
   for (int h = 0; h < kHeads; ++h) {
-    float sum = 0.0f;
+    float y[8], z[8], sum = 0.0f;
+    raw[h].get(y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(y[h][i], y[h][i], sum);
+    for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(group, sum, o, kLanes);
-    const float r = bad ? __int_as_float(0x7FC00000) : rsqrtf(sum / float(a.dim) + a.eps);
-    float z[8];
+    const float r = bad ? __int_as_float(0x7FC00000) : rsqrtf(fmaf(sum, per_element, a.eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[h][i] = y[h][i] * r * w[i];
+    for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float other = a.interleaved ? y[h][i ^ 1] : __shfl_sync(group, y[h][i], partner, kLanes);
-      z[i] = l * 8 < a.rotary ? fmaf(y[h][i], c[i], other * s[i]) : y[h][i];
+      const float other = a.interleaved ? y[i ^ 1] : __shfl_sync(group, y[i], partner, kLanes);
+      z[i] = l * 8 < a.rotary ? fmaf(y[i], c[i], other * s[i]) : y[i];
     }
     if (live && h < heads) store8(out + h * a.dim, z);
   }
@@ -167,7 +164,7 @@ static cudaError_t launch_vector(NormRopeArgs a, cudaStream_t st) {
   for (int w = 0; w < 2; ++w) a.chunks[w] = (a.heads[w] + kHeads - 1) / kHeads;
   const int64_t items = int64_t(a.tokens) * (a.chunks[0] + a.chunks[1]);
   const int64_t grid = (items * kLanes + kThreads - 1) / kThreads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (items > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_cluster(reinterpret_cast<const void*>(&norm_rope_kernel<T, kLanes, kHeads>), dim3(unsigned(grid)),
                         dim3(kThreads), ls, st, &a);
 }
@@ -190,12 +187,12 @@ static smp_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t st) {
   }
   cudaError_t err;
   if (vector) {
-    // four heads per group share the table row and the weights, and keep 64 (bf16) or 128 bytes per lane in flight;
-    // one head per group while that leaves SMs short of warps (16384 tokens of 40 heads of 128: see below)
+    // several heads per group share the table row and the weights and keep 128 bytes per lane in flight; one head
+    // per group while that would leave SMs short of warps
     const int dev = current_device();
     if (dev < 0) return fail_cuda(cudaGetLastError());
     const int64_t warps = int64_t(a.tokens) * (a.heads[0] + a.heads[1]) * (a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32) / 32;
-    err = warps >= int64_t(device_sms(dev)) * 128 ? launch_lanes<T, 4>(a, st) : launch_lanes<T, 1>(a, st);
+    err = warps >= int64_t(device_sms(dev)) * 128 ? launch_lanes<T, Eight<T>::kInFlight>(a, st) : launch_lanes<T, 1>(a, st);
   } else {
     LaunchShape ls;
     ls.pdl = true;
