@@ -17,10 +17,10 @@ extern "C" size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_
                                                       int32_t head_dim, int32_t batch) {
   if (!smp::attention_sizes_ok(tokens, q_heads, kv_heads, head_dim, batch)) return 0;
   const int dev = smp::current_device();
-  const size_t ctas = size_t(dev < 0 ? 160 : smp::device_sms(dev)) * smp::kAttnCtasPerSm;
+  const size_t ctas = size_t(dev < 0 ? 160 : smp::device_sms(dev)) * smp::kAttnMaxCtas;
   // per main CTA: one join record and two parts, each the most rows of a unit with their sums and (m, l)
   const size_t padded = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const size_t rows = padded == 256 ? 64 : 128;
+  const size_t rows = padded == 256 ? 32 : 64;
   return ctas * (16 + 2 * rows * (padded + 2) * 4);
 }
 
@@ -65,12 +65,15 @@ extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q,
   a.scale = scale * 1.4426950408889634f, a.window = window;
   a.out = out, a.out_stride = out_stride, a.lse = out_lse, a.status = status;
   a.joins = static_cast<int4*>(workspace);
-  a.partial = reinterpret_cast<float*>(a.joins + device_sms(dev) * kAttnCtasPerSm);
-  a.min_share = 8;
+  a.partial = reinterpret_cast<float*>(a.joins + device_sms(dev) * kAttnMaxCtas);
   a.q_vector = !misaligned(q, 16) && q_stride * int64_t(elem) % 16 == 0;
   a.out_vector = !misaligned(out, 4 * elem) && out_stride % 4 == 0;
-  // the tile shape follows the average request; longer ones take several row tiles
-  const int64_t rows = (int64_t(tokens) + batch - 1) / batch * a.group;
+  a.min_share = 6;
+  // The row tile follows the requests' tokens, of which the host knows the sum: the same for every request when that
+  // divides evenly (a plain step, or one with as many drafts everywhere), else a third over the average, since ragged
+  // steps have most requests near their longest.  Requests with more rows take several row tiles.
+  const int64_t each = tokens % batch == 0 ? tokens / batch : (int64_t(tokens) * 4 / 3 + batch - 1) / batch;
+  const int64_t rows = each * a.group;
   const bool e4m3 = cache->type == SMP_CACHE_E4M3, split = dtype == SMP_F32;
   const cudaError_t err = e4m3 ? split ? attn_launch<SMP_CACHE_E4M3, true>(a, rows, dev, st)
                                        : attn_launch<SMP_CACHE_E4M3, false>(a, rows, dev, st)

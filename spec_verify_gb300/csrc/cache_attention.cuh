@@ -3,14 +3,13 @@
 //
 // Mathematics.  For the rows of one key head (its queries times the query
 // heads that share it) and tiles of keys:
-//   S^T = K Q^T,  P = 2^(S c - m),  l += sum P,  O^T += V^T (P v u)
-// with c = scale * log2(e) * (the block's key scale), v the block's value
-// scale, and two references per row that move only when they must: m, raised
-// when a score passes it by more than 2^11 (then O and l are multiplied by
-// 2^(m_old - m_new)), and u, a power of two, lowered when a weight P v u would
-// pass 2^15, the range of 16-bit floats.  Both leave the largest weights far
-// above the smallest normal 16-bit float, so the weights that matter keep all
-// 11 bits whatever the scales of the blocks; l is summed from binary32 P.
+//   S^T = K Q^T,  P = 2^(S k f - m),  l += sum P,  O^T += V^T (P v)
+// with k and v the scales of a key's block, f a row's factor (scale * log2(e)
+// over the power of two that Q was scaled by) and one reference m per row,
+// which moves only when a weight P v passes 2^15, the range of 16-bit floats;
+// it then puts the row's largest weight at 2^8, and l and O are multiplied by
+// 2^(m_old - m_new).  Small weights keep all 11 bits down to 2^-22 of the
+// largest, whatever the blocks' scales; l is summed from binary32 P.
 //
 // Both products run on the tensor cores with the cache as the 16-row operand
 // (tokens, then head elements) and the query rows as the 8-wide one, so one
@@ -23,13 +22,16 @@
 // Split.  The keys of all (request, row tile, key head) units form one line of
 // work that is cut into equal shares, one per resident CTA, whatever the
 // lengths; a unit cut by a share's end leaves its parts (m, l, O) in the
-// workspace, and a second kernel joins them in order.  Inside a CTA the warps
-// form teams: a team streams its own tiles through a ring in shared memory by
-// 16-byte asynchronous copies, its warps taking 8 kNT rows each; teams are
-// joined at the unit's end.  Nothing waits on another CTA.
+// workspace, and a second kernel joins them in order.  Nothing waits on
+// another CTA.  A CTA is two warps.  Each takes half of a tile's keys for
+// S and P and half of the head for O, over all rows: every code is converted
+// once, and O, the largest thing in registers, is halved, so that a warp can
+// hold up to 64 rows.  P passes through shared memory, one barrier per tile.
+// K and V stream through rings in shared memory by 16-byte asynchronous
+// copies, a tile ahead.
 //
-// Bound: HBM (one byte per code) up to about 32 rows per key head, then the
-// conversions and tensor cores.
+// Bound: HBM (one byte per code) up to about 40 rows per key head, then the
+// instructions for conversions and softmax.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -41,14 +43,12 @@
 
 namespace smp {
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnThreads = 64;
 constexpr int kAttnUnitCost = 3;        // a unit's fixed cost, in tiles
-constexpr float kShift = 3.0f;          // a new reference m puts the row's largest score at 2^3
-constexpr float kRaise = 11.0f;         // and is replaced once a score passes 2^11
-constexpr uint32_t kWeightLimit = 0x7800u;       // 2^15 as a 16-bit float: u is lowered past it
-constexpr int kWeightExp = 8;                    // a new u puts the largest weight in [2^8, 2^9)
-constexpr int kMaxUExp = 60;                     // u <= 2^60 and v <= 2^66, so that v u is finite
+constexpr float kTopWeight = 8.0f;      // a new reference puts a row's largest weight at 2^8
+constexpr float kMostWeight = 15.0f;    // and is replaced once one passes 2^15
+constexpr uint32_t kWeightLimit = 0x7800u;   // that as a 16-bit float
+constexpr float kLeastScale = -60.0f;   // log2 of the smallest value scale that a reference follows: P stays finite
 
 struct AttnArgs {
   const uint8_t* k;
@@ -95,6 +95,132 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& a, int b) {
   if (r.len > room) r.len = int(room), r.bad = true;
   return r;
 }
+
+// ---------------------------------------------------------------- the line of work
+
+// A CTA's stay in one unit: tiles [tile_lo, tile_hi) of its keys for rows r0 ..
+// r0 + live_rows - 1 of the request's n * group rows of one key head.
+struct AttnSegment {
+  bool whole, first;          // the whole unit; from its beginning
+  int64_t r0;
+  int live_rows, p_first, p_last, tile_lo, tile_hi;
+};
+
+// The units (request, row tile, key head) in order, each as long as its tiles
+// of kTile keys plus kAttnUnitCost, and this CTA's place in them.  Equal
+// shares, whatever the lengths: share j is [j share, (j + 1) share).
+template <int kThreads, int kTile, int kRows>
+struct AttnLine {
+  static constexpr int kLineWarps = kThreads / 32;
+  struct Shared {
+    int64_t scan[kLineWarps];
+    int64_t found[2];
+  };
+  int64_t at, end, share, cost, pos;   // places on the line; the unit's length and the place in it
+  int b, rt, head;
+  AttnRequest req;
+
+  static __device__ __forceinline__ int tile_base(const AttnArgs& a, const AttnRequest& r) {
+    return a.window > 0 ? int(max(int64_t(r.len) - r.n - a.window + 1, int64_t(0)) / kTile) : 0;
+  }
+  static __device__ __forceinline__ int row_tiles(const AttnArgs& a, const AttnRequest& r) {
+    return int((int64_t(r.n) * a.group + kRows - 1) / kRows);
+  }
+  static __device__ __forceinline__ int64_t unit_cost(const AttnArgs& a, const AttnRequest& r) {
+    return max(0, int((int64_t(r.len) + kTile - 1) / kTile) - tile_base(a, r)) + kAttnUnitCost;
+  }
+
+  // Finds the share; every thread of the CTA calls it.  False: there is none.
+  __device__ __forceinline__ bool begin(const AttnArgs& a, Shared& sh, int& flags) {
+    const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    auto cost_of = [&](int request) -> int64_t {
+      const AttnRequest r = attn_request(a, request);
+      if (r.bad) flags |= kRowBadLength;
+      return int64_t(row_tiles(a, r)) * a.kv_heads * unit_cost(a, r);
+    };
+    const int64_t first_cost = tid < a.batch ? cost_of(tid) : 0;
+    int64_t sum = first_cost;
+    for (int r = tid + kThreads; r < a.batch; r += kThreads) sum += cost_of(r);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) sh.scan[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kLineWarps; ++w) total += sh.scan[w];
+    share = max(int64_t(a.min_share), (total + gridDim.x - 1) / gridDim.x);
+    at = share * blockIdx.x;
+    end = min(total, at + share);
+    if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (at >= end) return false;
+    for (int64_t base = 0, chunk = 0;; chunk += kThreads) {
+      const int64_t request = chunk + tid;
+      const int64_t c = chunk == 0 ? first_cost : request < a.batch ? cost_of(int(request)) : 0;
+      int64_t inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, inc, d);
+        if (lane >= d) inc += o;
+      }
+      __syncthreads();
+      if (lane == 31) sh.scan[warp] = inc;
+      __syncthreads();
+      int64_t before = base;
+#pragma unroll
+      for (int w = 0; w < kLineWarps; ++w) {
+        if (w < warp) before += sh.scan[w];
+        base += sh.scan[w];
+      }
+      if (before + inc - c <= at && at < before + inc) sh.found[0] = request, sh.found[1] = before + inc - c;
+      if (base > at) break;                // the same in every thread
+    }
+    __syncthreads();
+    b = int(sh.found[0]);
+    req = attn_request(a, b);
+    cost = unit_cost(a, req);
+    const int64_t unit = (at - sh.found[1]) / cost;
+    pos = at - sh.found[1] - unit * cost;
+    rt = int(unit / a.kv_heads);
+    head = int(unit - int64_t(rt) * a.kv_heads);
+    return true;
+  }
+
+  __device__ __forceinline__ AttnSegment segment(const AttnArgs& a) const {
+    AttnSegment s;
+    const int64_t take = min(cost - pos, end - at);
+    s.first = pos == 0;
+    s.whole = s.first && take == cost;
+    s.r0 = int64_t(rt) * kRows;
+    s.live_rows = int(min(int64_t(kRows), int64_t(req.n) * a.group - s.r0));
+    s.p_first = req.len - req.n + int(s.r0 / a.group);
+    s.p_last = req.len - req.n + int((s.r0 + s.live_rows - 1) / a.group);
+    const int see_first = a.window > 0 ? int(max(int64_t(0), int64_t(s.p_first) - a.window + 1)) : 0;
+    const int base = tile_base(a, req);
+    s.tile_lo = max(base + int(max(pos - kAttnUnitCost, int64_t(0))), see_first / kTile);
+    s.tile_hi = min(base + int(max(pos + take - kAttnUnitCost, int64_t(0))), s.p_last >= 0 ? s.p_last / kTile + 1 : 0);
+    return s;
+  }
+
+  // The parts of the unit at hand, from this CTA on.
+  __device__ __forceinline__ int parts() const { return int((at - pos + cost - 1) / share) - int(blockIdx.x) + 1; }
+
+  // To the next unit; false at the share's end.
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    at += min(cost - pos, end - at);
+    if (at >= end) return false;
+    pos = 0;
+    if (++head == a.kv_heads) {
+      head = 0;
+      if (++rt == row_tiles(a, req)) {
+        rt = 0;
+        do req = attn_request(a, ++b);
+        while (req.n == 0);
+        cost = unit_cost(a, req);
+      }
+    }
+    return true;
+  }
+};
 
 // ---------------------------------------------------------------- small pieces
 
@@ -209,6 +335,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t at) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
 // 16 bytes global to shared, or zeros where !live (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 16 : 0;
@@ -226,161 +358,92 @@ __device__ __forceinline__ void copies_wait() {
 
 // ---------------------------------------------------------------- shapes
 
-template <int kDP, int kNT, int kRG, bool kSplit>
+template <int kDP, int kNT, bool kSplit>
 struct AttnShape {
-  static constexpr int kTile = kDP == 256 ? 16 : 32;             // tokens per tile
-  static constexpr int kMT = kTile / 16;                         // 16-token row tiles of a tile
+  static constexpr int kMT = kDP == 256 ? 1 : 2;                 // 16-token row tiles of S per warp
+  static constexpr int kTile = 2 * kMT * 16;                     // tokens per tile
   static constexpr int kChunks = kDP / 16;                       // 16-byte chunks of a row
   static constexpr int kSteps = kDP / 16;                        // products of depth 16 over the head
-  static constexpr int kDT = kDP / 16;                           // 16-row tiles of V^T
-  static constexpr int kStage = 2 * kTile * kDP;                 // bytes of one ring stage (keys, then values)
-  static constexpr int kTeams = kAttnWarps / kRG;
-  static constexpr int kWarpRows = 8 * kNT;
-  static constexpr int kRows = kWarpRows * kRG;                  // rows of a unit's row tile
+  static constexpr int kDT = kDP / 32;                           // 16-row tiles of a warp's half of V^T
+  static constexpr int kRows = 8 * kNT;                          // rows of a unit's row tile
   static constexpr int kParts = kSplit ? 2 : 1;
-  static constexpr bool kQReg = kNT * kSteps * 2 * kParts <= 32; // query fragments in registers
-  static constexpr int kOPitch = kDP + 4;                        // floats of a row when teams are joined
-  // stages of a team's ring: 96, 80 or 64 KB per CTA for teams of 1, 2 or 4 warps, whose queries take up to 8, 16
-  // or 32 KB
-  static constexpr int kDepth = (kDP == 64 ? 2 : 1) * (kRG == 4 ? 8 : kRG == 2 ? 5 : 3);
-  static constexpr int kRing = kTeams * kDepth * kStage;
-  static constexpr int kJoin = kAttnWarps * kWarpRows * kOPitch * 4;
-  static constexpr int kRingBytes = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kQueryBytes = kQReg ? 0 : kRows / 8 * kSteps * kParts * 32 * 8;
-  // per stage: kMT key scales, kMT value scales, kMT flags; then (m, l, weight) of every warp's rows
-  static constexpr int kScaleBytes = kTeams * kDepth * kMT * 12;
-  static constexpr int kSmem = kRingBytes + kQueryBytes + kScaleBytes + 3 * kAttnWarps * kWarpRows * 4;
+  static constexpr bool kQReg = kNT * kSteps * 2 * kParts <= 16; // query fragments in registers
+  static constexpr int kDepth = kDP == 64 ? 4 : 2;               // stages of each ring
+  static constexpr int kWarpK = kMT * 16 * kDP;                  // bytes of a warp's keys of a tile
+  static constexpr int kVStage = kTile * kDP;
+  static constexpr int kQ4 = kSteps * kParts / 2;                // 16-byte pieces of 8 rows' fragments per lane
+  // shared memory: keys [warp][stage], values [stage], queries, weights [2][row tile of 16 tokens][8 rows][lane]
+  static constexpr int kVAt = 2 * kDepth * kWarpK;
+  static constexpr int kQAt = kVAt + kDepth * kVStage;
+  static constexpr int kPAt = kQAt + (kQReg ? 0 : kNT * kQ4 * 512);
+  static constexpr int kPStage = 2 * kMT * kNT * kParts * 256;
+  static constexpr int kSmem = kPAt + 2 * kPStage;
+  // as many CTAs per SM as 228 KB (1 KB reserved and about 1 KB static per CTA) and 64 K registers allow, 5 at most
+  static constexpr int kFit = 228 * 1024 / (kSmem + 2560);
+  static constexpr int kCtas = kFit > 5 ? 5 : kFit;
 };
+constexpr int kAttnMaxCtas = 5;
+constexpr int kMetaStages = 8;      // tiles whose scales are kept: copies run up to three ahead of a warp one tile behind
 
 // ---------------------------------------------------------------- main kernel
 
-template <int kDP, int kNT, int kRG, int kType, bool kSplit>
-__global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnArgs a) {
-  using S = AttnShape<kDP, kNT, kRG, kSplit>;
+template <int kDP, int kNT, int kType, bool kSplit>
+__global__ void __launch_bounds__(kAttnThreads, (AttnShape<kDP, kNT, kSplit>::kCtas)) attention_kernel(const AttnArgs a) {
+  using S = AttnShape<kDP, kNT, kSplit>;
   using T = typename std::conditional<kSplit, float, uint16_t>::type;
+  using Line = AttnLine<kAttnThreads, S::kTile, S::kRows>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[kAttnWarps + 1];
-  __shared__ int64_t found[2];
+  __shared__ typename Line::Shared line_shared;
+  __shared__ float scales[2][kMetaStages][2][S::kMT];      // [warp][tile][k, v][16 tokens]
+  __shared__ int valid[2][kMetaStages][S::kMT];            // the tokens' block id is one
+  __shared__ float row_factor[S::kRows];
+  __shared__ float row_part[2][S::kRows];                  // of each warp: largest weights, sums
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  constexpr int teams = S::kTeams, rows = S::kRows, depth = S::kDepth, ring_bytes = S::kRingBytes;
-  const int team = warp / kRG, rg = warp % kRG;
-  const uint32_t ring = smem_addr(smem) + uint32_t(team * depth) * S::kStage;
-  uint8_t* const meta = smem + ring_bytes + S::kQueryBytes;
-  float* const meta_scale = reinterpret_cast<float*>(meta) + team * depth * S::kMT * 3;
-  float* const row_m = reinterpret_cast<float*>(meta + S::kScaleBytes);       // [warp][row]
-  float* const row_l = row_m + kAttnWarps * S::kWarpRows;
-  float* const row_w = row_l + kAttnWarps * S::kWarpRows;
-
+  const uint32_t base = smem_addr(smem), keys = base + uint32_t(warp * S::kDepth * S::kWarpK);
   allow_dependent_launch();
   grid_dependency_wait();
 
-  // ---- this CTA's share of the line of work
-  const int cta = int(blockIdx.x);
-  auto unit_tiles = [&](const AttnRequest& r) {
-    const int64_t lo = a.window > 0 ? max(int64_t(r.len) - r.n - a.window + 1, int64_t(0)) : 0;
-    return max(0, (r.len + S::kTile - 1) / S::kTile - int(lo / S::kTile));
-  };
-  auto row_tiles = [&](const AttnRequest& r) {
-    return int((int64_t(r.n) * a.group + rows - 1) / rows);
-  };
-  auto cost_of = [&](int b, int& flags) -> int64_t {
-    const AttnRequest r = attn_request(a, b);
-    if (r.bad) flags |= kRowBadLength;
-    return int64_t(row_tiles(r)) * a.kv_heads * (unit_tiles(r) + kAttnUnitCost);
-  };
+  Line line;
   int flags = 0;
-  int64_t sum = 0;
-  const int64_t first_cost = tid < a.batch ? cost_of(tid, flags) : 0;
-  sum = first_cost;
-  for (int b = tid + kAttnThreads; b < a.batch; b += kAttnThreads) sum += cost_of(b, flags);
-  if (cta != 0) flags = 0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (lane == 0) scan[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) total += scan[w];
-  const int64_t share = max(int64_t(a.min_share), (total + gridDim.x - 1) / gridDim.x);
-  const int64_t mine = share * cta, end = min(total, mine + share);
-  if (tid == 0) a.joins[cta] = make_int4(0, 0, 0, 0);
-  if (mine >= end) {
+  const bool work = line.begin(a, line_shared, flags);
+  if (blockIdx.x != 0) flags = 0;              // one CTA reports the lengths
+  if (!work) {
     if (flags && a.status) atomicOr(a.status, flags);
     return;
   }
-  for (int64_t base = 0, chunk = 0;; chunk += kAttnThreads) {
-    const int b = int(chunk) + tid;
-    int ignored = 0;
-    const int64_t c = chunk == 0 ? first_cost : b < a.batch ? cost_of(b, ignored) : 0;
-    int64_t inc = c;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += o;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    int64_t before = base;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      if (w < warp) before += scan[w];
-      base += scan[w];
-    }
-    if (before + inc - c <= mine && mine < before + inc) found[0] = b, found[1] = before + inc - c;
-    if (base > mine) break;              // the same in every thread
-  }
-  __syncthreads();
 
-  // ---- unused chunks of padded heads stay zero
+  // ---- chunks past the head's end are never written: they stay zero
   if (a.dim < kDP) {
-    for (int i = tid; i < ring_bytes / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < S::kQAt / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
 
-  int b = int(found[0]);
-  AttnRequest req = attn_request(a, b);
-  int64_t cost = unit_tiles(req) + kAttnUnitCost;
-  int64_t unit = (mine - found[1]) / cost, at = mine;
-  int64_t pos = mine - found[1] - unit * cost;
-  int rt = int(unit / a.kv_heads), head = int(unit - int64_t(rt) * a.kv_heads);
-
-  // A stage's copies: one instruction covers kRowsPerCopy rows, keys first; the warps of a team take turns.
-  constexpr int kRowsPerCopy = 32 / S::kChunks, kCopies = 2 * S::kTile / kRowsPerCopy, kHalf = kCopies / 2;
-  constexpr int kPerMT = kHalf / S::kMT;                     // copies of 16 tokens' keys
-  constexpr int kSwizzles = 8 / kRowsPerCopy / kRG > 1 ? 8 / kRowsPerCopy / kRG : 1;
+  // A warp copies the keys and the values of its own tokens of a tile; one instruction covers kRowsPerCopy rows.
+  // Chunk c of row r lies at chunk c ^ swizzle(r): reads of keys (8 rows, 4 chunks) and of values (rows two apart)
+  // then meet the banks evenly.
+  constexpr int kRowsPerCopy = 32 / S::kChunks, kCopies = S::kMT * 16 / kRowsPerCopy, kPerMT = 16 / kRowsPerCopy;
+  constexpr int kSwizzles = 8 / kRowsPerCopy;
   const int my_chunk = lane % S::kChunks, my_row = lane / S::kChunks;
-  // chunk c of row r lies at chunk c ^ swizzle(r): 16-byte reads of keys (8 rows, 4 chunks) and of values (8 rows two
-  // apart, 2 chunks) then meet every bank once
   auto swizzle = [](int r) { return kDP == 64 ? (r >> 1) & 3 : (r & 6) ^ ((r & 1) << 2); };
   uint32_t lane_dst[kSwizzles];
 #pragma unroll
   for (int i = 0; i < kSwizzles; ++i)
-    lane_dst[i] = uint32_t((rg * kRowsPerCopy + my_row) * kDP +
-                           ((my_chunk ^ swizzle((i * kRG + rg) * kRowsPerCopy + my_row)) * 16));
-  const int lane_src = ((rg % kPerMT) * kRowsPerCopy + my_row) * kDP + my_chunk * 16;
+    lane_dst[i] = uint32_t(my_row * kDP + ((my_chunk ^ swizzle(i * kRowsPerCopy + my_row)) * 16));
+  const int lane_src = my_row * kDP + my_chunk * 16;
+  const int64_t block_bytes = (int64_t(a.kv_heads) << a.shift) * a.dim;
 
-  while (at < end) {
-    const int64_t take = min(cost - pos, end - at);
-    const bool whole = pos == 0 && take == cost;
-    const int n = req.n, len = req.len;
-    // rows of this tile: r0 .. r0 + live - 1 of the request's n * group
-    const int64_t r0 = int64_t(rt) * rows;
-    const int live_rows = int(min(int64_t(rows), int64_t(n) * a.group - r0));
-    const int p_first = len - n + int(r0 / a.group), p_last = len - n + int((r0 + live_rows - 1) / a.group);
-    const int see_first = a.window > 0 ? int(max(int64_t(0), int64_t(p_first) - a.window + 1)) : 0;
-    const int tile0 = int((a.window > 0 ? max(int64_t(len) - n - a.window + 1, int64_t(0)) : 0) / S::kTile);
-    const int tile_lo = max(tile0 + int(max(pos - kAttnUnitCost, int64_t(0))), see_first / S::kTile);
-    const int tile_hi = min(tile0 + int(max(pos + take - kAttnUnitCost, int64_t(0))),
-                            p_last >= 0 ? p_last / S::kTile + 1 : 0);
-    const int tiles = max(0, tile_hi - tile_lo);
-    const int iters = (tiles - team + teams - 1) / teams;       // of this team (<= 0: none)
+  for (bool more = true; more;) {
+    const AttnSegment seg = line.segment(a);
+    const AttnRequest req = line.req;
+    const int n = req.n, len = req.len, b = line.b, head = line.head, live_rows = seg.live_rows, p_first = seg.p_first,
+              p_last = seg.p_last, tile_lo = seg.tile_lo, iters = seg.tile_hi - seg.tile_lo;
+    const int64_t r0 = seg.r0;
 
-    // ---- the ring: copies run depth - 1 stages ahead
-    constexpr int kPer = 32 / S::kMT;                           // iterations whose block ids the lanes hold
+    // ---- the rings.  off, ok: where this warp's tokens of the tile last looked up are
+    constexpr int kPer = 32 / S::kMT;                           // tiles whose block ids the lanes hold
     auto load_ids = [&](int k0) {
-      const int k = k0 + lane / S::kMT, token = (tile_lo + team + k * teams) * S::kTile + (lane % S::kMT) * 16;
+      const int k = k0 + lane / S::kMT, token = (tile_lo + k) * S::kTile + (warp * S::kMT + lane % S::kMT) * 16;
       int id = -1;
       if (k < iters && token < len) {
         id = a.table[int64_t(b) * a.stride + (token >> a.shift)];
@@ -389,94 +452,89 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
       return id;
     };
     int ids = load_ids(0), ids_next = load_ids(kPer);
-    int in_k = 0, in_slot = 0, in_id = 0, in_token = (tile_lo + team) * S::kTile;
-    const int64_t head_at = (int64_t(head) << a.shift) * a.dim, block_size_all = (int64_t(a.kv_heads) << a.shift) * a.dim;
-    auto issue = [&]() {
-      if (in_k < iters) {
-        if (in_id == 32) {
-          in_id = 0;
-          ids = ids_next;
-          ids_next = load_ids(in_k + kPer);
+    const int64_t head_at = (int64_t(head) << a.shift) * a.dim;
+    int64_t off[S::kMT];
+    bool ok[S::kMT], full = false;
+    // keys (and scales) of tile k, then its values; both leave one group of copies
+    auto copy_tile = [&](const uint8_t* codes, uint32_t dst, int token0) {
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+          copy16(dst + uint32_t(i * kRowsPerCopy * kDP) + lane_dst[i % kSwizzles],
+                 codes + off[i / kPerMT] + (i % kPerMT) * kRowsPerCopy * kDP + lane_src);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int row = i * kRowsPerCopy + my_row;
+          if (my_chunk * 16 < a.dim)
+            copy16(dst + uint32_t(row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
+                   codes + off[i / kPerMT] + (row % 16) * a.dim + my_chunk * 16, ok[i / kPerMT] && token0 + row < len);
         }
-        const uint32_t dst = ring + uint32_t(in_slot) * S::kStage;
-        int64_t off[S::kMT];
-        bool ok[S::kMT], full = in_token + S::kTile <= len && a.dim == kDP;
+      }
+    };
+    auto issue_keys = [&](int k) {
+      if (k < iters) {
+        const int at = k % kPer * S::kMT, token0 = (tile_lo + k) * S::kTile + warp * S::kMT * 16;
+        if (at == 0 && k > 0) {
+          ids = ids_next;
+          ids_next = load_ids(k + kPer);
+        }
+        full = token0 + S::kMT * 16 <= len && a.dim == kDP;
 #pragma unroll
         for (int mt = 0; mt < S::kMT; ++mt) {
-          const int id = __shfl_sync(~0u, ids, in_id + mt);
+          const int id = __shfl_sync(~0u, ids, at + mt);
           ok[mt] = id >= 0;
           full &= ok[mt];
-          off[mt] = int64_t(max(id, 0)) * block_size_all + head_at + ((in_token + 16 * mt) & ((1 << a.shift) - 1)) * a.dim;
+          off[mt] = int64_t(max(id, 0)) * block_bytes + head_at + ((token0 + 16 * mt) & ((1 << a.shift) - 1)) * a.dim;
         }
-        if (rg == 0) {
-          const int id = __shfl_sync(~0u, ids, in_id + lane % S::kMT);
-          if (lane < 2 * S::kMT) {
-            float* m = meta_scale + in_slot * S::kMT * 3 + lane;
-            copy4(smem_addr(m), (lane < S::kMT ? a.k_scale : a.v_scale) + int64_t(max(id, 0)) * a.kv_heads + head, id >= 0);
-            if (lane < S::kMT) reinterpret_cast<int*>(m)[2 * S::kMT] = id >= 0;
-          }
+        const int id = __shfl_sync(~0u, ids, at + lane % S::kMT);
+        if (lane < 2 * S::kMT) {
+          copy4(smem_addr(&scales[warp][k % kMetaStages][lane / S::kMT][lane % S::kMT]),
+                (lane < S::kMT ? a.k_scale : a.v_scale) + int64_t(max(id, 0)) * a.kv_heads + head, id >= 0);
+          if (lane < S::kMT) valid[warp][k % kMetaStages][lane] = id >= 0;
         }
-        if (full) {
-          // every chunk of every row: a lane's offsets are constants but for kSwizzles of them
-#pragma unroll
-          for (int j = 0; j < kCopies / kRG; ++j) {
-            const int jj = j * kRG % kHalf;                            // + rg: the copy's place in its half
-            const bool second = kRG > kPerMT ? rg >= kPerMT : jj >= kPerMT;
-            copy16(dst + uint32_t((j * kRG / kHalf) * S::kTile * kDP + jj * kRowsPerCopy * kDP) +
-                       lane_dst[jj / kRG % kSwizzles],
-                   (j * kRG / kHalf ? a.v : a.k) + (second ? off[S::kMT - 1] : off[0]) + lane_src +
-                       (jj % kPerMT) * kRowsPerCopy * kDP);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kCopies / kRG; ++j) {
-            const int jj = j * kRG % kHalf + rg, row = jj * kRowsPerCopy + my_row;
-            const bool second = jj >= kPerMT;
-            if (my_chunk * 16 < a.dim)
-              copy16(dst + uint32_t((j * kRG / kHalf) * S::kTile * kDP + row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
-                     (j * kRG / kHalf ? a.v : a.k) + (second ? off[S::kMT - 1] : off[0]) + (row % 16) * a.dim +
-                         my_chunk * 16,
-                     (second ? ok[S::kMT - 1] : ok[0]) && in_token + row < len);
-          }
-        }
-        ++in_k;
-        in_id += S::kMT;
-        in_token += teams * S::kTile;
-        in_slot = in_slot + 1 == depth ? 0 : in_slot + 1;
+        copy_tile(a.k, keys + uint32_t(k % S::kDepth * S::kWarpK), token0);
       }
       copies_commit();
     };
-    for (int k = 0; k < depth - 1; ++k) issue();
+    auto issue_values = [&](int k) {
+      if (k < iters)
+        copy_tile(a.v, base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage + warp * S::kWarpK),
+                  (tile_lo + k) * S::kTile + warp * S::kMT * 16);
+      copies_commit();
+    };
+    for (int k = 0; k < S::kDepth - 1; ++k) {
+      issue_keys(k);
+      issue_values(k);
+    }
 
-    // ---- query fragments: lane (g, t) holds the 16-element chunks t + 4 h of row g of each row tile
-    constexpr int kQ4 = S::kSteps * S::kParts / 2;             // 16-byte pieces of a row tile's fragments per lane
+    // ---- query fragments: lane (g, t) holds the 16-element chunks t + 4 h of row g of each 8 rows
     uint32_t qreg[S::kQReg ? kNT : 1][S::kQReg ? S::kSteps * S::kParts * 2 : 1];
-    float factor[kNT][2];
     int see[kNT][2];                     // last visible position of columns 2t, 2t + 1
-    {
-      uint4* const qs = reinterpret_cast<uint4*>(smem + ring_bytes) + rg * kNT * kQ4 * 32;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        const int row = rg * S::kWarpRows + nt * 8 + g;
-        const bool ok = row < live_rows;
+    for (int nt = 0; nt < kNT; ++nt) {
+      if (S::kQReg || nt % 2 == warp) {
+        const int row = nt * 8 + g;
+        const bool live = row < live_rows;
         const int64_t gr = r0 + row;
-        const int token = req.first + int(gr / a.group), qh = head * a.group + int(gr % a.group);
-        const T* q = static_cast<const T*>(a.q) + (ok ? token * a.q_stride + int64_t(qh) * a.dim : 0);
+        const int64_t token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
+        const T* q = static_cast<const T*>(a.q) + (live ? token * a.q_stride + qh * a.dim : 0);
         float x[S::kSteps][4];
 #pragma unroll
         for (int h = 0; h < kDP / 64; ++h) {
           const int d = (t + 4 * h) * 16;
-          if (ok && d < a.dim && a.q_vector) {
+          Eight<T> e[2];
+          e[0].clear(), e[1].clear();
+          if (live && d < a.dim) {
+            if (a.q_vector) e[0].load(q + d), e[1].load(q + d + 8);
+            else e[0].load_any(q + d), e[1].load_any(q + d + 8);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             float y[8];
-            load8(q + d, y);
+            e[i].get(y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[h * 4 + e / 4][e % 4] = y[e];
-            load8(q + d + 8, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[h * 4 + 2 + e / 4][e % 4] = y[e];
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[h * 4 + e / 4][e % 4] = ok && d < a.dim ? load1(q + d + e) : 0.0f;
+            for (int j = 0; j < 8; ++j) x[h * 4 + i * 2 + j / 4][j % 4] = y[j];
           }
         }
         float top = 0.0f;
@@ -486,12 +544,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
           for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[s][e]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        // up: the power of two that takes the largest element to [2^9, 2^10); down: its inverse
+        // up: the power of two that takes the largest element to [2^9, 2^10); its inverse goes into the row's factor
         const int up_exp = min(max(263 - int(__float_as_uint(top) >> 23), 1), 253);
         const float up = __uint_as_float(uint32_t(up_exp) << 23);
-        const float down = __uint_as_float(uint32_t(254 - up_exp) << 23) * a.scale;
-        factor[nt][0] = __shfl_sync(~0u, down, 8 * t);
-        factor[nt][1] = __shfl_sync(~0u, down, 8 * t + 4);
+        if (t == 0) row_factor[row] = __uint_as_float(uint32_t(254 - up_exp) << 23) * a.scale;
         uint32_t f[S::kSteps * S::kParts * 2];                 // per step: two words, with kSplit the two rests
 #pragma unroll
         for (int s = 0; s < S::kSteps; ++s) {
@@ -508,31 +564,33 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         if (S::kQReg) {
 #pragma unroll
           for (int i = 0; i < S::kSteps * S::kParts * 2; ++i) qreg[S::kQReg ? nt : 0][S::kQReg ? i : 0] = f[i];
-        } else if (team == 0) {
+        } else {
 #pragma unroll
-          for (int i = 0; i < kQ4; ++i)
-            qs[(nt * kQ4 + i) * 32 + lane] = make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int64_t r = r0 + rg * S::kWarpRows + nt * 8 + 2 * t + c;
-          see[nt][c] = r - r0 < live_rows ? len - n + int(r / a.group) : len;     // unused rows: everything, unread
+          for (int i = 0; i < S::kQ4; ++i)
+            *reinterpret_cast<uint4*>(smem + S::kQAt + ((nt * S::kQ4 + i) * 32 + lane) * 16) =
+                make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
         }
       }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        see[nt][c] = r < live_rows ? len - n + int((r0 + r) / a.group) : len;     // unused rows: everything, unread
+      }
     }
-    if (!S::kQReg) __syncthreads();
-    const uint32_t q_at = smem_addr(smem + ring_bytes) + uint32_t(rg * kNT * kQ4 * 32 + lane) * 16;
-
+    __syncthreads();
+    const uint32_t q_at = base + uint32_t(S::kQAt + lane * 16);
+    float factor[kNT][2];
     float o[kNT][S::kDT][4];
-    float l[kNT][2], m[kNT][2], u[kNT][2];
-    uint32_t set_m = 0;                          // rows (2 nt + c) whose reference is set; m = 0, u = 1 before
-    constexpr uint32_t kAllSet = (1u << (2 * kNT)) - 1;
+    float l[kNT][2], m[kNT][2];
+    uint32_t has_ref = 0;                        // rows (2 nt + c) whose reference is set; m = 0 before
+    constexpr uint32_t kAll = (1u << (2 * kNT)) - 1;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = 0.0f, u[nt][c] = 1.0f, l[nt][c] = 0.0f;
-        if (rg * S::kWarpRows + nt * 8 + 2 * t + c >= live_rows) set_m |= 1u << (2 * nt + c);   // unused: never awaited
+        factor[nt][c] = row_factor[nt * 8 + 2 * t + c];
+        m[nt][c] = 0.0f, l[nt][c] = 0.0f;
+        if (nt * 8 + 2 * t + c >= live_rows) has_ref |= 1u << (2 * nt + c);       // unused: never awaited
       }
 #pragma unroll
       for (int d = 0; d < S::kDT; ++d)
@@ -540,17 +598,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.0f;
     }
 
-    uint32_t set_u = set_m;
-    int slot = 0, token0 = (tile_lo + team) * S::kTile;
     for (int k = 0; k < iters; ++k) {
-      copies_wait<depth - 2>();
-      if (kRG == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kRG * 32) : "memory");
-      issue();
-      const uint32_t kst = ring + uint32_t(slot) * S::kStage, vst = kst + S::kTile * kDP;
-      const float* sc = meta_scale + slot * S::kMT * 3;
+      const int token0 = (tile_lo + k) * S::kTile, meta = k % kMetaStages;
+      copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's keys of the tile
+      __syncwarp();
+      issue_keys(k + S::kDepth - 1);
+      const uint32_t kst = keys + uint32_t(k % S::kDepth * S::kWarpK), vst = base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage);
 
-      // ---- S^T = K Q^T
+      // ---- S^T = K Q^T for this warp's keys
       float s[S::kMT][kNT][4];
 #pragma unroll
       for (int mt = 0; mt < S::kMT; ++mt)
@@ -582,10 +637,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
               for (int p = 0; p < S::kParts * 2; ++p)
                 q[p] = qreg[S::kQReg ? nt : 0][S::kQReg ? (h * 4 + i) * S::kParts * 2 + p : 0];
             } else if (kSplit) {
-              const uint4 x = lds128(q_at + uint32_t(nt * kQ4 + h * 4 + i) * 512);
+              const uint4 x = lds128(q_at + uint32_t(nt * S::kQ4 + h * 4 + i) * 512);
               q[0] = x.x, q[1] = x.y, q[S::kParts * 2 - 2] = x.z, q[S::kParts * 2 - 1] = x.w;
             } else {
-              if (i % 2 == 0) q_two[nt] = lds128(q_at + uint32_t(nt * kQ4 + (h * 4 + i) / 2) * 512);
+              if (i % 2 == 0) q_two[nt] = lds128(q_at + uint32_t(nt * S::kQ4 + (h * 4 + i) / 2) * 512);
               q[0] = i % 2 ? q_two[nt].z : q_two[nt].x, q[1] = i % 2 ? q_two[nt].w : q_two[nt].y;
             }
 #pragma unroll
@@ -596,56 +651,103 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
         }
       }
 
-      // ---- exponents: s = S c - m, masked; m raised where one passes the limit
+      // ---- exponents: s = S k f - m, hidden ones -inf
       bool edge = token0 + S::kTile - 1 > p_first || (a.window > 0 && token0 <= p_last - a.window);
+      float v_scale[S::kMT];
 #pragma unroll
       for (int mt = 0; mt < S::kMT; ++mt) {
-        edge |= !reinterpret_cast<const int*>(sc)[2 * S::kMT + mt];
+        const float ks = scales[warp][meta][0][mt];
+        v_scale[mt] = scales[warp][meta][1][mt];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          const uint64_t c = mul2(pair(sc[mt], sc[mt]), pair(factor[nt][0], factor[nt][1]));
+          const uint64_t c = mul2(pair(ks, ks), pair(factor[nt][0], factor[nt][1]));
           const uint64_t less = pair(-m[nt][0], -m[nt][1]);
           unpair(fma2(pair(s[mt][nt][0], s[mt][nt][1]), c, less), s[mt][nt][0], s[mt][nt][1]);
           unpair(fma2(pair(s[mt][nt][2], s[mt][nt][3]), c, less), s[mt][nt][2], s[mt][nt][3]);
         }
       }
+      // whether a row sees token `of` of the tile's row tile mt (of both warps'), element e
       auto visible = [&](int mt, int nt, int e) {
         const int j = token0 + mt * 16 + g + (e / 2) * 8, p = see[nt][e % 2];
-        return j <= p && (a.window == 0 || j > p - a.window) && reinterpret_cast<const int*>(sc)[2 * S::kMT + mt];
+        return j <= p && (a.window == 0 || j > p - a.window) && valid[mt / S::kMT][meta][mt % S::kMT];
       };
-      if (edge) {
+      bool mine = edge;
+#pragma unroll
+      for (int mt = 0; mt < S::kMT; ++mt) mine |= !valid[warp][meta][mt];
+      if (mine) {
 #pragma unroll
         for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!visible(mt, nt, e)) s[mt][nt][e] = -INFINITY;
+              if (!visible(warp * S::kMT + mt, nt, e)) s[mt][nt][e] = -INFINITY;
       }
-      float largest = s[0][0][0];
+
+      // ---- weights P v as 16-bit floats, transposed into the right operand of V^T P^T, for both warps
+      uint32_t packed_max = 0;
+      float sum[kNT][2];
+      const uint32_t p_at = base + uint32_t(S::kPAt + (k & 1) * S::kPStage + lane * 8 * S::kParts);
+      auto weigh = [&] {
+        packed_max = 0;
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt)
+        for (int nt = 0; nt < kNT; ++nt) {
+          uint64_t all = pair(0.0f, 0.0f);
+#pragma unroll
+          for (int mt = 0; mt < S::kMT; ++mt) {
+            const uint64_t vv = pair(v_scale[mt], v_scale[mt]);
+            uint32_t f[S::kParts][2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint64_t p = pair(exp2_approx(s[mt][nt][half * 2]), exp2_approx(s[mt][nt][half * 2 + 1]));
+              all = add2(all, p);
+              float w0, w1;
+              unpair(mul2(p, vv), w0, w1);
+              const uint32_t hi = pack_f16(w0, w1);
+              packed_max = max_f16x2(packed_max, hi);
+              f[0][half] = transpose8(hi);
+              if (kSplit) f[S::kParts - 1][half] = transpose8(rest_f16(hi, w0, w1));
+            }
+            const uint32_t at = p_at + uint32_t(((warp * S::kMT + mt) * kNT + nt) * S::kParts * 256);
+            if (kSplit)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]),
+                           "r"(f[S::kParts - 1][0]), "r"(f[S::kParts - 1][1])
+                           : "memory");
+            else
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]) : "memory");
+          }
+          unpair(all, sum[nt][0], sum[nt][1]);
+        }
+      };
+      weigh();
+      copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's values of the tile
+      const bool past = (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || has_ref != kAll;
+      if (__syncthreads_or(past)) {
+        // rare: the rows' largest weights over both warps' keys, and new references where they pass the limit
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) largest = max3(largest, s[mt][nt][c], s[mt][nt][c + 2]);
-      if (__any_sync(~0u, largest > kRaise || set_m != kAllSet)) {
+          for (int c = 0; c < 2; ++c) {
+            float y = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < S::kMT; ++mt)
+              y = fmaxf(y, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) + fmaxf(__log2f(v_scale[mt]), kLeastScale));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
+            if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = y;
+          }
+        __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          float alpha[2];
+          float alpha[2] = {1.0f, 1.0f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-#pragma unroll
-            for (int mt = 1; mt < S::kMT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]));
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+            const float y = fmaxf(row_part[0][nt * 8 + 2 * t + c], row_part[1][nt * 8 + 2 * t + c]);
             const uint32_t bit = 1u << (2 * nt + c);
-            alpha[c] = 1.0f;
-            if ((set_m & bit) ? x > kShift : x > -INFINITY) {
-              const float up = x - kShift;
-              if (set_m & bit) alpha[c] = exp2_approx(-up);
-              set_m |= bit;
+            if ((has_ref & bit) ? y > kMostWeight : y > -INFINITY) {
+              const float up = y - kTopWeight;
+              if (has_ref & bit) alpha[c] = exp2_approx(-up);
+              has_ref |= bit;
               m[nt][c] += up;
               l[nt][c] *= alpha[c];
 #pragma unroll
@@ -657,277 +759,170 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnAr
             o[nt][d][0] *= alpha[0], o[nt][d][1] *= alpha[1], o[nt][d][2] *= alpha[0], o[nt][d][3] *= alpha[1];
           }
         }
-      }
-
-      // ---- weights P v u as 16-bit floats; u lowered where one passes the limit
-      float v_scale[S::kMT];
-#pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt) v_scale[mt] = fminf(sc[S::kMT + mt], 0x1p66f);
-      uint32_t pf[S::kMT][kNT][S::kParts][2];
-      uint32_t packed_max = 0;
-      auto weigh = [&]() {
-#pragma unroll
-        for (int mt = 0; mt < S::kMT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            const uint64_t vu = mul2(pair(v_scale[mt], v_scale[mt]), pair(u[nt][0], u[nt][1]));
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float p0, p1;
-              unpair(mul2(pair(s[mt][nt][half * 2], s[mt][nt][half * 2 + 1]), vu), p0, p1);
-              pf[mt][nt][0][half] = pack_f16(p0, p1);
-              if (kSplit) pf[mt][nt][S::kParts - 1][half] = rest_f16(pf[mt][nt][0][half], p0, p1);
-              packed_max = max_f16x2(packed_max, pf[mt][nt][0][half]);
-            }
-          }
-      };
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        uint64_t sum = pair(l[nt][0], l[nt][1]);
-#pragma unroll
-        for (int mt = 0; mt < S::kMT; ++mt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = exp2_approx(s[mt][nt][e]);
-          sum = add2(sum, add2(pair(s[mt][nt][0], s[mt][nt][1]), pair(s[mt][nt][2], s[mt][nt][3])));
-        }
-        unpair(sum, l[nt][0], l[nt][1]);
-      }
-      weigh();
-      if (__any_sync(~0u, (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || set_u != kAllSet)) {
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          float beta[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = 0.0f;
-#pragma unroll
-            for (int mt = 0; mt < S::kMT; ++mt) x = fmaxf(x, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) * v_scale[mt]);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-            const uint32_t bit = 1u << (2 * nt + c);
-            beta[c] = 1.0f;
-            const int exp = min(kWeightExp + 127 - int(__float_as_uint(x) >> 23), kMaxUExp);
-            const float lower = __uint_as_float(uint32_t(max(exp, -126) + 127) << 23);
-            if (x > 0.0f && (!(set_u & bit) || lower < u[nt][c])) {
-              if (set_u & bit) beta[c] = lower / u[nt][c];
-              u[nt][c] = lower;
-              set_u |= bit;
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < S::kDT; ++d) {
-            o[nt][d][0] *= beta[0], o[nt][d][1] *= beta[1], o[nt][d][2] *= beta[0], o[nt][d][3] *= beta[1];
-          }
-        }
         weigh();
+        __syncthreads();
       }
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int p = 0; p < S::kParts; ++p)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) pf[mt][nt][p][half] = transpose8(pf[mt][nt][p][half]);
+      for (int nt = 0; nt < kNT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
+      issue_values(k + S::kDepth - 1);
 
-      // ---- O^T += V^T P^T: lane (g, t) reads elements of tokens 2t, 2t+1, 2t+8, 2t+9; row g of tile d is element
-      // 16 g + 2 d (8 g + 2 d of 64), row g + 8 the next one
-      auto values = [&](int mt, int part, uint32_t (&w)[4][4]) {
+      // ---- O^T += V^T P^T for this warp's half of the head: lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 of 16; row g
+      // of row tile d is element kDP / 16 g + 2 d of the half, row g + 8 the next one
+      constexpr int kWords = kDP / 64;           // 4-byte words of a lane's elements
+      auto values = [&](int mt, uint32_t (&w)[4][4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 2 * t + (i & 1) + (i / 2) * 8;
           const uint32_t row = vst + uint32_t((mt * 16 + r) * kDP);
           if (kDP == 64) {
-            const uint2 x = lds64(row + uint32_t((((g >> 1) ^ swizzle(r)) * 16) + (g & 1) * 8));
+            w[i][0] = lds32(row + uint32_t((((warp * 2 + (g >> 2)) ^ swizzle(r)) * 16) + (g & 3) * 4));
+          } else if (kDP == 128) {
+            const uint2 x = lds64(row + uint32_t((((warp * 4 + (g >> 1)) ^ swizzle(r)) * 16) + (g & 1) * 8));
             w[i][0] = x.x, w[i][1] = x.y;
           } else {
-            const uint4 x = lds128(row + uint32_t(((g + 8 * part) ^ swizzle(r)) * 16));
+            const uint4 x = lds128(row + uint32_t(((warp * 8 + g) ^ swizzle(r)) * 16));
             w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
           }
         }
       };
-      constexpr int kPartsV = kDP == 256 ? 2 : 1, kWords = kDP == 64 ? 2 : 4;
       bool nan = false;
-      if (kType == SMP_CACHE_E4M3 && edge) {
-        // a NaN code times a weight of 0 would reach rows that do not see its token
+      if (kType == SMP_CACHE_E4M3) {
 #pragma unroll
-        for (int mt = 0; mt < S::kMT; ++mt)
+        for (int mt = 0; mt < 2 * S::kMT; ++mt) edge |= !valid[mt / S::kMT][meta][mt % S::kMT];
+        if (edge) {
+          // a NaN code times a weight of 0 would reach rows that do not see its token
 #pragma unroll
-          for (int part = 0; part < kPartsV; ++part) {
+          for (int mt = 0; mt < 2 * S::kMT; ++mt) {
             uint32_t w[4][4];
-            values(mt, part, w);
+            values(mt, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int j = 0; j < kWords; ++j) nan |= __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
           }
-        nan = __any_sync(~0u, nan);
+          nan = __any_sync(~0u, nan);
+        }
       }
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt)
+      for (int mt = 0; mt < 2 * S::kMT; ++mt) {
+        uint32_t w[4][4], pf[kNT][S::kParts][2];
+        values(mt, w);
 #pragma unroll
-        for (int part = 0; part < kPartsV; ++part) {
-          uint32_t w[4][4];
-          values(mt, part, w);
-          if (kType == SMP_CACHE_E4M3 && nan) {
-            // NaN codes become 0 for the product; a row that sees one gets NaN from a count of them
-            uint32_t seen[kNT][2];
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-              for (int half = 0; half < 2; ++half)
-                seen[nt][half] = transpose8(pack_f16(visible(mt, nt, half * 2) ? 1.0f : 0.0f,
-                                                     visible(mt, nt, half * 2 + 1) ? 1.0f : 0.0f));
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) {
-              uint32_t z[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                z[i] = __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                w[i][j] &= ~z[i];
-                z[i] &= 0x38383838u;                               // the code of 1
-              }
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t f[4];
-                unpack4<kType>(__byte_perm(z[0], z[1], half ? 0x7362 : 0x5140), f[0], f[1]);
-                unpack4<kType>(__byte_perm(z[2], z[3], half ? 0x7362 : 0x5140), f[2], f[3]);
-                const int d = part * 8 + 2 * j + half;
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                  float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  mma_f16(count, f, seen[nt][0], seen[nt][1]);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (count[e] > 0.0f) o[nt][d][e] = __int_as_float(0x7FC00000);
-                }
-              }
-            }
+        for (int nt = 0; nt < kNT; ++nt) {
+          const uint32_t at = p_at + uint32_t((mt * kNT + nt) * S::kParts * 256);
+          if (kSplit) {
+            const uint4 x = lds128(at);
+            pf[nt][0][0] = x.x, pf[nt][0][1] = x.y, pf[nt][S::kParts - 1][0] = x.z, pf[nt][S::kParts - 1][1] = x.w;
+          } else {
+            const uint2 x = lds64(at);
+            pf[nt][0][0] = x.x, pf[nt][0][1] = x.y;
           }
+        }
+        if (kType == SMP_CACHE_E4M3 && nan) {
+          // NaN codes become 0 for the product; a row that sees one gets NaN from a count of them
+          uint32_t seen[kNT][2];
 #pragma unroll
-          for (int j = 0; j < kWords; ++j)
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              seen[nt][half] = transpose8(
+                  pack_f16(visible(mt, nt, half * 2) ? 1.0f : 0.0f, visible(mt, nt, half * 2 + 1) ? 1.0f : 0.0f));
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            uint32_t z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              z[i] = __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              w[i][j] &= ~z[i];
+              z[i] &= 0x38383838u;                               // the code of 1
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               uint32_t f[4];
-              unpack4<kType>(__byte_perm(w[0][j], w[1][j], half ? 0x7362 : 0x5140), f[0], f[1]);
-              unpack4<kType>(__byte_perm(w[2][j], w[3][j], half ? 0x7362 : 0x5140), f[2], f[3]);
-              const int d = part * 8 + 2 * j + half;
+              unpack4<kType>(__byte_perm(z[0], z[1], half ? 0x7362 : 0x5140), f[0], f[1]);
+              unpack4<kType>(__byte_perm(z[2], z[3], half ? 0x7362 : 0x5140), f[2], f[3]);
 #pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
+              for (int nt = 0; nt < kNT; ++nt) {
+                float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_f16(count, f, seen[nt][0], seen[nt][1]);
 #pragma unroll
-                for (int p = 0; p < S::kParts; ++p) mma_f16(o[nt][d], f, pf[mt][nt][p][0], pf[mt][nt][p][1]);
+                for (int e = 0; e < 4; ++e)
+                  if (count[e] > 0.0f) o[nt][2 * j + half][e] = __int_as_float(0x7FC00000);
+              }
             }
+          }
         }
-      slot = slot + 1 == depth ? 0 : slot + 1;
-      token0 += teams * S::kTile;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t f[4];
+            unpack4<kType>(__byte_perm(w[0][j], w[1][j], half ? 0x7362 : 0x5140), f[0], f[1]);
+            unpack4<kType>(__byte_perm(w[2][j], w[3][j], half ? 0x7362 : 0x5140), f[2], f[3]);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int p = 0; p < S::kParts; ++p) mma_f16(o[nt][2 * j + half], f, pf[nt][p][0], pf[nt][p][1]);
+          }
+      }
     }
     copies_wait<0>();
 
-    // ---- join the teams: (m, l) of every row, then O through the ring's memory
+    // ---- l over all keys; O needs no joining: a warp has its half of the head
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], d);
-        if (g == 0) {
-          row_m[warp * S::kWarpRows + nt * 8 + 2 * t + c] = set_m >> (2 * nt + c) & 1 ? m[nt][c] : -INFINITY;
-          row_l[warp * S::kWarpRows + nt * 8 + 2 * t + c] = l[nt][c];
-        }
+        if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = l[nt][c];
       }
-    __syncthreads();                              // every team is done with the ring
-    float* const join = reinterpret_cast<float*>(smem) + warp * S::kWarpRows * S::kOPitch;
+    __syncthreads();                             // and both warps are done with the rings
+    float* const part = a.partial + (int64_t(blockIdx.x) * 2 + (seg.first ? 1 : 0)) * S::kRows * (kDP + 2);
+    constexpr int kMine = kDP / 16;              // a lane's consecutive elements of a row
+    const int d0 = warp * (kDP / 2) + g * kMine;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const float back[2] = {1.0f / u[nt][0], 1.0f / u[nt][1]};
+    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-      for (int d = 0; d < S::kDT; ++d)
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        if (r >= live_rows) continue;
+        const float all = row_part[0][r] + row_part[1][r];
+        const float ref = has_ref >> (2 * nt + c) & 1 ? m[nt][c] : -INFINITY;     // -inf: nothing was seen (or only NaN)
+        const int64_t gr = r0 + r, token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
+        const float inv = !seg.whole ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+        float y[kMine];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int e = kDP == 64 ? 8 * g + 2 * d : (d / 8) * 128 + 16 * g + 2 * (d % 8);
-          *reinterpret_cast<float2*>(join + (nt * 8 + 2 * t + c) * S::kOPitch + e) =
-              make_float2(o[nt][d][c] * back[c], o[nt][d][c + 2] * back[c]);
-        }
-    }
-    // each warp's weight in its row, and the rows' joined (m, l) in the first team's place
-    for (int r = tid; r < rows; r += kAttnThreads) {
-      float top = -INFINITY, all = 0.0f;
-      for (int w = 0; w < teams; ++w) top = fmaxf(top, row_m[w * rows + r]);
-      for (int w = 0; w < teams; ++w) {
-        const float mw = row_m[w * rows + r], f = mw == -INFINITY ? 0.0f : exp2_approx(mw - top);
-        // a NaN score leaves its row's reference alone: its sum, not the weight, is NaN
-        row_w[w * rows + r] = row_l[w * rows + r] != 0.0f ? (mw == -INFINITY ? 1.0f : f) : 0.0f;
-        if (row_l[w * rows + r] != 0.0f) all += row_l[w * rows + r] * row_w[w * rows + r];
-      }
-      row_m[r] = top;
-      row_l[r] = all;
-    }
-    __syncthreads();
-    constexpr int kVecs = kDP / 4;
-    float* const part = a.partial + (int64_t(cta) * 2 + (pos > 0 ? 0 : 1)) * rows * (kDP + 2);
-    for (int i = tid; i < rows * kVecs; i += kAttnThreads) {
-      const int r = i / kVecs, d = i % kVecs * 4;
-      if (r >= live_rows) break;
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int w = 0; w < teams; ++w) {
-        const float f = row_w[w * rows + r];
-        if (f != 0.0f) {
-          const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * rows + r) * S::kOPitch + d);
-          x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-        }
-      }
-      if (whole) {
-        const float inv = row_l[r] == 0.0f ? 0.0f : 1.0f / row_l[r];
-        const int64_t gr = r0 + r;
-        T* out = static_cast<T*>(a.out) + (req.first + gr / a.group) * a.out_stride +
-                 (int64_t(head) * a.group + gr % a.group) * a.dim;
-        const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
-        if (d < a.dim) {
-          if (a.out_vector) {
-            store4(out + d, y);
-          } else {
+        for (int d = 0; d < S::kDT; ++d) y[2 * d] = o[nt][d][c] * inv, y[2 * d + 1] = o[nt][d][c + 2] * inv;
+        if (!seg.whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store1(out + d + e, y[e]);
+          for (int i = 0; i < kMine; i += 4)
+            *reinterpret_cast<float4*>(part + r * kDP + d0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        } else if (d0 < a.dim) {
+          T* const out = static_cast<T*>(a.out) + token * a.out_stride + qh * a.dim + d0;
+#pragma unroll
+          for (int i = 0; i < kMine; i += 4) {
+            const float z[4] = {y[i], y[i + 1], y[i + 2], y[i + 3]};
+            if (a.out_vector) {
+              store4(out + i, z);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) store1(out + i + e, z[e]);
+            }
           }
         }
-      } else {
-        *reinterpret_cast<float4*>(part + r * kDP + d) = x;
-      }
-    }
-    for (int r = tid; r < live_rows; r += kAttnThreads) {
-      if (!whole) {
-        part[rows * kDP + r] = row_m[r];
-        part[rows * kDP + rows + r] = row_l[r];
-      } else if (a.lse) {
-        const int64_t gr = r0 + r;
-        a.lse[(req.first + gr / a.group) * a.q_heads + int64_t(head) * a.group + gr % a.group] =
-            row_l[r] == 0.0f ? -INFINITY : (row_m[r] + log2f(row_l[r])) * 0.6931471805599453f;
-      }
-    }
-    if (!whole && pos == 0 && tid == 0)
-      a.joins[cta] = make_int4(b, rt, head, int((at + cost - 1) / share) - cta + 1);
-    __syncthreads();
-
-    // ---- the next unit
-    at += take;
-    pos = 0;
-    if (++head == a.kv_heads) {
-      head = 0;
-      if (++rt == row_tiles(req)) {
-        rt = 0;
-        if (at < end) {
-          do req = attn_request(a, ++b);
-          while (req.n == 0);
-          cost = unit_tiles(req) + kAttnUnitCost;
+        if (warp == 0 && g == 0) {
+          if (!seg.whole) {
+            part[S::kRows * kDP + r] = ref;
+            part[S::kRows * kDP + S::kRows + r] = all;
+          } else if (a.lse) {
+            a.lse[token * a.q_heads + qh] = all == 0.0f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+          }
         }
       }
-    }
-    // unused chunks of padded heads were overwritten by the join
-    if (a.dim < kDP && at < end) {
-      for (int i = tid; i < ring_bytes / 16; i += kAttnThreads)
-        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-      __syncthreads();
-    }
+    if (!seg.whole && seg.first && tid == 0) a.joins[blockIdx.x] = make_int4(b, line.rt, head, line.parts());
+    more = line.next(a);
+    __syncthreads();                             // row_part and row_factor have been read
   }
   if (flags && a.status) atomicOr(a.status, flags);
 }
@@ -989,16 +984,13 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, c
 
 // ---------------------------------------------------------------- launch
 
-constexpr int kAttnCtasPerSm = 2;
-
-template <int kDP, int kNT, int kRG, int kType, bool kSplit>
+template <int kDP, int kNT, int kType, bool kSplit>
 cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
-  using S = AttnShape<kDP, kNT, kRG, kSplit>;
+  using S = AttnShape<kDP, kNT, kSplit>;
   LaunchShape ls;
   ls.smem = size_t(S::kSmem);
-  // one wave: as many CTAs as fit at once (228 KB of shared memory per SM, 1 KB of it reserved per CTA)
-  const int grid = device_sms(dev) * (2 * (S::kSmem + 1280) <= 228 * 1024 ? kAttnCtasPerSm : 1);
-  cudaError_t err = prepare_kernel(reinterpret_cast<const void*>(&attention_kernel<kDP, kNT, kRG, kType, kSplit>), dev, ls);
+  const int grid = device_sms(dev) * S::kCtas;         // one wave
+  cudaError_t err = prepare_kernel(reinterpret_cast<const void*>(&attention_kernel<kDP, kNT, kType, kSplit>), dev, ls);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
@@ -1010,7 +1002,7 @@ cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kNT, kRG, kType, kSplit>, a);
+  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kNT, kType, kSplit>, a);
   if (err != cudaSuccess) return err;
   cfg.gridDim = dim3(unsigned(grid), unsigned(S::kRows / 8));
   cfg.blockDim = dim3(256);
@@ -1018,23 +1010,22 @@ cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, S::kRows);
 }
 
-// The smallest row tile that holds `rows` rows of a key head: more row tiles
-// of 8 per warp while the registers hold their sums (they share the codes'
-// conversion), then more warps per team.
+// The smallest row tile that holds `rows` rows of a key head, up to what the
+// registers hold; more rows take several tiles, which read the keys again.
 template <int kType, bool kSplit, int kDP>
 cudaError_t attn_launch_dim(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {
-  if (rows <= 8) return attn_launch_shape<kDP, 1, 1, kType, kSplit>(a, dev, st);
-  if (rows <= 16) return attn_launch_shape<kDP, 2, 1, kType, kSplit>(a, dev, st);
+  if (rows <= 8) return attn_launch_shape<kDP, 1, kType, kSplit>(a, dev, st);
+  if (rows <= 16) return attn_launch_shape<kDP, 2, kType, kSplit>(a, dev, st);
   if constexpr (kSplit || kDP == 256) {
-    if (rows <= 32) return attn_launch_shape<kDP, 2, 2, kType, kSplit>(a, dev, st);
-    return attn_launch_shape<kDP, 2, 4, kType, kSplit>(a, dev, st);
+    return attn_launch_shape<kDP, 4, kType, kSplit>(a, dev, st);
   } else {
-    if (rows <= 24) return attn_launch_shape<kDP, 3, 1, kType, kSplit>(a, dev, st);
-    if (rows <= 32) return attn_launch_shape<kDP, 4, 1, kType, kSplit>(a, dev, st);
-    if (rows <= 48) return attn_launch_shape<kDP, 3, 2, kType, kSplit>(a, dev, st);
-    if (rows <= 64) return attn_launch_shape<kDP, 4, 2, kType, kSplit>(a, dev, st);
-    if (rows <= 96) return attn_launch_shape<kDP, 3, 4, kType, kSplit>(a, dev, st);
-    return attn_launch_shape<kDP, 4, 4, kType, kSplit>(a, dev, st);
+    // several tiles: the fewest, and then the smallest that are as few
+    const int64_t tiles = (rows + 63) / 64, each = (rows + tiles - 1) / tiles;
+    if (each <= 24) return attn_launch_shape<kDP, 3, kType, kSplit>(a, dev, st);
+    if (each <= 32) return attn_launch_shape<kDP, 4, kType, kSplit>(a, dev, st);
+    if (each <= 40) return attn_launch_shape<kDP, 5, kType, kSplit>(a, dev, st);
+    if (each <= 48) return attn_launch_shape<kDP, 6, kType, kSplit>(a, dev, st);
+    return attn_launch_shape<kDP, 8, kType, kSplit>(a, dev, st);
   }
 }
 
