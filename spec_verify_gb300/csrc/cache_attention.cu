@@ -20,7 +20,7 @@ extern "C" size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_
   const size_t ctas = size_t(dev < 0 ? 160 : smp::device_sms(dev)) * smp::kAttnMaxCtas;
   // per main CTA: one join record and two parts, each the most rows of a unit with their sums and (m, l)
   const size_t padded = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  const size_t rows = padded == 256 ? 32 : 64;
+  const size_t rows = padded == 256 ? 32 : 40;
   return ctas * (16 + 2 * rows * (padded + 2) * 4);
 }
 
@@ -69,11 +69,8 @@ extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q,
   a.q_vector = !misaligned(q, 16) && q_stride * int64_t(elem) % 16 == 0;
   a.out_vector = !misaligned(out, 4 * elem) && out_stride % 4 == 0;
   a.min_share = 6;
-  // The row tile follows the requests' tokens, of which the host knows the sum: the same for every request when that
-  // divides evenly (a plain step, or one with as many drafts everywhere), else a third over the average, since ragged
-  // steps have most requests near their longest.  Requests with more rows take several row tiles.
-  const int64_t each = tokens % batch == 0 ? tokens / batch : (int64_t(tokens) * 4 / 3 + batch - 1) / batch;
-  const int64_t rows = each * a.group;
+  // a little over the average request: ragged steps have most requests near their longest
+  const int64_t rows = (int64_t(tokens) * a.group * 5 / 4 + batch - 1) / batch;
   const bool e4m3 = cache->type == SMP_CACHE_E4M3, split = dtype == SMP_F32;
   const cudaError_t err = e4m3 ? split ? attn_launch<SMP_CACHE_E4M3, true>(a, rows, dev, st)
                                        : attn_launch<SMP_CACHE_E4M3, false>(a, rows, dev, st)

@@ -38,6 +38,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 #include "launch.h"
 
@@ -71,7 +73,7 @@ struct AttnArgs {
   float* lse;
   int32_t* status;
   float* partial;           // [CTA][2][rows][dim_padded + 2]
-  int4* joins;              // [CTA]: request, row tile, key head, parts of the unit that begins there (0: none)
+  int4* joins;              // [CTA]: request, row tile, key head, parts (0: none) and eights << 24 of the unit cut there
   bool q_vector, out_vector;   // queries and results take 16-byte (results: 4-element) accesses
   int min_share;            // smallest share of a CTA, in tiles
 };
@@ -108,8 +110,11 @@ struct AttnSegment {
 
 // The units (request, row tile, key head) in order, each as long as its tiles
 // of kTile keys plus kAttnUnitCost, and this CTA's place in them.  Equal
-// shares, whatever the lengths: share j is [j share, (j + 1) share).
-template <int kThreads, int kTile, int kRows>
+// shares, whatever the lengths: share j is [j share, (j + 1) share).  Each
+// request has row tiles of its own size, the fewest and then the smallest of
+// up to kMaxNT eights that hold its rows, so that a step of one token beside
+// one of many costs what its rows cost.
+template <int kThreads, int kTile, int kMaxNT>
 struct AttnLine {
   static constexpr int kLineWarps = kThreads / 32;
   struct Shared {
@@ -117,14 +122,17 @@ struct AttnLine {
     int64_t found[2];
   };
   int64_t at, end, share, cost, pos;   // places on the line; the unit's length and the place in it
+  int nt;                              // rows of a row tile, in eights
   int b, rt, head;
   AttnRequest req;
 
   static __device__ __forceinline__ int tile_base(const AttnArgs& a, const AttnRequest& r) {
     return a.window > 0 ? int(max(int64_t(r.len) - r.n - a.window + 1, int64_t(0)) / kTile) : 0;
   }
-  static __device__ __forceinline__ int row_tiles(const AttnArgs& a, const AttnRequest& r) {
-    return int((int64_t(r.n) * a.group + kRows - 1) / kRows);
+  // Row tiles of a request.
+  __device__ __forceinline__ int row_tiles(const AttnArgs& a, const AttnRequest& r) const {
+    const int64_t rows = int64_t(r.n) * a.group;
+    return rows <= 8 * nt ? rows > 0 : int((rows + 8 * nt - 1) / (8 * nt));
   }
   static __device__ __forceinline__ int64_t unit_cost(const AttnArgs& a, const AttnRequest& r) {
     return max(0, int((int64_t(r.len) + kTile - 1) / kTile) - tile_base(a, r)) + kAttnUnitCost;
@@ -133,9 +141,23 @@ struct AttnLine {
   // Finds the share; every thread of the CTA calls it.  False: there is none.
   __device__ __forceinline__ bool begin(const AttnArgs& a, Shared& sh, int& flags) {
     const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    int64_t most = 0;
+    for (int r = tid; r < a.batch; r += kThreads) {
+      const AttnRequest q = attn_request(a, r);
+      if (q.bad) flags |= kRowBadLength;
+      most = max(most, int64_t(q.n) * a.group);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
+    if (lane == 0) sh.scan[warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kLineWarps; ++w) most = max(most, sh.scan[w]);
+    __syncthreads();
+    const int64_t tiles = max((most + 8 * kMaxNT - 1) / (8 * kMaxNT), int64_t(1));
+    nt = max(int(((most + tiles - 1) / tiles + 7) / 8), 1);
     auto cost_of = [&](int request) -> int64_t {
       const AttnRequest r = attn_request(a, request);
-      if (r.bad) flags |= kRowBadLength;
       return int64_t(row_tiles(a, r)) * a.kv_heads * unit_cost(a, r);
     };
     const int64_t first_cost = tid < a.batch ? cost_of(tid) : 0;
@@ -190,8 +212,8 @@ struct AttnLine {
     const int64_t take = min(cost - pos, end - at);
     s.first = pos == 0;
     s.whole = s.first && take == cost;
-    s.r0 = int64_t(rt) * kRows;
-    s.live_rows = int(min(int64_t(kRows), int64_t(req.n) * a.group - s.r0));
+    s.r0 = int64_t(rt) * 8 * nt;
+    s.live_rows = int(min(int64_t(8 * nt), int64_t(req.n) * a.group - s.r0));
     s.p_first = req.len - req.n + int(s.r0 / a.group);
     s.p_last = req.len - req.n + int((s.r0 + s.live_rows - 1) / a.group);
     const int see_first = a.window > 0 ? int(max(int64_t(0), int64_t(s.p_first) - a.window + 1)) : 0;
@@ -378,46 +400,44 @@ struct AttnShape {
   static constexpr int kPAt = kQAt + (kQReg ? 0 : kNT * kQ4 * 512);
   static constexpr int kPStage = 2 * kMT * kNT * kParts * 256;
   static constexpr int kSmem = kPAt + 2 * kPStage;
-  // as many CTAs per SM as 228 KB (1 KB reserved and about 1 KB static per CTA) and 64 K registers allow, 5 at most
-  static constexpr int kFit = 228 * 1024 / (kSmem + 2560);
-  static constexpr int kCtas = kFit > 5 ? 5 : kFit;
 };
 constexpr int kAttnMaxCtas = 5;
+
+// What a kernel with row tiles of up to kMaxNT eights needs: as many CTAs per
+// SM as 228 KB (1 KB reserved and about 1.5 KB static per CTA) hold, 5 at most.
+template <int kDP, int kMaxNT, bool kSplit>
+struct AttnKernel {
+  static constexpr int kSmem = AttnShape<kDP, kMaxNT, kSplit>::kSmem;
+  static constexpr int kFit = 228 * 1024 / (kSmem + 2560);
+  static constexpr int kCtas = kFit > kAttnMaxCtas ? kAttnMaxCtas : kFit;
+  static constexpr int kRows = 8 * kMaxNT;
+};
 constexpr int kMetaStages = 8;      // tiles whose scales are kept: copies run up to three ahead of a warp one tile behind
 
 // ---------------------------------------------------------------- main kernel
 
-template <int kDP, int kNT, int kType, bool kSplit>
-__global__ void __launch_bounds__(kAttnThreads, (AttnShape<kDP, kNT, kSplit>::kCtas)) attention_kernel(const AttnArgs a) {
+// Scales and exchanges of a CTA, beside its rings.
+template <int kMT, int kRows>
+struct AttnShared {
+  float scales[2][kMetaStages][2][kMT];      // [warp][tile][k, v][16 tokens]
+  int valid[2][kMetaStages][kMT];            // the tokens' block id is one
+  float row_factor[kRows];
+  float row_part[2][kRows];                  // of each warp: largest weights, sums
+};
+
+// One segment: its keys, values and queries to its result, or its part of one.
+template <int kDP, int kNT, int kMaxNT, int kType, bool kSplit>
+__device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnSegment& seg, const AttnRequest& req,
+                                                  const int b, const int head, uint8_t* smem,
+                                                  AttnShared<AttnShape<kDP, 1, kSplit>::kMT, 8 * kMaxNT>& sh, int& flags) {
   using S = AttnShape<kDP, kNT, kSplit>;
   using T = typename std::conditional<kSplit, float, uint16_t>::type;
-  using Line = AttnLine<kAttnThreads, S::kTile, S::kRows>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ typename Line::Shared line_shared;
-  __shared__ float scales[2][kMetaStages][2][S::kMT];      // [warp][tile][k, v][16 tokens]
-  __shared__ int valid[2][kMetaStages][S::kMT];            // the tokens' block id is one
-  __shared__ float row_factor[S::kRows];
-  __shared__ float row_part[2][S::kRows];                  // of each warp: largest weights, sums
-
+  auto& scales = sh.scales;
+  auto& valid = sh.valid;
+  auto& row_factor = sh.row_factor;
+  auto& row_part = sh.row_part;
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t base = smem_addr(smem), keys = base + uint32_t(warp * S::kDepth * S::kWarpK);
-  allow_dependent_launch();
-  grid_dependency_wait();
-
-  Line line;
-  int flags = 0;
-  const bool work = line.begin(a, line_shared, flags);
-  if (blockIdx.x != 0) flags = 0;              // one CTA reports the lengths
-  if (!work) {
-    if (flags && a.status) atomicOr(a.status, flags);
-    return;
-  }
-
-  // ---- chunks past the head's end are never written: they stay zero
-  if (a.dim < kDP) {
-    for (int i = tid; i < S::kQAt / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
 
   // A warp copies the keys and the values of its own tokens of a tile; one instruction covers kRowsPerCopy rows.
   // Chunk c of row r lies at chunk c ^ swizzle(r): reads of keys (8 rows, 4 chunks) and of values (rows two apart)
@@ -432,497 +452,542 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnShape<kDP, kNT, kSplit>::kC
     lane_dst[i] = uint32_t(my_row * kDP + ((my_chunk ^ swizzle(i * kRowsPerCopy + my_row)) * 16));
   const int lane_src = my_row * kDP + my_chunk * 16;
   const int64_t block_bytes = (int64_t(a.kv_heads) << a.shift) * a.dim;
+  const int n = req.n, len = req.len, live_rows = seg.live_rows, p_first = seg.p_first, p_last = seg.p_last,
+            tile_lo = seg.tile_lo, iters = seg.tile_hi - seg.tile_lo;
+  const int64_t r0 = seg.r0;
 
-  for (bool more = true; more;) {
-    const AttnSegment seg = line.segment(a);
-    const AttnRequest req = line.req;
-    const int n = req.n, len = req.len, b = line.b, head = line.head, live_rows = seg.live_rows, p_first = seg.p_first,
-              p_last = seg.p_last, tile_lo = seg.tile_lo, iters = seg.tile_hi - seg.tile_lo;
-    const int64_t r0 = seg.r0;
-
-    // ---- the rings.  off, ok: where this warp's tokens of the tile last looked up are
-    constexpr int kPer = 32 / S::kMT;                           // tiles whose block ids the lanes hold
-    auto load_ids = [&](int k0) {
-      const int k = k0 + lane / S::kMT, token = (tile_lo + k) * S::kTile + (warp * S::kMT + lane % S::kMT) * 16;
-      int id = -1;
-      if (k < iters && token < len) {
-        id = a.table[int64_t(b) * a.stride + (token >> a.shift)];
-        if (id < 0 || id >= a.num_blocks) id = -1, flags |= kRowBadBlock;
-      }
-      return id;
-    };
-    int ids = load_ids(0), ids_next = load_ids(kPer);
-    const int64_t head_at = (int64_t(head) << a.shift) * a.dim;
-    int64_t off[S::kMT];
-    bool ok[S::kMT], full = false;
-    // keys (and scales) of tile k, then its values; both leave one group of copies
-    auto copy_tile = [&](const uint8_t* codes, uint32_t dst, int token0) {
-      if (full) {
+  // ---- the rings.  off, ok: where this warp's tokens of the tile last looked up are
+  constexpr int kPer = 32 / S::kMT;                           // tiles whose block ids the lanes hold
+  auto load_ids = [&](int k0) {
+    const int k = k0 + lane / S::kMT, token = (tile_lo + k) * S::kTile + (warp * S::kMT + lane % S::kMT) * 16;
+    int id = -1;
+    if (k < iters && token < len) {
+      id = a.table[int64_t(b) * a.stride + (token >> a.shift)];
+      if (id < 0 || id >= a.num_blocks) id = -1, flags |= kRowBadBlock;
+    }
+    return id;
+  };
+  int ids = load_ids(0), ids_next = load_ids(kPer);
+  const int64_t head_at = (int64_t(head) << a.shift) * a.dim;
+  int64_t off[S::kMT];
+  bool ok[S::kMT], full = false;
+  // keys (and scales) of tile k, then its values; both leave one group of copies
+  auto copy_tile = [&](const uint8_t* codes, uint32_t dst, int token0) {
+    if (full) {
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i)
-          copy16(dst + uint32_t(i * kRowsPerCopy * kDP) + lane_dst[i % kSwizzles],
-                 codes + off[i / kPerMT] + (i % kPerMT) * kRowsPerCopy * kDP + lane_src);
+      for (int i = 0; i < kCopies; ++i)
+        copy16(dst + uint32_t(i * kRowsPerCopy * kDP) + lane_dst[i % kSwizzles],
+               codes + off[i / kPerMT] + (i % kPerMT) * kRowsPerCopy * kDP + lane_src);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const int row = i * kRowsPerCopy + my_row;
+        if (my_chunk * 16 < a.dim)
+          copy16(dst + uint32_t(row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
+                 codes + off[i / kPerMT] + (row % 16) * a.dim + my_chunk * 16, ok[i / kPerMT] && token0 + row < len);
+      }
+    }
+  };
+  auto issue_keys = [&](int k) {
+    if (k < iters) {
+      const int at = k % kPer * S::kMT, token0 = (tile_lo + k) * S::kTile + warp * S::kMT * 16;
+      if (at == 0 && k > 0) {
+        ids = ids_next;
+        ids_next = load_ids(k + kPer);
+      }
+      full = token0 + S::kMT * 16 <= len && a.dim == kDP;
+#pragma unroll
+      for (int mt = 0; mt < S::kMT; ++mt) {
+        const int id = __shfl_sync(~0u, ids, at + mt);
+        ok[mt] = id >= 0;
+        full &= ok[mt];
+        off[mt] = int64_t(max(id, 0)) * block_bytes + head_at + ((token0 + 16 * mt) & ((1 << a.shift) - 1)) * a.dim;
+      }
+      const int id = __shfl_sync(~0u, ids, at + lane % S::kMT);
+      if (lane < 2 * S::kMT) {
+        copy4(smem_addr(&scales[warp][k % kMetaStages][lane / S::kMT][lane % S::kMT]),
+              (lane < S::kMT ? a.k_scale : a.v_scale) + int64_t(max(id, 0)) * a.kv_heads + head, id >= 0);
+        if (lane < S::kMT) valid[warp][k % kMetaStages][lane] = id >= 0;
+      }
+      copy_tile(a.k, keys + uint32_t(k % S::kDepth * S::kWarpK), token0);
+    }
+    copies_commit();
+  };
+  auto issue_values = [&](int k) {
+    if (k < iters)
+      copy_tile(a.v, base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage + warp * S::kWarpK),
+                (tile_lo + k) * S::kTile + warp * S::kMT * 16);
+    copies_commit();
+  };
+  for (int k = 0; k < S::kDepth - 1; ++k) {
+    issue_keys(k);
+    issue_values(k);
+  }
+
+  // ---- query fragments: lane (g, t) holds the 16-element chunks t + 4 h of row g of each 8 rows
+  uint32_t qreg[S::kQReg ? kNT : 1][S::kQReg ? S::kSteps * S::kParts * 2 : 1];
+  int see[kNT][2];                     // last visible position of columns 2t, 2t + 1
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    if (S::kQReg || nt % 2 == warp) {
+      const int row = nt * 8 + g;
+      const bool live = row < live_rows;
+      const int64_t gr = r0 + row;
+      const int64_t token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
+      const T* q = static_cast<const T*>(a.q) + (live ? token * a.q_stride + qh * a.dim : 0);
+      float x[S::kSteps][4];
+#pragma unroll
+      for (int h = 0; h < kDP / 64; ++h) {
+        const int d = (t + 4 * h) * 16;
+        Eight<T> e[2];
+        e[0].clear(), e[1].clear();
+        if (live && d < a.dim) {
+          if (a.q_vector) e[0].load(q + d), e[1].load(q + d + 8);
+          else e[0].load_any(q + d), e[1].load_any(q + d + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float y[8];
+          e[i].get(y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[h * 4 + i * 2 + j / 4][j % 4] = y[j];
+        }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[s][e]));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // up: the power of two that takes the largest element to [2^9, 2^10); its inverse goes into the row's factor
+      const int up_exp = min(max(263 - int(__float_as_uint(top) >> 23), 1), 253);
+      const float up = __uint_as_float(uint32_t(up_exp) << 23);
+      if (t == 0) row_factor[row] = __uint_as_float(uint32_t(254 - up_exp) << 23) * a.scale;
+      uint32_t f[S::kSteps * S::kParts * 2];                 // per step: two words, with kSplit the two rests
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[s][e] *= up;
+        uint32_t* const fs = f + s * S::kParts * 2;
+        fs[0] = pack_f16(x[s][0], x[s][1]);
+        fs[1] = pack_f16(x[s][2], x[s][3]);
+        if (kSplit) {
+          fs[S::kParts * 2 - 2] = rest_f16(fs[0], x[s][0], x[s][1]);
+          fs[S::kParts * 2 - 1] = rest_f16(fs[1], x[s][2], x[s][3]);
+        }
+      }
+      if (S::kQReg) {
+#pragma unroll
+        for (int i = 0; i < S::kSteps * S::kParts * 2; ++i) qreg[S::kQReg ? nt : 0][S::kQReg ? i : 0] = f[i];
       } else {
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          const int row = i * kRowsPerCopy + my_row;
-          if (my_chunk * 16 < a.dim)
-            copy16(dst + uint32_t(row * kDP + ((my_chunk ^ swizzle(row)) * 16)),
-                   codes + off[i / kPerMT] + (row % 16) * a.dim + my_chunk * 16, ok[i / kPerMT] && token0 + row < len);
-        }
+        for (int i = 0; i < S::kQ4; ++i)
+          *reinterpret_cast<uint4*>(smem + S::kQAt + ((nt * S::kQ4 + i) * 32 + lane) * 16) =
+              make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
       }
-    };
-    auto issue_keys = [&](int k) {
-      if (k < iters) {
-        const int at = k % kPer * S::kMT, token0 = (tile_lo + k) * S::kTile + warp * S::kMT * 16;
-        if (at == 0 && k > 0) {
-          ids = ids_next;
-          ids_next = load_ids(k + kPer);
-        }
-        full = token0 + S::kMT * 16 <= len && a.dim == kDP;
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nt * 8 + 2 * t + c;
+      see[nt][c] = r < live_rows ? len - n + int((r0 + r) / a.group) : len;     // unused rows: everything, unread
+    }
+  }
+  __syncthreads();
+  const uint32_t q_at = base + uint32_t(S::kQAt + lane * 16);
+  float factor[kNT][2];
+  float o[kNT][S::kDT][4];
+  float l[kNT][2], m[kNT][2];
+  uint32_t has_ref = 0;                        // rows (2 nt + c) whose reference is set; m = 0 before
+  constexpr uint32_t kAll = (1u << (2 * kNT)) - 1;
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      factor[nt][c] = row_factor[nt * 8 + 2 * t + c];
+      m[nt][c] = 0.0f, l[nt][c] = 0.0f;
+      if (nt * 8 + 2 * t + c >= live_rows) has_ref |= 1u << (2 * nt + c);       // unused: never awaited
+    }
+#pragma unroll
+    for (int d = 0; d < S::kDT; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.0f;
+  }
+
+  for (int k = 0; k < iters; ++k) {
+    const int token0 = (tile_lo + k) * S::kTile, meta = k % kMetaStages;
+    copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's keys of the tile
+    __syncwarp();
+    issue_keys(k + S::kDepth - 1);
+    const uint32_t kst = keys + uint32_t(k % S::kDepth * S::kWarpK), vst = base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage);
+
+    // ---- S^T = K Q^T for this warp's keys
+    float s[S::kMT][kNT][4];
+#pragma unroll
+    for (int mt = 0; mt < S::kMT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < kDP / 64; ++h) {
+      uint4 w[S::kMT][2], q_two[kNT];
+#pragma unroll
+      for (int mt = 0; mt < S::kMT; ++mt)
+#pragma unroll
+        for (int up = 0; up < 2; ++up)
+          w[mt][up] = lds128(kst + uint32_t((mt * 16 + up * 8 + g) * kDP + (((t + 4 * h) ^ swizzle(g)) * 16)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t f[S::kMT][4];
 #pragma unroll
         for (int mt = 0; mt < S::kMT; ++mt) {
-          const int id = __shfl_sync(~0u, ids, at + mt);
-          ok[mt] = id >= 0;
-          full &= ok[mt];
-          off[mt] = int64_t(max(id, 0)) * block_bytes + head_at + ((token0 + 16 * mt) & ((1 << a.shift) - 1)) * a.dim;
+          unpack4<kType>(reinterpret_cast<const uint32_t*>(&w[mt][0])[i], f[mt][0], f[mt][2]);
+          unpack4<kType>(reinterpret_cast<const uint32_t*>(&w[mt][1])[i], f[mt][1], f[mt][3]);
         }
-        const int id = __shfl_sync(~0u, ids, at + lane % S::kMT);
-        if (lane < 2 * S::kMT) {
-          copy4(smem_addr(&scales[warp][k % kMetaStages][lane / S::kMT][lane % S::kMT]),
-                (lane < S::kMT ? a.k_scale : a.v_scale) + int64_t(max(id, 0)) * a.kv_heads + head, id >= 0);
-          if (lane < S::kMT) valid[warp][k % kMetaStages][lane] = id >= 0;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          uint32_t q[S::kParts * 2];
+          if (S::kQReg) {
+#pragma unroll
+            for (int p = 0; p < S::kParts * 2; ++p)
+              q[p] = qreg[S::kQReg ? nt : 0][S::kQReg ? (h * 4 + i) * S::kParts * 2 + p : 0];
+          } else if (kSplit) {
+            const uint4 x = lds128(q_at + uint32_t(nt * S::kQ4 + h * 4 + i) * 512);
+            q[0] = x.x, q[1] = x.y, q[S::kParts * 2 - 2] = x.z, q[S::kParts * 2 - 1] = x.w;
+          } else {
+            if (i % 2 == 0) q_two[nt] = lds128(q_at + uint32_t(nt * S::kQ4 + (h * 4 + i) / 2) * 512);
+            q[0] = i % 2 ? q_two[nt].z : q_two[nt].x, q[1] = i % 2 ? q_two[nt].w : q_two[nt].y;
+          }
+#pragma unroll
+          for (int p = 0; p < S::kParts; ++p)
+#pragma unroll
+            for (int mt = 0; mt < S::kMT; ++mt) mma_f16(s[mt][nt], f[mt], q[2 * p], q[2 * p + 1]);
         }
-        copy_tile(a.k, keys + uint32_t(k % S::kDepth * S::kWarpK), token0);
       }
-      copies_commit();
+    }
+
+    // ---- exponents: s = S k f - m, hidden ones -inf
+    bool edge = token0 + S::kTile - 1 > p_first || (a.window > 0 && token0 <= p_last - a.window);
+    float v_scale[S::kMT];
+#pragma unroll
+    for (int mt = 0; mt < S::kMT; ++mt) {
+      const float ks = scales[warp][meta][0][mt];
+      v_scale[mt] = scales[warp][meta][1][mt];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const uint64_t c = mul2(pair(ks, ks), pair(factor[nt][0], factor[nt][1]));
+        const uint64_t less = pair(-m[nt][0], -m[nt][1]);
+        unpair(fma2(pair(s[mt][nt][0], s[mt][nt][1]), c, less), s[mt][nt][0], s[mt][nt][1]);
+        unpair(fma2(pair(s[mt][nt][2], s[mt][nt][3]), c, less), s[mt][nt][2], s[mt][nt][3]);
+      }
+    }
+    // whether a row sees token `of` of the tile's row tile mt (of both warps'), element e
+    auto visible = [&](int mt, int nt, int e) {
+      const int j = token0 + mt * 16 + g + (e / 2) * 8, p = see[nt][e % 2];
+      return j <= p && (a.window == 0 || j > p - a.window) && valid[mt / S::kMT][meta][mt % S::kMT];
     };
-    auto issue_values = [&](int k) {
-      if (k < iters)
-        copy_tile(a.v, base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage + warp * S::kWarpK),
-                  (tile_lo + k) * S::kTile + warp * S::kMT * 16);
-      copies_commit();
-    };
-    for (int k = 0; k < S::kDepth - 1; ++k) {
-      issue_keys(k);
-      issue_values(k);
-    }
-
-    // ---- query fragments: lane (g, t) holds the 16-element chunks t + 4 h of row g of each 8 rows
-    uint32_t qreg[S::kQReg ? kNT : 1][S::kQReg ? S::kSteps * S::kParts * 2 : 1];
-    int see[kNT][2];                     // last visible position of columns 2t, 2t + 1
+    bool mine = edge;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      if (S::kQReg || nt % 2 == warp) {
-        const int row = nt * 8 + g;
-        const bool live = row < live_rows;
-        const int64_t gr = r0 + row;
-        const int64_t token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
-        const T* q = static_cast<const T*>(a.q) + (live ? token * a.q_stride + qh * a.dim : 0);
-        float x[S::kSteps][4];
-#pragma unroll
-        for (int h = 0; h < kDP / 64; ++h) {
-          const int d = (t + 4 * h) * 16;
-          Eight<T> e[2];
-          e[0].clear(), e[1].clear();
-          if (live && d < a.dim) {
-            if (a.q_vector) e[0].load(q + d), e[1].load(q + d + 8);
-            else e[0].load_any(q + d), e[1].load_any(q + d + 8);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float y[8];
-            e[i].get(y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[h * 4 + i * 2 + j / 4][j % 4] = y[j];
-          }
-        }
-        float top = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S::kSteps; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[s][e]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        // up: the power of two that takes the largest element to [2^9, 2^10); its inverse goes into the row's factor
-        const int up_exp = min(max(263 - int(__float_as_uint(top) >> 23), 1), 253);
-        const float up = __uint_as_float(uint32_t(up_exp) << 23);
-        if (t == 0) row_factor[row] = __uint_as_float(uint32_t(254 - up_exp) << 23) * a.scale;
-        uint32_t f[S::kSteps * S::kParts * 2];                 // per step: two words, with kSplit the two rests
-#pragma unroll
-        for (int s = 0; s < S::kSteps; ++s) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[s][e] *= up;
-          uint32_t* const fs = f + s * S::kParts * 2;
-          fs[0] = pack_f16(x[s][0], x[s][1]);
-          fs[1] = pack_f16(x[s][2], x[s][3]);
-          if (kSplit) {
-            fs[S::kParts * 2 - 2] = rest_f16(fs[0], x[s][0], x[s][1]);
-            fs[S::kParts * 2 - 1] = rest_f16(fs[1], x[s][2], x[s][3]);
-          }
-        }
-        if (S::kQReg) {
-#pragma unroll
-          for (int i = 0; i < S::kSteps * S::kParts * 2; ++i) qreg[S::kQReg ? nt : 0][S::kQReg ? i : 0] = f[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < S::kQ4; ++i)
-            *reinterpret_cast<uint4*>(smem + S::kQAt + ((nt * S::kQ4 + i) * 32 + lane) * 16) =
-                make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * t + c;
-        see[nt][c] = r < live_rows ? len - n + int((r0 + r) / a.group) : len;     // unused rows: everything, unread
-      }
-    }
-    __syncthreads();
-    const uint32_t q_at = base + uint32_t(S::kQAt + lane * 16);
-    float factor[kNT][2];
-    float o[kNT][S::kDT][4];
-    float l[kNT][2], m[kNT][2];
-    uint32_t has_ref = 0;                        // rows (2 nt + c) whose reference is set; m = 0 before
-    constexpr uint32_t kAll = (1u << (2 * kNT)) - 1;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        factor[nt][c] = row_factor[nt * 8 + 2 * t + c];
-        m[nt][c] = 0.0f, l[nt][c] = 0.0f;
-        if (nt * 8 + 2 * t + c >= live_rows) has_ref |= 1u << (2 * nt + c);       // unused: never awaited
-      }
-#pragma unroll
-      for (int d = 0; d < S::kDT; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.0f;
-    }
-
-    for (int k = 0; k < iters; ++k) {
-      const int token0 = (tile_lo + k) * S::kTile, meta = k % kMetaStages;
-      copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's keys of the tile
-      __syncwarp();
-      issue_keys(k + S::kDepth - 1);
-      const uint32_t kst = keys + uint32_t(k % S::kDepth * S::kWarpK), vst = base + uint32_t(S::kVAt + k % S::kDepth * S::kVStage);
-
-      // ---- S^T = K Q^T for this warp's keys
-      float s[S::kMT][kNT][4];
+    for (int mt = 0; mt < S::kMT; ++mt) mine |= !valid[warp][meta][mt];
+    if (mine) {
 #pragma unroll
       for (int mt = 0; mt < S::kMT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
-#pragma unroll
-      for (int h = 0; h < kDP / 64; ++h) {
-        uint4 w[S::kMT][2], q_two[kNT];
-#pragma unroll
-        for (int mt = 0; mt < S::kMT; ++mt)
-#pragma unroll
-          for (int up = 0; up < 2; ++up)
-            w[mt][up] = lds128(kst + uint32_t((mt * 16 + up * 8 + g) * kDP + (((t + 4 * h) ^ swizzle(g)) * 16)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t f[S::kMT][4];
-#pragma unroll
-          for (int mt = 0; mt < S::kMT; ++mt) {
-            unpack4<kType>(reinterpret_cast<const uint32_t*>(&w[mt][0])[i], f[mt][0], f[mt][2]);
-            unpack4<kType>(reinterpret_cast<const uint32_t*>(&w[mt][1])[i], f[mt][1], f[mt][3]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            uint32_t q[S::kParts * 2];
-            if (S::kQReg) {
-#pragma unroll
-              for (int p = 0; p < S::kParts * 2; ++p)
-                q[p] = qreg[S::kQReg ? nt : 0][S::kQReg ? (h * 4 + i) * S::kParts * 2 + p : 0];
-            } else if (kSplit) {
-              const uint4 x = lds128(q_at + uint32_t(nt * S::kQ4 + h * 4 + i) * 512);
-              q[0] = x.x, q[1] = x.y, q[S::kParts * 2 - 2] = x.z, q[S::kParts * 2 - 1] = x.w;
-            } else {
-              if (i % 2 == 0) q_two[nt] = lds128(q_at + uint32_t(nt * S::kQ4 + (h * 4 + i) / 2) * 512);
-              q[0] = i % 2 ? q_two[nt].z : q_two[nt].x, q[1] = i % 2 ? q_two[nt].w : q_two[nt].y;
-            }
-#pragma unroll
-            for (int p = 0; p < S::kParts; ++p)
-#pragma unroll
-              for (int mt = 0; mt < S::kMT; ++mt) mma_f16(s[mt][nt], f[mt], q[2 * p], q[2 * p + 1]);
-          }
-        }
-      }
+          for (int e = 0; e < 4; ++e)
+            if (!visible(warp * S::kMT + mt, nt, e)) s[mt][nt][e] = -INFINITY;
+    }
 
-      // ---- exponents: s = S k f - m, hidden ones -inf
-      bool edge = token0 + S::kTile - 1 > p_first || (a.window > 0 && token0 <= p_last - a.window);
-      float v_scale[S::kMT];
+    // ---- weights P v as 16-bit floats, transposed into the right operand of V^T P^T, for both warps
+    uint32_t packed_max = 0;
+    float sum[kNT][2];
+    const uint32_t p_at = base + uint32_t(S::kPAt + (k & 1) * S::kPStage + lane * 8 * S::kParts);
+    auto weigh = [&] {
+      packed_max = 0;
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt) {
-        const float ks = scales[warp][meta][0][mt];
-        v_scale[mt] = scales[warp][meta][1][mt];
+      for (int nt = 0; nt < kNT; ++nt) {
+        uint64_t all = pair(0.0f, 0.0f);
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const uint64_t c = mul2(pair(ks, ks), pair(factor[nt][0], factor[nt][1]));
-          const uint64_t less = pair(-m[nt][0], -m[nt][1]);
-          unpair(fma2(pair(s[mt][nt][0], s[mt][nt][1]), c, less), s[mt][nt][0], s[mt][nt][1]);
-          unpair(fma2(pair(s[mt][nt][2], s[mt][nt][3]), c, less), s[mt][nt][2], s[mt][nt][3]);
-        }
-      }
-      // whether a row sees token `of` of the tile's row tile mt (of both warps'), element e
-      auto visible = [&](int mt, int nt, int e) {
-        const int j = token0 + mt * 16 + g + (e / 2) * 8, p = see[nt][e % 2];
-        return j <= p && (a.window == 0 || j > p - a.window) && valid[mt / S::kMT][meta][mt % S::kMT];
-      };
-      bool mine = edge;
+        for (int mt = 0; mt < S::kMT; ++mt) {
+          const uint64_t vv = pair(v_scale[mt], v_scale[mt]);
+          uint32_t f[S::kParts][2];
 #pragma unroll
-      for (int mt = 0; mt < S::kMT; ++mt) mine |= !valid[warp][meta][mt];
-      if (mine) {
-#pragma unroll
-        for (int mt = 0; mt < S::kMT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!visible(warp * S::kMT + mt, nt, e)) s[mt][nt][e] = -INFINITY;
-      }
-
-      // ---- weights P v as 16-bit floats, transposed into the right operand of V^T P^T, for both warps
-      uint32_t packed_max = 0;
-      float sum[kNT][2];
-      const uint32_t p_at = base + uint32_t(S::kPAt + (k & 1) * S::kPStage + lane * 8 * S::kParts);
-      auto weigh = [&] {
-        packed_max = 0;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          uint64_t all = pair(0.0f, 0.0f);
-#pragma unroll
-          for (int mt = 0; mt < S::kMT; ++mt) {
-            const uint64_t vv = pair(v_scale[mt], v_scale[mt]);
-            uint32_t f[S::kParts][2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint64_t p = pair(exp2_approx(s[mt][nt][half * 2]), exp2_approx(s[mt][nt][half * 2 + 1]));
-              all = add2(all, p);
-              float w0, w1;
-              unpair(mul2(p, vv), w0, w1);
-              const uint32_t hi = pack_f16(w0, w1);
-              packed_max = max_f16x2(packed_max, hi);
-              f[0][half] = transpose8(hi);
-              if (kSplit) f[S::kParts - 1][half] = transpose8(rest_f16(hi, w0, w1));
-            }
-            const uint32_t at = p_at + uint32_t(((warp * S::kMT + mt) * kNT + nt) * S::kParts * 256);
-            if (kSplit)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]),
-                           "r"(f[S::kParts - 1][0]), "r"(f[S::kParts - 1][1])
-                           : "memory");
-            else
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]) : "memory");
+          for (int half = 0; half < 2; ++half) {
+            const uint64_t p = pair(exp2_approx(s[mt][nt][half * 2]), exp2_approx(s[mt][nt][half * 2 + 1]));
+            all = add2(all, p);
+            float w0, w1;
+            unpair(mul2(p, vv), w0, w1);
+            const uint32_t hi = pack_f16(w0, w1);
+            packed_max = max_f16x2(packed_max, hi);
+            f[0][half] = transpose8(hi);
+            if (kSplit) f[S::kParts - 1][half] = transpose8(rest_f16(hi, w0, w1));
           }
-          unpair(all, sum[nt][0], sum[nt][1]);
+          const uint32_t at = p_at + uint32_t(((warp * S::kMT + mt) * kNT + nt) * S::kParts * 256);
+          if (kSplit)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]),
+                         "r"(f[S::kParts - 1][0]), "r"(f[S::kParts - 1][1])
+                         : "memory");
+          else
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f[0][0]), "r"(f[0][1]) : "memory");
         }
-      };
+        unpair(all, sum[nt][0], sum[nt][1]);
+      }
+    };
+    weigh();
+    copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's values of the tile
+    const bool past = (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || has_ref != kAll;
+    if (__syncthreads_or(past)) {
+      // rare: the rows' largest weights over both warps' keys, and new references where they pass the limit
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float y = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < S::kMT; ++mt)
+            y = fmaxf(y, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) + fmaxf(__log2f(v_scale[mt]), kLeastScale));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
+          if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = y;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float alpha[2] = {1.0f, 1.0f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float y = fmaxf(row_part[0][nt * 8 + 2 * t + c], row_part[1][nt * 8 + 2 * t + c]);
+          const uint32_t bit = 1u << (2 * nt + c);
+          if ((has_ref & bit) ? y > kMostWeight : y > -INFINITY) {
+            const float up = y - kTopWeight;
+            if (has_ref & bit) alpha[c] = exp2_approx(-up);
+            has_ref |= bit;
+            m[nt][c] += up;
+            l[nt][c] *= alpha[c];
+#pragma unroll
+            for (int mt = 0; mt < S::kMT; ++mt) s[mt][nt][c] -= up, s[mt][nt][c + 2] -= up;
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < S::kDT; ++d) {
+          o[nt][d][0] *= alpha[0], o[nt][d][1] *= alpha[1], o[nt][d][2] *= alpha[0], o[nt][d][3] *= alpha[1];
+        }
+      }
       weigh();
-      copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's values of the tile
-      const bool past = (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || has_ref != kAll;
-      if (__syncthreads_or(past)) {
-        // rare: the rows' largest weights over both warps' keys, and new references where they pass the limit
+      __syncthreads();
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
+    issue_values(k + S::kDepth - 1);
+
+    // ---- O^T += V^T P^T for this warp's half of the head: lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 of 16; row g
+    // of row tile d is element kDP / 16 g + 2 d of the half, row g + 8 the next one
+    constexpr int kWords = kDP / 64;           // 4-byte words of a lane's elements
+    auto values = [&](int mt, uint32_t (&w)[4][4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * t + (i & 1) + (i / 2) * 8;
+        const uint32_t row = vst + uint32_t((mt * 16 + r) * kDP);
+        if (kDP == 64) {
+          w[i][0] = lds32(row + uint32_t((((warp * 2 + (g >> 2)) ^ swizzle(r)) * 16) + (g & 3) * 4));
+        } else if (kDP == 128) {
+          const uint2 x = lds64(row + uint32_t((((warp * 4 + (g >> 1)) ^ swizzle(r)) * 16) + (g & 1) * 8));
+          w[i][0] = x.x, w[i][1] = x.y;
+        } else {
+          const uint4 x = lds128(row + uint32_t(((warp * 8 + g) ^ swizzle(r)) * 16));
+          w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+        }
+      }
+    };
+    bool nan = false;
+    if (kType == SMP_CACHE_E4M3) {
+#pragma unroll
+      for (int mt = 0; mt < 2 * S::kMT; ++mt) edge |= !valid[mt / S::kMT][meta][mt % S::kMT];
+      if (edge) {
+        // a NaN code times a weight of 0 would reach rows that do not see its token
+#pragma unroll
+        for (int mt = 0; mt < 2 * S::kMT; ++mt) {
+          uint32_t w[4][4];
+          values(mt, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) nan |= __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+        }
+        nan = __any_sync(~0u, nan);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2 * S::kMT; ++mt) {
+      uint32_t w[4][4], pf[kNT][S::kParts][2];
+      values(mt, w);
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        const uint32_t at = p_at + uint32_t((mt * kNT + nt) * S::kParts * 256);
+        if (kSplit) {
+          const uint4 x = lds128(at);
+          pf[nt][0][0] = x.x, pf[nt][0][1] = x.y, pf[nt][S::kParts - 1][0] = x.z, pf[nt][S::kParts - 1][1] = x.w;
+        } else {
+          const uint2 x = lds64(at);
+          pf[nt][0][0] = x.x, pf[nt][0][1] = x.y;
+        }
+      }
+      if (kType == SMP_CACHE_E4M3 && nan) {
+        // NaN codes become 0 for the product; a row that sees one gets NaN from a count of them
+        uint32_t seen[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float y = -INFINITY;
+          for (int half = 0; half < 2; ++half)
+            seen[nt][half] = transpose8(
+                pack_f16(visible(mt, nt, half * 2) ? 1.0f : 0.0f, visible(mt, nt, half * 2 + 1) ? 1.0f : 0.0f));
 #pragma unroll
-            for (int mt = 0; mt < S::kMT; ++mt)
-              y = fmaxf(y, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) + fmaxf(__log2f(v_scale[mt]), kLeastScale));
+        for (int j = 0; j < kWords; ++j) {
+          uint32_t z[4];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
-            if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = y;
+          for (int i = 0; i < 4; ++i) {
+            z[i] = __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            w[i][j] &= ~z[i];
+            z[i] &= 0x38383838u;                               // the code of 1
           }
-        __syncthreads();
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          float alpha[2] = {1.0f, 1.0f};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float y = fmaxf(row_part[0][nt * 8 + 2 * t + c], row_part[1][nt * 8 + 2 * t + c]);
-            const uint32_t bit = 1u << (2 * nt + c);
-            if ((has_ref & bit) ? y > kMostWeight : y > -INFINITY) {
-              const float up = y - kTopWeight;
-              if (has_ref & bit) alpha[c] = exp2_approx(-up);
-              has_ref |= bit;
-              m[nt][c] += up;
-              l[nt][c] *= alpha[c];
-#pragma unroll
-              for (int mt = 0; mt < S::kMT; ++mt) s[mt][nt][c] -= up, s[mt][nt][c + 2] -= up;
-            }
-          }
-#pragma unroll
-          for (int d = 0; d < S::kDT; ++d) {
-            o[nt][d][0] *= alpha[0], o[nt][d][1] *= alpha[1], o[nt][d][2] *= alpha[0], o[nt][d][3] *= alpha[1];
-          }
-        }
-        weigh();
-        __syncthreads();
-      }
-#pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) l[nt][0] += sum[nt][0], l[nt][1] += sum[nt][1];
-      issue_values(k + S::kDepth - 1);
-
-      // ---- O^T += V^T P^T for this warp's half of the head: lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 of 16; row g
-      // of row tile d is element kDP / 16 g + 2 d of the half, row g + 8 the next one
-      constexpr int kWords = kDP / 64;           // 4-byte words of a lane's elements
-      auto values = [&](int mt, uint32_t (&w)[4][4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 2 * t + (i & 1) + (i / 2) * 8;
-          const uint32_t row = vst + uint32_t((mt * 16 + r) * kDP);
-          if (kDP == 64) {
-            w[i][0] = lds32(row + uint32_t((((warp * 2 + (g >> 2)) ^ swizzle(r)) * 16) + (g & 3) * 4));
-          } else if (kDP == 128) {
-            const uint2 x = lds64(row + uint32_t((((warp * 4 + (g >> 1)) ^ swizzle(r)) * 16) + (g & 1) * 8));
-            w[i][0] = x.x, w[i][1] = x.y;
-          } else {
-            const uint4 x = lds128(row + uint32_t(((warp * 8 + g) ^ swizzle(r)) * 16));
-            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-          }
-        }
-      };
-      bool nan = false;
-      if (kType == SMP_CACHE_E4M3) {
-#pragma unroll
-        for (int mt = 0; mt < 2 * S::kMT; ++mt) edge |= !valid[mt / S::kMT][meta][mt % S::kMT];
-        if (edge) {
-          // a NaN code times a weight of 0 would reach rows that do not see its token
-#pragma unroll
-          for (int mt = 0; mt < 2 * S::kMT; ++mt) {
-            uint32_t w[4][4];
-            values(mt, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < kWords; ++j) nan |= __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
-          }
-          nan = __any_sync(~0u, nan);
-        }
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2 * S::kMT; ++mt) {
-        uint32_t w[4][4], pf[kNT][S::kParts][2];
-        values(mt, w);
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const uint32_t at = p_at + uint32_t((mt * kNT + nt) * S::kParts * 256);
-          if (kSplit) {
-            const uint4 x = lds128(at);
-            pf[nt][0][0] = x.x, pf[nt][0][1] = x.y, pf[nt][S::kParts - 1][0] = x.z, pf[nt][S::kParts - 1][1] = x.w;
-          } else {
-            const uint2 x = lds64(at);
-            pf[nt][0][0] = x.x, pf[nt][0][1] = x.y;
-          }
-        }
-        if (kType == SMP_CACHE_E4M3 && nan) {
-          // NaN codes become 0 for the product; a row that sees one gets NaN from a count of them
-          uint32_t seen[kNT][2];
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              seen[nt][half] = transpose8(
-                  pack_f16(visible(mt, nt, half * 2) ? 1.0f : 0.0f, visible(mt, nt, half * 2 + 1) ? 1.0f : 0.0f));
-#pragma unroll
-          for (int j = 0; j < kWords; ++j) {
-            uint32_t z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              z[i] = __vcmpeq4(w[i][j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              w[i][j] &= ~z[i];
-              z[i] &= 0x38383838u;                               // the code of 1
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t f[4];
-              unpack4<kType>(__byte_perm(z[0], z[1], half ? 0x7362 : 0x5140), f[0], f[1]);
-              unpack4<kType>(__byte_perm(z[2], z[3], half ? 0x7362 : 0x5140), f[2], f[3]);
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) {
-                float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16(count, f, seen[nt][0], seen[nt][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (count[e] > 0.0f) o[nt][2 * j + half][e] = __int_as_float(0x7FC00000);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kWords; ++j)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t f[4];
-            unpack4<kType>(__byte_perm(w[0][j], w[1][j], half ? 0x7362 : 0x5140), f[0], f[1]);
-            unpack4<kType>(__byte_perm(w[2][j], w[3][j], half ? 0x7362 : 0x5140), f[2], f[3]);
+            unpack4<kType>(__byte_perm(z[0], z[1], half ? 0x7362 : 0x5140), f[0], f[1]);
+            unpack4<kType>(__byte_perm(z[2], z[3], half ? 0x7362 : 0x5140), f[2], f[3]);
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt) {
+              float count[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_f16(count, f, seen[nt][0], seen[nt][1]);
 #pragma unroll
-              for (int p = 0; p < S::kParts; ++p) mma_f16(o[nt][2 * j + half], f, pf[nt][p][0], pf[nt][p][1]);
-          }
-      }
-    }
-    copies_wait<0>();
-
-    // ---- l over all keys; O needs no joining: a warp has its half of the head
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], d);
-        if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = l[nt][c];
-      }
-    __syncthreads();                             // and both warps are done with the rings
-    float* const part = a.partial + (int64_t(blockIdx.x) * 2 + (seg.first ? 1 : 0)) * S::kRows * (kDP + 2);
-    constexpr int kMine = kDP / 16;              // a lane's consecutive elements of a row
-    const int d0 = warp * (kDP / 2) + g * kMine;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = nt * 8 + 2 * t + c;
-        if (r >= live_rows) continue;
-        const float all = row_part[0][r] + row_part[1][r];
-        const float ref = has_ref >> (2 * nt + c) & 1 ? m[nt][c] : -INFINITY;     // -inf: nothing was seen (or only NaN)
-        const int64_t gr = r0 + r, token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
-        const float inv = !seg.whole ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
-        float y[kMine];
-#pragma unroll
-        for (int d = 0; d < S::kDT; ++d) y[2 * d] = o[nt][d][c] * inv, y[2 * d + 1] = o[nt][d][c + 2] * inv;
-        if (!seg.whole) {
-#pragma unroll
-          for (int i = 0; i < kMine; i += 4)
-            *reinterpret_cast<float4*>(part + r * kDP + d0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-        } else if (d0 < a.dim) {
-          T* const out = static_cast<T*>(a.out) + token * a.out_stride + qh * a.dim + d0;
-#pragma unroll
-          for (int i = 0; i < kMine; i += 4) {
-            const float z[4] = {y[i], y[i + 1], y[i + 2], y[i + 3]};
-            if (a.out_vector) {
-              store4(out + i, z);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) store1(out + i + e, z[e]);
+              for (int e = 0; e < 4; ++e)
+                if (count[e] > 0.0f) o[nt][2 * j + half][e] = __int_as_float(0x7FC00000);
             }
           }
         }
-        if (warp == 0 && g == 0) {
-          if (!seg.whole) {
-            part[S::kRows * kDP + r] = ref;
-            part[S::kRows * kDP + S::kRows + r] = all;
-          } else if (a.lse) {
-            a.lse[token * a.q_heads + qh] = all == 0.0f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+      }
+#pragma unroll
+      for (int j = 0; j < kWords; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t f[4];
+          unpack4<kType>(__byte_perm(w[0][j], w[1][j], half ? 0x7362 : 0x5140), f[0], f[1]);
+          unpack4<kType>(__byte_perm(w[2][j], w[3][j], half ? 0x7362 : 0x5140), f[2], f[3]);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int p = 0; p < S::kParts; ++p) mma_f16(o[nt][2 * j + half], f, pf[nt][p][0], pf[nt][p][1]);
+        }
+    }
+  }
+  copies_wait<0>();
+
+  // ---- l over all keys; O needs no joining: a warp has its half of the head
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], d);
+      if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = l[nt][c];
+    }
+  __syncthreads();                             // and both warps are done with the rings
+  float* const part = a.partial + (int64_t(blockIdx.x) * 2 + (seg.first ? 1 : 0)) * (8 * kMaxNT) * (kDP + 2);
+  constexpr int kMine = kDP / 16;              // a lane's consecutive elements of a row
+  const int d0 = warp * (kDP / 2) + g * kMine;
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nt * 8 + 2 * t + c;
+      if (r >= live_rows) continue;
+      const float all = row_part[0][r] + row_part[1][r];
+      const float ref = has_ref >> (2 * nt + c) & 1 ? m[nt][c] : -INFINITY;     // -inf: nothing was seen (or only NaN)
+      const int64_t gr = r0 + r, token = req.first + gr / a.group, qh = int64_t(head) * a.group + gr % a.group;
+      const float inv = !seg.whole ? 1.0f : all == 0.0f ? 0.0f : 1.0f / all;
+      float y[kMine];
+#pragma unroll
+      for (int d = 0; d < S::kDT; ++d) y[2 * d] = o[nt][d][c] * inv, y[2 * d + 1] = o[nt][d][c + 2] * inv;
+      if (!seg.whole) {
+#pragma unroll
+        for (int i = 0; i < kMine; i += 4)
+          *reinterpret_cast<float4*>(part + r * kDP + d0 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+      } else if (d0 < a.dim) {
+        T* const out = static_cast<T*>(a.out) + token * a.out_stride + qh * a.dim + d0;
+#pragma unroll
+        for (int i = 0; i < kMine; i += 4) {
+          const float z[4] = {y[i], y[i + 1], y[i + 2], y[i + 3]};
+          if (a.out_vector) {
+            store4(out + i, z);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store1(out + i + e, z[e]);
           }
         }
       }
-    if (!seg.whole && seg.first && tid == 0) a.joins[blockIdx.x] = make_int4(b, line.rt, head, line.parts());
+      if (warp == 0 && g == 0) {
+        if (!seg.whole) {
+          part[8 * kMaxNT * kDP + r] = ref;
+          part[8 * kMaxNT * (kDP + 1) + r] = all;
+        } else if (a.lse) {
+          a.lse[token * a.q_heads + qh] = all == 0.0f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+        }
+      }
+    }
+}
+
+template <int kDP, int kMaxNT, int kType, bool kSplit>
+__global__ void __launch_bounds__(kAttnThreads, (AttnKernel<kDP, kMaxNT, kSplit>::kCtas)) attention_kernel(const AttnArgs a) {
+  using S = AttnShape<kDP, kMaxNT, kSplit>;
+  using Line = AttnLine<kAttnThreads, S::kTile, kMaxNT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ typename Line::Shared line_shared;
+  __shared__ AttnShared<S::kMT, S::kRows> sh;
+  __shared__ Line line_at;
+  const int tid = int(threadIdx.x);
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  int flags = 0;
+  {
+    Line line;
+    const bool work = line.begin(a, line_shared, flags);
+    if (blockIdx.x != 0) flags = 0;            // one CTA reports the lengths
+    if (!work) {
+      if (flags && a.status) atomicOr(a.status, flags);
+      return;
+    }
+    if (tid == 0) line_at = line;              // kept in shared memory: the segments need the registers
+  }
+  // chunks past the head's end are never written: they stay zero
+  if (a.dim < kDP)
+    for (int i = tid; i < S::kQAt / 16; i += kAttnThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int nt = line_at.nt;
+  for (bool more = true; more;) {
+    {
+      const AttnSegment seg = line_at.segment(a);
+      const AttnRequest req = line_at.req;
+      const int b = line_at.b, head = line_at.head;
+      auto run = [&](auto size) {
+        attention_segment<kDP, decltype(size)::value, kMaxNT, kType, kSplit>(a, seg, req, b, head, smem, sh, flags);
+      };
+      using std::integral_constant;
+      if (nt == 1) run(integral_constant<int, 1>());
+      else if (kMaxNT == 2 || nt == 2) run(integral_constant<int, 2>());
+      else if (nt == 3) run(integral_constant<int, kMaxNT < 3 ? kMaxNT : 3>());
+      else if (kMaxNT == 4 || nt == 4) run(integral_constant<int, kMaxNT < 4 ? kMaxNT : 4>());
+      else run(integral_constant<int, kMaxNT>());
+    }
+    Line line = line_at;
+    if (line.pos == 0 && line.end - line.at < line.cost && tid == 0)       // begun here, and cut
+      a.joins[blockIdx.x] = make_int4(line.b, line.rt, line.head, line.parts() | nt << 24);
     more = line.next(a);
-    __syncthreads();                             // row_part and row_factor have been read
+    __syncthreads();                           // everyone has read the line and the shared exchanges
+    if (tid == 0) line_at = line;
+    __syncthreads();
   }
   if (flags && a.status) atomicOr(a.status, flags);
 }
@@ -937,12 +1002,14 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, c
   using T = typename std::conditional<kSplit, float, uint16_t>::type;
   allow_dependent_launch();
   grid_dependency_wait();
-  const int4 u = a.joins[blockIdx.x];
+  int4 u = a.joins[blockIdx.x];
+  const int tile_rows = (u.w >> 24) * 8;
+  u.w &= 0xFFFFFF;
   if (u.w < 2) return;
   const AttnRequest req = attn_request(a, u.x);
   const int r = int(blockIdx.y) * 8 + (int(threadIdx.x) >> 5), lane = int(threadIdx.x) & 31;
-  const int64_t gr = int64_t(u.y) * rows + r;
-  if (r >= rows || gr >= int64_t(req.n) * a.group) return;
+  const int64_t gr = int64_t(u.y) * tile_rows + r;
+  if (r >= tile_rows || gr >= int64_t(req.n) * a.group) return;
   const int64_t slot = int64_t(rows) * (kDP + 2);
   auto part = [&](int i) { return a.partial + (int64_t(blockIdx.x + i) * 2 + (i == 0)) * slot; };
   float top = -INFINITY, all = 0.0f;
@@ -984,13 +1051,13 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, c
 
 // ---------------------------------------------------------------- launch
 
-template <int kDP, int kNT, int kType, bool kSplit>
+template <int kDP, int kMaxNT, int kType, bool kSplit>
 cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
-  using S = AttnShape<kDP, kNT, kSplit>;
+  using K = AttnKernel<kDP, kMaxNT, kSplit>;
   LaunchShape ls;
-  ls.smem = size_t(S::kSmem);
-  const int grid = device_sms(dev) * S::kCtas;         // one wave
-  cudaError_t err = prepare_kernel(reinterpret_cast<const void*>(&attention_kernel<kDP, kNT, kType, kSplit>), dev, ls);
+  ls.smem = size_t(K::kSmem);
+  const int grid = device_sms(dev) * K::kCtas;         // one wave
+  cudaError_t err = prepare_kernel(reinterpret_cast<const void*>(&attention_kernel<kDP, kMaxNT, kType, kSplit>), dev, ls);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
@@ -1002,31 +1069,22 @@ cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kNT, kType, kSplit>, a);
+  err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kMaxNT, kType, kSplit>, a);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3(unsigned(grid), unsigned(S::kRows / 8));
+  cfg.gridDim = dim3(unsigned(grid), unsigned(kMaxNT));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, S::kRows);
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, K::kRows);
 }
 
-// The smallest row tile that holds `rows` rows of a key head, up to what the
-// registers hold; more rows take several tiles, which read the keys again.
+// Two kernels per head size: row tiles of up to 16 rows, whose smaller state
+// leaves room for five CTAs per SM, and of up to 40 (32 for heads of 256 and
+// binary32 queries), beyond which the registers spill.  `rows` is what the
+// host expects of most requests; the kernel sees the longest itself.
 template <int kType, bool kSplit, int kDP>
 cudaError_t attn_launch_dim(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {
-  if (rows <= 8) return attn_launch_shape<kDP, 1, kType, kSplit>(a, dev, st);
   if (rows <= 16) return attn_launch_shape<kDP, 2, kType, kSplit>(a, dev, st);
-  if constexpr (kSplit || kDP == 256) {
-    return attn_launch_shape<kDP, 4, kType, kSplit>(a, dev, st);
-  } else {
-    // several tiles: the fewest, and then the smallest that are as few
-    const int64_t tiles = (rows + 63) / 64, each = (rows + tiles - 1) / tiles;
-    if (each <= 24) return attn_launch_shape<kDP, 3, kType, kSplit>(a, dev, st);
-    if (each <= 32) return attn_launch_shape<kDP, 4, kType, kSplit>(a, dev, st);
-    if (each <= 40) return attn_launch_shape<kDP, 5, kType, kSplit>(a, dev, st);
-    if (each <= 48) return attn_launch_shape<kDP, 6, kType, kSplit>(a, dev, st);
-    return attn_launch_shape<kDP, 8, kType, kSplit>(a, dev, st);
-  }
+  return attn_launch_shape<kDP, kSplit || kDP == 256 ? 4 : 5, kType, kSplit>(a, dev, st);
 }
 
 // One translation unit per cache and query type defines its own.
