@@ -21,7 +21,7 @@ extern "C" size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_
   // per main CTA: one join record and two parts, each the most rows of a unit with their sums and (m, l)
   const size_t padded = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   const size_t rows = padded == 256 ? 32 : 40;
-  return ctas * (16 + 2 * rows * (padded + 2) * 4);
+  return ctas * (sizeof(smp::AttnJoin) + 2 * rows * (padded + 2) * 4);
 }
 
 extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q, int32_t tokens, int32_t q_heads,
@@ -64,11 +64,11 @@ extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q,
   a.start = start, a.lens = lens, a.batch = batch, a.table = block_table, a.stride = table_stride;
   a.scale = scale * 1.4426950408889634f, a.window = window;
   a.out = out, a.out_stride = out_stride, a.lse = out_lse, a.status = status;
-  a.joins = static_cast<int4*>(workspace);
+  a.joins = static_cast<AttnJoin*>(workspace);
   a.partial = reinterpret_cast<float*>(a.joins + device_sms(dev) * kAttnMaxCtas);
   a.q_vector = !misaligned(q, 16) && q_stride * int64_t(elem) % 16 == 0;
   a.out_vector = !misaligned(out, 4 * elem) && out_stride % 4 == 0;
-  a.min_share = 6;
+  a.min_share = 4;      // one request of 1 K keys: 14.5 us, 16.5 with 6
   // a little over the average request: ragged steps have most requests near their longest
   const int64_t rows = (int64_t(tokens) * a.group * 5 / 4 + batch - 1) / batch;
   const bool e4m3 = cache->type == SMP_CACHE_E4M3, split = dtype == SMP_F32;

@@ -26,12 +26,17 @@
 // another CTA.  A CTA is two warps.  Each takes half of a tile's keys for
 // S and P and half of the head for O, over all rows: every code is converted
 // once, and O, the largest thing in registers, is halved, so that a warp can
-// hold up to 64 rows.  P passes through shared memory, one barrier per tile.
+// hold 40 rows.  P passes through shared memory, one barrier per tile.
 // K and V stream through rings in shared memory by 16-byte asynchronous
 // copies, a tile ahead.
 //
-// Bound: HBM (one byte per code) up to about 40 rows per key head, then the
-// instructions for conversions and softmax.
+// Bound: HBM (one byte per code) for up to 8 rows per key head, then issue: the
+// conversions of codes, the softmax and the 8-wide products, whose rate is a
+// third of what the widest ones reach.  Measured on heads of 128 in e4m3, with
+// requests from a quarter of the longest up: 4 requests of up to 128 K keys,
+// int8, 8 rows: 128 us, 5.6 TB/s (83 % of a plain copy); 32 requests of up to
+// 4 K, 4 rows: 39.5 us, 4.0 TB/s; the same of up to 20 rows: 59 us, 2.9 TB/s;
+// 8 requests of up to 64 K, 40 rows: 208 us, 3.3 TB/s and 208 TFLOP/s.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,6 +56,14 @@ constexpr float kTopWeight = 8.0f;      // a new reference puts a row's largest 
 constexpr float kMostWeight = 15.0f;    // and is replaced once one passes 2^15
 constexpr uint32_t kWeightLimit = 0x7800u;   // that as a 16-bit float
 constexpr float kLeastScale = -60.0f;   // log2 of the smallest value scale that a reference follows: P stays finite
+
+// A unit that is cut: where its rows are, and how many CTAs have parts of it.
+struct alignas(16) AttnJoin {
+  int parts;                 // 0: none
+  int first;                 // the request's first token
+  int live_rows, head;
+  int64_t r0;                // of the row tile, among the request's rows
+};
 
 struct AttnArgs {
   const uint8_t* k;
@@ -73,7 +86,7 @@ struct AttnArgs {
   float* lse;
   int32_t* status;
   float* partial;           // [CTA][2][rows][dim_padded + 2]
-  int4* joins;              // [CTA]: request, row tile, key head, parts (0: none) and eights << 24 of the unit cut there
+  AttnJoin* joins;          // [CTA]: the unit that begins there and is cut
   bool q_vector, out_vector;   // queries and results take 16-byte (results: 4-element) accesses
   int min_share;            // smallest share of a CTA, in tiles
 };
@@ -108,6 +121,11 @@ struct AttnSegment {
   int live_rows, p_first, p_last, tile_lo, tile_hi;
 };
 
+// The smallest row tile of the kernel whose largest is `most`, in eights.  The
+// more sizes one kernel has, the slower each came out (20 rows of 32 requests
+// of up to 4 K keys: 68 us with one to five eights in one kernel, 59 us alone).
+__host__ __device__ constexpr int attn_least_eights(int most) { return most == 2 ? 1 : most == 4 ? 2 : most == 5 ? 4 : most; }
+
 // The units (request, row tile, key head) in order, each as long as its tiles
 // of kTile keys plus kAttnUnitCost, and this CTA's place in them.  Equal
 // shares, whatever the lengths: share j is [j share, (j + 1) share).  Each
@@ -141,9 +159,12 @@ struct AttnLine {
   // Finds the share; every thread of the CTA calls it.  False: there is none.
   __device__ __forceinline__ bool begin(const AttnArgs& a, Shared& sh, int& flags) {
     const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    // the first kThreads requests stay in registers between the passes
+    AttnRequest own{0, 0, 0, false};
+    if (tid < a.batch) own = attn_request(a, tid);
     int64_t most = 0;
     for (int r = tid; r < a.batch; r += kThreads) {
-      const AttnRequest q = attn_request(a, r);
+      const AttnRequest q = r == tid ? own : attn_request(a, r);
       if (q.bad) flags |= kRowBadLength;
       most = max(most, int64_t(q.n) * a.group);
     }
@@ -155,12 +176,10 @@ struct AttnLine {
     for (int w = 0; w < kLineWarps; ++w) most = max(most, sh.scan[w]);
     __syncthreads();
     const int64_t tiles = max((most + 8 * kMaxNT - 1) / (8 * kMaxNT), int64_t(1));
-    nt = max(int(((most + tiles - 1) / tiles + 7) / 8), 1);
-    auto cost_of = [&](int request) -> int64_t {
-      const AttnRequest r = attn_request(a, request);
-      return int64_t(row_tiles(a, r)) * a.kv_heads * unit_cost(a, r);
-    };
-    const int64_t first_cost = tid < a.batch ? cost_of(tid) : 0;
+    nt = max(int(((most + tiles - 1) / tiles + 7) / 8), attn_least_eights(kMaxNT));
+    auto cost_at = [&](const AttnRequest& r) { return int64_t(row_tiles(a, r)) * a.kv_heads * unit_cost(a, r); };
+    auto cost_of = [&](int request) { return cost_at(attn_request(a, request)); };
+    const int64_t first_cost = cost_at(own);
     int64_t sum = first_cost;
     for (int r = tid + kThreads; r < a.batch; r += kThreads) sum += cost_of(r);
 #pragma unroll
@@ -173,7 +192,7 @@ struct AttnLine {
     share = max(int64_t(a.min_share), (total + gridDim.x - 1) / gridDim.x);
     at = share * blockIdx.x;
     end = min(total, at + share);
-    if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0) a.joins[blockIdx.x].parts = 0;
     if (at >= end) return false;
     for (int64_t base = 0, chunk = 0;; chunk += kThreads) {
       const int64_t request = chunk + tid;
@@ -404,12 +423,15 @@ struct AttnShape {
 constexpr int kAttnMaxCtas = 5;
 
 // What a kernel with row tiles of up to kMaxNT eights needs: as many CTAs per
-// SM as 228 KB (1 KB reserved and about 1.5 KB static per CTA) hold, 5 at most.
+// SM as 228 KB (1 KB reserved and about 1.5 KB static per CTA) hold, but 5 at
+// most, or 4 above two eights: the registers of five do not hold three (heads of
+// 64, 32 requests of up to 8 K keys: 76 us with five, 67 us with four).
 template <int kDP, int kMaxNT, bool kSplit>
 struct AttnKernel {
   static constexpr int kSmem = AttnShape<kDP, kMaxNT, kSplit>::kSmem;
   static constexpr int kFit = 228 * 1024 / (kSmem + 2560);
-  static constexpr int kCtas = kFit > kAttnMaxCtas ? kAttnMaxCtas : kFit;
+  static constexpr int kMost = kMaxNT > 2 ? kAttnMaxCtas - 1 : kAttnMaxCtas;
+  static constexpr int kCtas = kFit > kMost ? kMost : kFit;
   static constexpr int kRows = 8 * kMaxNT;
 };
 constexpr int kMetaStages = 8;      // tiles whose scales are kept: copies run up to three ahead of a warp one tile behind
@@ -975,15 +997,19 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnKernel<kDP, kMaxNT, kSplit>
         attention_segment<kDP, decltype(size)::value, kMaxNT, kType, kSplit>(a, seg, req, b, head, smem, sh, flags);
       };
       using std::integral_constant;
-      if (nt == 1) run(integral_constant<int, 1>());
-      else if (kMaxNT == 2 || nt == 2) run(integral_constant<int, 2>());
-      else if (nt == 3) run(integral_constant<int, kMaxNT < 3 ? kMaxNT : 3>());
-      else if (kMaxNT == 4 || nt == 4) run(integral_constant<int, kMaxNT < 4 ? kMaxNT : 4>());
-      else run(integral_constant<int, kMaxNT>());
+      constexpr int kMin = attn_least_eights(kMaxNT);
+      if (kMin == kMaxNT || nt == kMaxNT) run(integral_constant<int, kMaxNT>());
+      else if (kMin == kMaxNT - 1 || nt == kMaxNT - 1) run(integral_constant<int, kMin < kMaxNT ? kMaxNT - 1 : kMin>());
+      else run(integral_constant<int, kMin>());
     }
     Line line = line_at;
-    if (line.pos == 0 && line.end - line.at < line.cost && tid == 0)       // begun here, and cut
-      a.joins[blockIdx.x] = make_int4(line.b, line.rt, line.head, line.parts() | nt << 24);
+    if (line.pos == 0 && line.end - line.at < line.cost && tid == 0) {     // begun here, and cut
+
+      const AttnSegment seg = line.segment(a);
+      AttnJoin j{};
+      j.parts = line.parts(), j.first = line.req.first, j.r0 = seg.r0, j.live_rows = seg.live_rows, j.head = line.head;
+      a.joins[blockIdx.x] = j;
+    }
     more = line.next(a);
     __syncthreads();                           // everyone has read the line and the shared exchanges
     if (tid == 0) line_at = line;
@@ -994,52 +1020,50 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnKernel<kDP, kMaxNT, kSplit>
 
 // ---------------------------------------------------------------- joining cut units
 //
-// Grid: (CTAs of the main kernel, row tiles of 8).  The unit that began in
-// main CTA j and was cut there has its parts in slot 1 of j and slots 0 of the
-// next CTAs; one warp joins one row.
+// Grid: (CTAs of the main kernel, row tiles of 8).  The unit that began in main
+// CTA j and was cut there has its parts in slot 1 of j and slots 0 of the next
+// CTAs; one warp joins one row.
+constexpr int kJoinThreads = 256;
+
 template <int kDP, bool kSplit>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs a, const int rows) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, const int rows) {
   using T = typename std::conditional<kSplit, float, uint16_t>::type;
   allow_dependent_launch();
   grid_dependency_wait();
-  int4 u = a.joins[blockIdx.x];
-  const int tile_rows = (u.w >> 24) * 8;
-  u.w &= 0xFFFFFF;
-  if (u.w < 2) return;
-  const AttnRequest req = attn_request(a, u.x);
-  const int r = int(blockIdx.y) * 8 + (int(threadIdx.x) >> 5), lane = int(threadIdx.x) & 31;
-  const int64_t gr = int64_t(u.y) * tile_rows + r;
-  if (r >= tile_rows || gr >= int64_t(req.n) * a.group) return;
+  const AttnJoin u = a.joins[blockIdx.x];
+  const int r = int(blockIdx.y) * (kJoinThreads / 32) + (int(threadIdx.x) >> 5), lane = int(threadIdx.x) & 31;
+  if (u.parts < 2 || r >= u.live_rows) return;
   const int64_t slot = int64_t(rows) * (kDP + 2);
   auto part = [&](int i) { return a.partial + (int64_t(blockIdx.x + i) * 2 + (i == 0)) * slot; };
-  float top = -INFINITY, all = 0.0f;
-  for (int i = lane; i < u.w; i += 32) top = fmaxf(top, part(i)[rows * kDP + r]);
+  constexpr int kPer = kDP / 32;
+  float top = -INFINITY, all = 0.0f, x[kPer] = {};
+  for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, part(i)[rows * kDP + r]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  constexpr int kPer = kDP / 32;
-  float x[kPer] = {};
-  for (int i0 = 0; i0 < u.w; i0 += 32) {
+  for (int i0 = 0; i0 < u.parts; i0 += 32) {
     float f = 0.0f;
-    if (i0 + lane < u.w) {
-      const float m = part(i0 + lane)[rows * kDP + r], l = part(i0 + lane)[rows * kDP + rows + r];
+    if (i0 + lane < u.parts) {
+      const float m = part(i0 + lane)[rows * kDP + r], l = part(i0 + lane)[rows * (kDP + 1) + r];
+      // a part that saw only NaN has no reference, but a sum
       f = l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : exp2_approx(m - top);
       if (l != 0.0f) all += l * f;
     }
-    const int count = min(32, u.w - i0);
-#pragma unroll 4
+    const int count = min(32, u.parts - i0);
+#pragma unroll 8
     for (int i = 0; i < count; ++i) {
       const float w = __shfl_sync(~0u, f, i);
-      if (w != 0.0f) {
-        const float* p = part(i0 + i) + r * kDP + lane * kPer;
+      const float* p = part(i0 + i) + r * kDP + lane * kPer;
+      float y[kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = fmaf(p[e], w, x[e]);
-      }
+      for (int e = 0; e < kPer; ++e) y[e] = p[e];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = w != 0.0f ? fmaf(y[e], w, x[e]) : x[e];
     }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
   const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-  const int64_t token = req.first + gr / a.group, qh = int64_t(u.z) * a.group + gr % a.group;
+  const int64_t gr = u.r0 + r, token = u.first + gr / a.group, qh = int64_t(u.head) * a.group + gr % a.group;
   T* out = static_cast<T*>(a.out) + token * a.out_stride + qh * a.dim + lane * kPer;
   if (lane * kPer < a.dim) {
 #pragma unroll
@@ -1072,18 +1096,21 @@ cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
   err = cudaLaunchKernelEx(&cfg, attention_kernel<kDP, kMaxNT, kType, kSplit>, a);
   if (err != cudaSuccess) return err;
   cfg.gridDim = dim3(unsigned(grid), unsigned(kMaxNT));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDP, kSplit>, a, K::kRows);
 }
 
-// Two kernels per head size: row tiles of up to 16 rows, whose smaller state
-// leaves room for five CTAs per SM, and of up to 40 (32 for heads of 256 and
-// binary32 queries), beyond which the registers spill.  `rows` is what the
-// host expects of most requests; the kernel sees the longest itself.
+// Kernels per head size: row tiles of up to 16 rows, whose smaller state leaves
+// room for five CTAs per SM, of 24, and of up to 40 (32 for heads of 256 and
+// binary32 queries), beyond which the registers spill.  `rows` is what the host
+// expects of most requests; the kernel sees the longest itself, and takes
+// several row tiles, which read the keys again, where its largest is too small.
 template <int kType, bool kSplit, int kDP>
 cudaError_t attn_launch_dim(const AttnArgs& a, int64_t rows, int dev, cudaStream_t st) {
   if (rows <= 16) return attn_launch_shape<kDP, 2, kType, kSplit>(a, dev, st);
+  if constexpr (!kSplit && kDP != 256)
+    if (rows <= 24) return attn_launch_shape<kDP, 3, kType, kSplit>(a, dev, st);
   return attn_launch_shape<kDP, kSplit || kDP == 256 ? 4 : 5, kType, kSplit>(a, dev, st);
 }
 
