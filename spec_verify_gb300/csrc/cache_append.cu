@@ -19,7 +19,7 @@
 
 namespace smp {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256;       // 128 where the call is short of runs
 constexpr int kMinScaleExp = -100;
 
 struct AppendArgs {
@@ -113,7 +113,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inverse) {
 }
 
 // The rare forms are out of line and rolled: inlined, they made the kernel
-// miss its instruction cache (56 us against the figure at the kernel).
+// miss its instruction cache (16 K tokens of prompts: 56 us, 27 out of line).
 
 // Eight codes of any x and any s.
 template <int kType>
@@ -128,10 +128,10 @@ __device__ __noinline__ uint2 encode8_any(float x0, float x1, float x2, float x3
 }
 
 // The `count` codes before a run, encoded again after the scale grew.
-template <int kType>
+template <int kThreads, int kType>
 __device__ __noinline__ void encode_again(uint8_t* codes, int count, float old, float s) {
   const float ratio = __fdiv_rn(old, s);
-  for (int i = int(threadIdx.x); i < count / 4; i += kAppendThreads) {
+  for (int i = int(threadIdx.x); i < count / 4; i += kThreads) {
     uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
     const uint32_t c = *p;
     uint32_t out = 0;
@@ -162,7 +162,7 @@ struct AppendSide {
 
 // A run of one head, k and v together: their loads are all in flight before
 // the first is used, and one pair of barriers finds both maxima.
-template <typename T, int kType>
+template <int kThreads, typename T, int kType>
 __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide<T> (&side)[2], int head,
                                            int64_t token, int count, int64_t slot, float (*scratch)[2], int& flags) {
   // vectors of eight elements that a thread keeps of each side between the two
@@ -183,9 +183,9 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
     old[w] = offset ? *scale[w] : 0.0f;
   }
 
-  // vector v = tid + i * kAppendThreads is piece v % per_row of row v / per_row
+  // vector v = tid + i * kThreads is piece v % per_row of row v / per_row
   const int row0 = tid / per_row, piece0 = tid - row0 * per_row;
-  const int step_row = kAppendThreads / per_row, step_piece = kAppendThreads - step_row * per_row;
+  const int step_row = kThreads / per_row, step_piece = kThreads - step_row * per_row;
   Eight<T> kept[2][kKept];
   float amax[2] = {0.0f, 0.0f};
   bool odd = false;
@@ -212,14 +212,14 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    if (tid + i * kAppendThreads < vectors) load(0, row, piece, kept[0][i]), load(1, row, piece, kept[1][i]);
+    if (tid + i * kThreads < vectors) load(0, row, piece, kept[0][i]), load(1, row, piece, kept[1][i]);
     advance();
   }
   const int more_row = row, more_piece = piece;
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
-    if (tid + i * kAppendThreads < vectors) look(kept[0][i], amax[0]), look(kept[1][i], amax[1]);
-  for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
+    if (tid + i * kThreads < vectors) look(kept[0][i], amax[0]), look(kept[1][i], amax[1]);
+  for (int v = tid + kKept * kThreads; v < vectors; v += kThreads) {
     Eight<T> e[2];
     load(0, row, piece, e[0]), load(1, row, piece, e[1]);
     advance();
@@ -235,7 +235,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
   if ((tid & 31) == 0) scratch[tid >> 5][0] = amax[0], scratch[tid >> 5][1] = amax[1];
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w)
+  for (int w = 0; w < kThreads / 32; ++w)
     amax[0] = fmaxf(amax[0], scratch[w][0]), amax[1] = fmaxf(amax[1], scratch[w][1]);
 
 #pragma unroll
@@ -243,7 +243,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
     const float s = fmaxf(needed_scale<kType>(amax[w]), old[w]);
     const float inverse = (__float_as_uint(s) & 0x7FFFFFu) == 0 ? __fdiv_rn(1.0f, s) : 0.0f;
     if (tid == 0) *scale[w] = s;
-    if (offset && s != old[w]) encode_again<kType>(codes[w], offset * a.dim, old[w], s);
+    if (offset && s != old[w]) encode_again<kThreads, kType>(codes[w], offset * a.dim, old[w], s);
     uint2* out = reinterpret_cast<uint2*>(codes[w] + offset * a.dim);   // rows of a run are contiguous
     const bool plain = inverse != 0.0f && !odd;
     auto encode = [&](const Eight<T>& e) {
@@ -253,11 +253,11 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
     };
 #pragma unroll
     for (int i = 0; i < kKept; ++i) {
-      const int v = tid + i * kAppendThreads;
+      const int v = tid + i * kThreads;
       if (v < vectors) out[v] = encode(kept[w][i]);
     }
     row = more_row, piece = more_piece;
-    for (int v = tid + kKept * kAppendThreads; v < vectors; v += kAppendThreads) {
+    for (int v = tid + kKept * kThreads; v < vectors; v += kThreads) {
       Eight<T> e;
       load(w, row, piece, e);
       advance();
@@ -266,13 +266,28 @@ __device__ __forceinline__ void append_run(const AppendArgs& a, const AppendSide
   }
 }
 
-// Grid: (spans of tokens, heads).
-template <typename T, int kType>
-__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const AppendArgs a) {
-  __shared__ float scratch[kAppendThreads / 32][2];
+// Grid: (spans of tokens, heads).  Prompts of 16 K tokens, 8 heads of 128, bf16
+// to i8: 26 us, 3.9 TB/s of elements and codes (the codes mostly stay in L2),
+// in seven waves of CTAs that each wait for their loads once; the prefetch of
+// the span's rows takes 1 us off.  160 tokens of 32 requests: 4.0 us, the
+// latency of slots, elements, maximum and stores one after the other.
+template <int kThreads, typename T, int kType>
+__global__ void __launch_bounds__(kThreads, kThreads == kAppendThreads ? 4 : 6) cache_append_kernel(const AppendArgs a) {
+  __shared__ float scratch[kThreads / 32][2];
   allow_dependent_launch();
-  grid_dependency_wait();
   const int head = int(blockIdx.y), lane = int(threadIdx.x) & 31;
+  if (a.span > 1) {
+    // the span's rows into L2 while the slots are looked up (a hint, which changes no memory)
+    const int lines = (a.dim * int(sizeof(T)) + 127) / 128;
+    const int rows = int(min(int64_t(a.span), int64_t(a.tokens) - int64_t(blockIdx.x) * a.span));
+    for (int i = int(threadIdx.x); i < 2 * rows * lines; i += kThreads) {
+      const int w = i >= rows * lines, r = i / lines - w * rows, l = i % lines;
+      const T* x = static_cast<const T*>(w ? a.new_v : a.new_k) +
+                   (int64_t(blockIdx.x) * a.span + r) * (w ? a.v_stride : a.k_stride) + int64_t(head) * a.dim;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(x) + l * 128));
+    }
+  }
+  grid_dependency_wait();
   const AppendSide<T> side[2] = {{a.k, a.k_scale, static_cast<const T*>(a.new_k), a.k_stride, a.k_vector},
                                  {a.v, a.v_scale, static_cast<const T*>(a.new_v), a.v_stride, a.v_vector}};
   const int64_t first = int64_t(blockIdx.x) * a.span;
@@ -310,25 +325,35 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const A
         count += more ? 32 : __ffs(broken) - 1;
       }
     }
-    append_run<T, kType>(a, side, head, first + at, count, run, scratch, flags);
+    append_run<kThreads, T, kType>(a, side, head, first + at, count, run, scratch, flags);
   }
   if (flags && a.status) atomicOr(a.status, flags);
 }
 
-template <typename T, int kType>
-static smp_status launch_append(const AppendArgs& a, cudaStream_t st) {
+template <int kThreads, typename T, int kType>
+static smp_status launch_append_with(const AppendArgs& a, cudaStream_t st) {
   const int64_t spans = (int64_t(a.tokens) + a.span - 1) / a.span;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(spans), unsigned(a.heads));
-  cfg.blockDim = dim3(kAppendThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, cache_append_kernel<T, kType>, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, cache_append_kernel<kThreads, T, kType>, a);
   return err == cudaSuccess ? SMP_OK : fail_cuda(err);
+}
+
+// Where a CTA looks at one token (fewer than 16 tokens and heads per SM), runs
+// are short and few: half the threads start and meet sooner (32 requests' 5
+// tokens, 8 heads of 128: 4.0 us, 5.4 with 256; 16 K tokens of prompts: 28 us
+// with 128, 26 with 256).
+template <typename T, int kType>
+static smp_status launch_append(const AppendArgs& a, cudaStream_t st) {
+  return a.span == 1 ? launch_append_with<kAppendThreads / 2, T, kType>(a, st)
+                     : launch_append_with<kAppendThreads, T, kType>(a, st);
 }
 
 }  // namespace smp

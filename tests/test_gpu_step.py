@@ -267,6 +267,21 @@ def test_append(heads, d, bs, runs, dt, kind):
     assert check_append(arrays, kind, x, slots, bs, dt) == 0
 
 
+@pytest.mark.parametrize("kind,dt", [("e4m3", "f32"), ("i8", "bf16")])
+@pytest.mark.parametrize("heads,d,bs,runs", [(12, 32, 16, [37, 1, 180, 5, 99]), (16, 16, 128, [700, 3, 129, 1000, 1, 64, 700]),
+                                             (40, 48, 64, [333, 1, 64, 65, 500, 90])])
+def test_append_of_long_steps(heads, d, bs, runs, dt, kind):
+    # enough tokens and heads that a CTA looks at 2 to 32 tokens; padding and bad slots among them
+    rng = np.random.default_rng(sum(runs) * heads)
+    blocks = sum(-(-n // bs) + 1 for n in runs) + 2
+    arrays = random_cache(rng, blocks, heads, bs, d, kind)
+    slots = run_slots(rng, bs, blocks, runs)
+    slots = np.insert(slots, [0, runs[0], len(slots)], [-1, -7, blocks * bs])
+    x = rng.normal(0, 1, (2, len(slots), heads, d)) * 2.0 ** rng.integers(-12, 6, (2, len(slots), 1, 1))
+    x[0, 5, heads - 1, 3], x[1, -9, 0, d - 1] = np.nan, np.inf
+    assert check_append(arrays, kind, x, slots, bs, dt) == binding.ROW_BAD_LENGTH | binding.ROW_NONFINITE
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "i8"])
 def test_append_exact_limits_zeros_and_nonfinite(kind):
     rng = np.random.default_rng(3)
