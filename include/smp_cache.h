@@ -93,7 +93,8 @@ typedef struct smp_cache {
  *                  position lens[b] + i, the request b and the slot; -1 past
  *                  the last token, so that a captured step of a fixed size
  *                  can run with fewer.
- *   batch 0 .. 2^24; num_blocks 1 ..; outputs must not overlap inputs.
+ *   batch 0 .. 2^24; num_blocks 1 ..; max_tokens and free_count 0 .. 2^31-2;
+ *   outputs must not overlap inputs.
  * An invalid request adds nothing (SMP_ROW_BAD_LENGTH): its length and blocks
  * stay.  When tokens or free blocks run out, the first request that does not
  * fit and all later ones that add tokens add nothing (SMP_ROW_NO_CAPACITY).

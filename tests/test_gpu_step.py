@@ -101,6 +101,22 @@ def test_block_plan_without_requests_or_room():
     assert check_plan(lens, add, held, free, 0, table, 16, blocks, 0) == 32
 
 
+def test_block_plan_of_half_a_million_tokens():
+    rng = np.random.default_rng(7)
+    lens, add, held, free, table, blocks = plan_case(rng, 300, 90, 3300, 64)
+    cap = int(add.sum())
+    assert cap > 400000
+    assert check_plan(lens, add, held, free, 0, table, 64, blocks, cap) == 0
+    assert check_plan(lens, add, held, free, 0, table, 64, blocks, cap - 1) == 32
+
+
+def test_block_plan_sums_past_32_bits():
+    lens, held = np.zeros(6, dtype=np.int64), np.zeros(6, dtype=np.int64)
+    table = np.full((6, 1 << 22), -1, dtype=np.int32)
+    for add in ([5, 2 ** 30, 2 ** 30, 2 ** 30, 2 ** 30, 3], [5, 0, 2 ** 30, 2 ** 30, 7, 2 ** 30]):
+        assert check_plan(lens, np.array(add), held, np.arange(9), 0, table, 256, 9, 40) == 32
+
+
 def test_block_plan_bad_inputs():
     rng = np.random.default_rng(2)
     lens, add, held, free, table, blocks = plan_case(rng, 40, 100, 30, 16)

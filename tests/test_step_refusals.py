@@ -31,6 +31,7 @@ def test_block_plan(lib):
                 dict(free=NULL), dict(free_count=-1), dict(head=NULL), dict(table=NULL), dict(stride=-1), dict(bs=8),
                 dict(bs=24), dict(bs=512), dict(blocks=0), dict(cap=-1), dict(olens=NULL), dict(oheld=NULL),
                 dict(ohead=NULL), dict(ostart=NULL), dict(opos=NULL), dict(oreq=NULL), dict(oslot=NULL),
+                dict(cap=2 ** 31 - 1), dict(free_count=2 ** 31 - 1),
                 dict(lens=ODD), dict(table=ODD), dict(oslot=ctypes.c_void_p(0x1004)), dict(status=ODD)):
         assert call(lib.smp_block_plan, good, **bad) == 1, bad
 
