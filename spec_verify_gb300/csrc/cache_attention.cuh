@@ -128,10 +128,10 @@ __host__ __device__ constexpr int attn_least_eights(int most) { return most == 2
 
 // The units (request, row tile, key head) in order, each as long as its tiles
 // of kTile keys plus kAttnUnitCost, and this CTA's place in them.  Equal
-// shares, whatever the lengths: share j is [j share, (j + 1) share).  Each
-// request has row tiles of its own size, the fewest and then the smallest of
-// up to kMaxNT eights that hold its rows, so that a step of one token beside
-// one of many costs what its rows cost.
+// shares, whatever the lengths: share j is [j share, (j + 1) share).  The row
+// tile is one size for the call, from the longest request as the device sees
+// it: the fewest tiles of up to kMaxNT eights, and then the smallest that are
+// as few.
 template <int kThreads, int kTile, int kMaxNT>
 struct AttnLine {
   static constexpr int kLineWarps = kThreads / 32;
