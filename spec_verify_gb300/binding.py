@@ -6,6 +6,7 @@ been built, loading fails loudly: there is no other implementation to fall
 back to.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -166,6 +167,14 @@ def _stream(stream):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream):
+    """The context in which a call that is launched on `stream` (None: the
+    current one) makes its own tensors.  The allocator then keeps their memory
+    for that stream: nothing that runs elsewhere is given it while the call,
+    which is asynchronous, still uses it."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
 def params_to_device(params, device):
@@ -450,11 +459,13 @@ def spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens=None, out_acc
     draft_lens: int32 [B], the drafts each row really has, or None for K.
     status: an int32 [1] tensor for the SMP_ROW_* flags, or None (no status
     word).  Returns (accepted_len int32 [B], ids int32 [B, K+1])."""
-    native = step_module()
-    if out_accepted is None:
-        out_accepted = _torch().empty(p.shape[0], dtype=_torch().int32, device=p.device)
-    if out_ids is None:
-        out_ids = _torch().empty(p.shape[:2], dtype=_torch().int32, device=p.device)
+    native, torch = step_module(), _torch()
+    if out_accepted is None or out_ids is None:
+        with _on(stream):
+            if out_accepted is None:
+                out_accepted = torch.empty(p.shape[0], dtype=torch.int32, device=p.device)
+            if out_ids is None:
+                out_ids = torch.empty(p.shape[:2], dtype=torch.int32, device=p.device)
     native.spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens, out_accepted, out_ids, status,
                              None if stream is None else stream.cuda_stream)
     return out_accepted, out_ids

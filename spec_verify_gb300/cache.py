@@ -8,13 +8,14 @@ float32 scales [blocks, kv_heads].  `new_cache` makes one.
 
 Every call takes `status`, an int32 [1] CUDA tensor that is cleared and gets
 the ROW_* flags of binding.py, or None (no status word), and `stream`, a
-torch.cuda.Stream, or None for the current one.  What a call cannot take is
-refused with SmpError before anything is launched.
+torch.cuda.Stream, or None for the current one.  Tensors that a call makes
+itself (outputs not given, scratch) belong to the stream it is launched on.
+What a call cannot take is refused with SmpError before anything is launched.
 """
 
 import collections
 
-from .binding import _torch, load, step_module
+from .binding import _on, _torch, load, step_module
 
 BlockPlan = collections.namedtuple("BlockPlan", "lens held free_head start position request slot")
 
@@ -55,7 +56,8 @@ def block_plan(lens, add, held, free_blocks, free_head, block_table, block_size,
         torch = _torch()
         b, i32 = lens.shape[0], torch.int32
         new = lambda n, t=i32: torch.empty(n, dtype=t, device=lens.device)  # noqa: E731
-        out = (new(b), new(b), new(1), new(b + 1), new(max_tokens), new(max_tokens), new(max_tokens, torch.int64))
+        with _on(stream):
+            out = (new(b), new(b), new(1), new(b + 1), new(max_tokens), new(max_tokens), new(max_tokens, torch.int64))
     native.block_plan(lens, add, held, free_blocks, free_head, block_table, block_size, num_blocks, max_tokens, *out,
                       status, _queue(stream))
     return BlockPlan(*out)
@@ -70,10 +72,12 @@ def qk_norm_rope(q, k, positions, table=None, q_weight=None, k_weight=None, eps=
     and k themselves: in place), or None for new ones.  Returns (out_q,
     out_k)."""
     native = step_module()
-    if out_q is None:
-        out_q = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and out_k is None:
-        out_k = _torch().empty(k.shape, dtype=k.dtype, device=k.device)
+    if out_q is None or (k is not None and out_k is None):
+        with _on(stream):
+            if out_q is None:
+                out_q = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+            if k is not None and out_k is None:
+                out_k = _torch().empty(k.shape, dtype=k.dtype, device=k.device)
     native.qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps, interleaved, out_q, out_k, status,
                         _queue(stream))
     return out_q, out_k
@@ -99,12 +103,14 @@ def cache_attention(cache, q, start, lens, block_table, scale=None, window=0, ou
     attention_workspace_bytes(...) that no overlapping call uses, or None to
     allocate one.  Returns out [T, Hq, D]."""
     native = step_module()
-    if out is None:
-        out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
-    if workspace is None:
+    if out is None or workspace is None:
         torch = _torch()
-        need = attention_workspace_bytes(q.shape[0], q.shape[1], cache[0].shape[1], q.shape[2], lens.shape[0])
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if workspace is None:
+                need = attention_workspace_bytes(q.shape[0], q.shape[1], cache[0].shape[1], q.shape[2], lens.shape[0])
+                workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
     native.cache_attention(cache, q, start, lens, block_table, q.shape[2] ** -0.5 if scale is None else scale, window,
                            out, lse, workspace, status, _queue(stream))
     return out
