@@ -200,13 +200,14 @@ def sample(logits, params, seed=0, offset=0, out_ids=None, out_probs=None, statu
         raise SmpError("logits must be a contiguous [B, V] CUDA tensor")
     batch, vocab = logits.shape
     dev = logits.device
-    prm = params_to_device(params, dev)
-    out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
-    out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
-    if status is False:
-        status = None
-    elif status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        prm = params_to_device(params, dev)
+        out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
+        out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
+        if status is False:
+            status = None
+        elif status is None:
+            status = torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_sample(_ptr(logits), batch, vocab, _dtype_code(logits), _ptr(prm), seed, offset,
                           _ptr(out_ids), _ptr(out_probs), _ptr(status), _stream(stream)))
     return out_ids, out_probs, status
@@ -224,7 +225,6 @@ def sample_processed(logits, params, seed=0, offset=0, allowed=None, history=Non
         raise SmpError("logits must be a contiguous [B, V] CUDA tensor")
     batch, vocab = logits.shape
     dev = logits.device
-    prm = params_to_device(params, dev)
     for t, shape in ((allowed, (batch, (vocab + 31) // 32)), (penalty, (batch,))):
         if t is not None and (tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous()):
             raise SmpError(f"expected a contiguous CUDA tensor of shape {shape}")
@@ -233,9 +233,11 @@ def sample_processed(logits, params, seed=0, offset=0, allowed=None, history=Non
         if history.dim() != 2 or history.shape[0] != batch or history.dtype != torch.int32:
             raise SmpError("history must be an int32 [B, H] CUDA tensor")
         hlen = int(history.shape[1])
-    out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
-    out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
-    status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        prm = params_to_device(params, dev)
+        out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
+        out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
+        status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_sample_processed(_ptr(logits), batch, vocab, _dtype_code(logits), _ptr(prm), _ptr(allowed),
                                     _ptr(history), hlen, _ptr(penalty), seed, offset, _ptr(out_ids),
                                     _ptr(out_probs), _ptr(status), _stream(stream)))
@@ -254,7 +256,6 @@ def sample_rows(logits, params, seed=0, offset=0, row_base=0, allowed=None, hist
         raise SmpError("logits must be a contiguous [B, V] CUDA tensor")
     batch, vocab = logits.shape
     dev = logits.device
-    prm = params_to_device(params, dev)
     for t, shape in ((allowed, (batch, (vocab + 31) // 32)), (penalty, (batch,))):
         if t is not None and (tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous()):
             raise SmpError(f"expected a contiguous CUDA tensor of shape {shape}")
@@ -263,12 +264,14 @@ def sample_rows(logits, params, seed=0, offset=0, row_base=0, allowed=None, hist
         if history.dim() != 2 or history.shape[0] != batch or history.dtype != torch.int32:
             raise SmpError("history must be an int32 [B, H] CUDA tensor")
         hlen = int(history.shape[1])
-    out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
-    out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
-    if status is False:
-        status = None
-    elif status is None:
-        status = torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        prm = params_to_device(params, dev)
+        out_ids = out_ids if out_ids is not None else torch.empty(batch, dtype=torch.int32, device=dev)
+        out_probs = out_probs if out_probs is not None else torch.empty(batch, dtype=torch.float32, device=dev)
+        if status is False:
+            status = None
+        elif status is None:
+            status = torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_sample_rows(_ptr(logits), batch, vocab, _dtype_code(logits), _ptr(prm), _ptr(allowed),
                                _ptr(history), hlen, _ptr(penalty), seed, offset, int(row_base), _ptr(out_ids),
                                _ptr(out_probs), _ptr(status), _stream(stream)))
@@ -293,7 +296,8 @@ def logit_prepass(logits, allowed=None, history=None, penalty=None, status=None,
         if history.dim() != 2 or history.shape[0] != batch or history.dtype != torch.int32:
             raise SmpError("history must be an int32 [B, H] CUDA tensor")
         hlen = int(history.shape[1])
-    status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_logit_prepass(_ptr(logits), batch, vocab, _dtype_code(logits), _ptr(allowed), _ptr(history),
                                  hlen, _ptr(penalty), _ptr(status), _stream(stream)))
     return status
@@ -307,12 +311,13 @@ def filter_debug(logits, params, seed=0, offset=0, stream=None):
         raise SmpError("logits must be a contiguous [B, V] CUDA tensor")
     batch, vocab = logits.shape
     dev = logits.device
-    prm = params_to_device(params, dev)
-    ids = torch.empty(batch, dtype=torch.int32, device=dev)
-    probs = torch.empty(batch, dtype=torch.float32, device=dev)
-    full = torch.empty(batch, vocab, dtype=torch.float32, device=dev)
-    kept = torch.empty(batch, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        prm = params_to_device(params, dev)
+        ids = torch.empty(batch, dtype=torch.int32, device=dev)
+        probs = torch.empty(batch, dtype=torch.float32, device=dev)
+        full = torch.empty(batch, vocab, dtype=torch.float32, device=dev)
+        kept = torch.empty(batch, dtype=torch.int32, device=dev)
+        status = torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_filter_debug(_ptr(logits), batch, vocab, _dtype_code(logits), _ptr(prm), seed, offset,
                                 _ptr(ids), _ptr(probs), _ptr(full), _ptr(kept), _ptr(status),
                                 _stream(stream)))
@@ -339,15 +344,17 @@ def _verify_shapes(p_logits, q_logits, draft_ids):
     return batch, k, vocab
 
 
-def _verify_outputs(batch, k, dev, workspace, out_accepted, out_ids, status):
+def _verify_outputs(batch, k, dev, workspace, out_accepted, out_ids, status, params, stream):
     torch = _torch()
     need = spec_verify_workspace_bytes(batch, k)
-    if workspace is None:
-        workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=dev)
-    out_accepted = out_accepted if out_accepted is not None else torch.empty(batch, dtype=torch.int32, device=dev)
-    out_ids = out_ids if out_ids is not None else torch.empty(batch, k + 1, dtype=torch.int32, device=dev)
-    status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
-    return workspace, out_accepted, out_ids, status
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=dev)
+        out_accepted = out_accepted if out_accepted is not None else torch.empty(batch, dtype=torch.int32, device=dev)
+        out_ids = out_ids if out_ids is not None else torch.empty(batch, k + 1, dtype=torch.int32, device=dev)
+        status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
+        prm = params_to_device(params, dev) if params is not None else None
+    return workspace, out_accepted, out_ids, status, prm
 
 
 def spec_verify(p_logits, q_logits, draft_ids, seed=0, offset=0, workspace=None, out_accepted=None,
@@ -358,8 +365,8 @@ def spec_verify(p_logits, q_logits, draft_ids, seed=0, offset=0, workspace=None,
     """
     lib = load()
     batch, k, vocab = _verify_shapes(p_logits, q_logits, draft_ids)
-    workspace, out_accepted, out_ids, status = _verify_outputs(batch, k, p_logits.device, workspace,
-                                                               out_accepted, out_ids, status)
+    workspace, out_accepted, out_ids, status, _ = _verify_outputs(batch, k, p_logits.device, workspace, out_accepted,
+                                                                  out_ids, status, None, stream)
     _check(lib.smp_spec_verify(_ptr(p_logits), _ptr(q_logits), _ptr(draft_ids), batch, k, vocab,
                                _dtype_code(p_logits), seed, offset, _ptr(out_accepted), _ptr(out_ids),
                                _ptr(status), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -376,9 +383,8 @@ def spec_verify_params(p_logits, q_logits, draft_ids, params, seed=0, offset=0, 
     lib = load()
     batch, k, vocab = _verify_shapes(p_logits, q_logits, draft_ids)
     dev = p_logits.device
-    prm = params_to_device(params, dev) if params is not None else None
-    workspace, out_accepted, out_ids, status = _verify_outputs(batch, k, dev, workspace, out_accepted,
-                                                               out_ids, status)
+    workspace, out_accepted, out_ids, status, prm = _verify_outputs(batch, k, dev, workspace, out_accepted, out_ids,
+                                                                    status, params, stream)
     _check(lib.smp_spec_verify_params(_ptr(p_logits), _ptr(q_logits), _ptr(draft_ids), batch, k, vocab,
                                       _dtype_code(p_logits), _ptr(prm), seed, offset, _ptr(out_accepted),
                                       _ptr(out_ids), _ptr(out_alpha), _ptr(status), _ptr(workspace),
@@ -394,9 +400,8 @@ def spec_verify_rows(p_logits, q_logits, draft_ids, params=None, seed=0, offset=
     lib = load()
     batch, k, vocab = _verify_shapes(p_logits, q_logits, draft_ids)
     dev = p_logits.device
-    prm = params_to_device(params, dev) if params is not None else None
-    workspace, out_accepted, out_ids, status = _verify_outputs(batch, k, dev, workspace, out_accepted,
-                                                               out_ids, status)
+    workspace, out_accepted, out_ids, status, prm = _verify_outputs(batch, k, dev, workspace, out_accepted, out_ids,
+                                                                    status, params, stream)
     _check(lib.smp_spec_verify_rows(_ptr(p_logits), _ptr(q_logits), _ptr(draft_ids), batch, k, vocab,
                                     _dtype_code(p_logits), _ptr(prm), seed, offset, int(row_base), _ptr(out_accepted),
                                     _ptr(out_ids), _ptr(out_alpha), _ptr(status), _ptr(workspace),
@@ -414,9 +419,10 @@ def spec_verify_static(p_logits, q_logits, draft_ids, seed=0, offset=0, out_acce
     batch, k1, vocab = p_logits.shape
     k = k1 - 1
     dev = p_logits.device
-    out_accepted = out_accepted if out_accepted is not None else torch.empty(batch, dtype=torch.int32, device=dev)
-    out_ids = out_ids if out_ids is not None else torch.empty(batch, k + 1, dtype=torch.int32, device=dev)
-    status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        out_accepted = out_accepted if out_accepted is not None else torch.empty(batch, dtype=torch.int32, device=dev)
+        out_ids = out_ids if out_ids is not None else torch.empty(batch, k + 1, dtype=torch.int32, device=dev)
+        status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_spec_verify_static(_ptr(p_logits), _ptr(q_logits), _ptr(draft_ids), batch, k, vocab,
                                       _dtype_code(p_logits), seed, offset, _ptr(out_accepted),
                                       _ptr(out_ids), _ptr(status), _stream(stream)))
@@ -439,12 +445,13 @@ def beam_topk(logits, beam_scores, width=None, workspace=None, out_parent=None, 
     width = beams if width is None else int(width)
     dev = logits.device
     need = int(lib.smp_beam_topk_workspace_bytes(groups, beams, width))
-    if workspace is None:
-        workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=dev)
-    out_parent = out_parent if out_parent is not None else torch.empty(groups, width, dtype=torch.int32, device=dev)
-    out_token = out_token if out_token is not None else torch.empty(groups, width, dtype=torch.int32, device=dev)
-    out_score = out_score if out_score is not None else torch.empty(groups, width, dtype=torch.float64, device=dev)
-    status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(need, 8), dtype=torch.uint8, device=dev)
+        out_parent = out_parent if out_parent is not None else torch.empty(groups, width, dtype=torch.int32, device=dev)
+        out_token = out_token if out_token is not None else torch.empty(groups, width, dtype=torch.int32, device=dev)
+        out_score = out_score if out_score is not None else torch.empty(groups, width, dtype=torch.float64, device=dev)
+        status = status if status is not None else torch.empty(1, dtype=torch.int32, device=dev)
     _check(lib.smp_beam_topk(_ptr(logits), _ptr(beam_scores), groups, beams, vocab, width, _dtype_code(logits),
                              _ptr(out_parent), _ptr(out_token), _ptr(out_score), _ptr(status), _ptr(workspace),
                              workspace.numel(), _stream(stream)))
