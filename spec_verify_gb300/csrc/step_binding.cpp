@@ -6,6 +6,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <initializer_list>
@@ -33,12 +34,20 @@ std::string shape_text(c10::IntArrayRef s) {
 
 using Tensor = at::Tensor;
 
+// The GPU of the call at hand: its first tensor's, which the others must share (-1: none seen yet).
+thread_local int g_device = -1;
+
 // The tensor of an argument, or nullptr for None.
 const Tensor* optional(PyObject* o, const char* name) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a torch tensor");
   const Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
+  const int device = t.device().index();
+  if (g_device < 0) g_device = device;
+  if (device != g_device)
+    refuse("the tensors of a call must be on one GPU: " + std::string(name) + " is on cuda:" + std::to_string(device) +
+           ", the first one on cuda:" + std::to_string(g_device));
   return &t;
 }
 
@@ -99,11 +108,20 @@ double number(PyObject* o) {
   return v;
 }
 
-// A torch.cuda.Stream's handle (an int), or None for the current stream of the tensor's device.
-void* stream_of(PyObject* o, const Tensor& t) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+// A torch.cuda.Stream's handle (an int), or None for the current stream of the call's GPU.
+void* stream_of(PyObject* o) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(g_device)).stream();
   return reinterpret_cast<void*>(uintptr_t(integer(o)));
 }
+
+// What every call takes last; with it all tensors have been seen, and their GPU is the current one for the launch.
+struct Launch {
+  int32_t* status;
+  c10::cuda::CUDAGuard on;
+  void* stream;
+  Launch(PyObject* status_arg, PyObject* stream_arg)
+      : status(status_of(status_arg)), on(c10::DeviceIndex(g_device)), stream(stream_of(stream_arg)) {}
+};
 
 smp_dtype dtype_of(const Tensor& t, const char* name) {
   if (t.scalar_type() == at::kBFloat16) return SMP_BF16;
@@ -168,6 +186,7 @@ template <typename F>
 PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& body) {
   try {
     if (have != want) refuse("wrong number of arguments");
+    g_device = -1;
     body();
     Py_RETURN_NONE;
   } catch (const Refused& e) {
@@ -211,12 +230,13 @@ PyObject* py_block_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       out[i] = &tensor(a[9 + i], names[i]);
       flat(*out[i], names[i], i == 6 ? at::kLong : at::kInt, {sizes[i]});
     }
+    const Launch to(a[16], a[17]);
     check(smp_block_plan(ptr<int32_t>(lens), ptr<int32_t>(add), ptr<int32_t>(held), small(b, "batch"),
                          ptr<int32_t>(free_blocks), small(free_blocks.size(0), "free_blocks"), ptr<int32_t>(head),
                          ptr<int32_t>(table), small(table.size(1), "block_table"), integer32(a[6], "block_size"),
                          integer32(a[7], "num_blocks"), cap, ptr<int32_t>(out[0]), ptr<int32_t>(out[1]),
                          ptr<int32_t>(out[2]), ptr<int32_t>(out[3]), ptr<int32_t>(out[4]), ptr<int32_t>(out[5]),
-                         ptr<int64_t>(out[6]), status_of(a[16]), stream_of(a[17], lens)));
+                         ptr<int64_t>(out[6]), to.status, to.stream));
   });
 }
 
@@ -245,12 +265,12 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (table) flat(*table, "table", at::kFloat, {-1, -1});
     if (qw) flat(*qw, "q_weight", at::kFloat, {d});
     if (kw) flat(*kw, "k_weight", at::kFloat, {d});
+    const Launch to(a[10], a[11]);
     check(smp_qk_norm_rope(at_of(q), at_of(k), small(t, "tokens"), small(q.size(1), "heads"), small(hk, "heads"),
                            small(d, "dim"), qs, ks, dtype_of(q, "q"), ptr<float>(qw), ptr<float>(kw),
                            float(number(a[6])), ptr<float>(table), table ? small(table->size(0), "table") : 0,
                            table ? small(table->size(1), "table") : 0, integer32(a[7], "interleaved"),
-                           ptr<int32_t>(positions), at_of(oq), k ? at_of(ok) : nullptr, oqs, oks, status_of(a[10]),
-                           stream_of(a[11], q)));
+                           ptr<int32_t>(positions), at_of(oq), k ? at_of(ok) : nullptr, oqs, oks, to.status, to.stream));
   });
 }
 
@@ -264,8 +284,9 @@ PyObject* py_cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ks = heads_of(k, "k"), vs = heads_of(v, "v", &k), t = k.size(0);
     if (k.size(1) != c.kv_heads || k.size(2) != c.head_dim) refuse("k must be [tokens, kv_heads, head_dim] of the cache");
     flat(slots, "slots", at::kLong, {t});
+    const Launch to(a[4], a[5]);
     check(smp_cache_append(&c, at_of(k), at_of(v), small(t, "tokens"), ks, vs, dtype_of(k, "k"), ptr<int64_t>(slots),
-                           status_of(a[4]), stream_of(a[5], k)));
+                           to.status, to.stream));
   });
 }
 
@@ -288,11 +309,12 @@ PyObject* py_cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     flat(table, "block_table", at::kInt, {b, -1});
     if (lse) flat(*lse, "lse", at::kFloat, {t, h});
     flat(work, "workspace", at::kByte, {-1});
+    const Launch to(a[10], a[11]);
     check(smp_cache_attention(&c, at_of(q), small(t, "tokens"), small(h, "heads"), qs, dtype_of(q, "q"),
                               ptr<int32_t>(start), ptr<int32_t>(lens), small(b, "batch"), ptr<int32_t>(table),
                               small(table.size(1), "block_table"), float(number(a[5])), integer32(a[6], "window"),
-                              at_of(out), os, ptr<float>(lse), status_of(a[10]), at_of(work), size_t(work.numel()),
-                              stream_of(a[11], q)));
+                              at_of(out), os, ptr<float>(lse), to.status, at_of(work), size_t(work.numel()),
+                              to.stream));
   });
 }
 
@@ -318,9 +340,10 @@ PyObject* py_spec_verify_probs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (lens) flat(*lens, "draft_lens", at::kInt, {b});
     flat(accepted, "out_accepted", at::kInt, {b});
     flat(out, "out_ids", at::kInt, {b, k + 1});
+    const Launch to(a[8], a[9]);
     check(smp_spec_verify_probs(at_of(p), at_of(q), ptr<int32_t>(ids), ptr<int32_t>(lens), small(b, "batch"),
                                 small(k, "drafts"), small(v, "vocab"), dtype, ptr<float>(uniforms), ptr<float>(noise),
-                                ptr<int32_t>(accepted), ptr<int32_t>(out), status_of(a[8]), stream_of(a[9], p)));
+                                ptr<int32_t>(accepted), ptr<int32_t>(out), to.status, to.stream));
   });
 }
 

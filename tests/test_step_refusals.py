@@ -114,3 +114,40 @@ def test_the_python_layer_refuses_what_it_can_see():
     with pytest.raises(binding.SmpError):
         binding.spec_verify_probs(torch.zeros(1, 2, 8), None, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1),
                                   torch.zeros(1, 8))
+
+
+def test_tensors_of_two_gpus_are_refused():
+    # tensors that only claim a GPU: the answer comes before anything looks at their memory
+    torch = pytest.importorskip("torch")
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    if torch.cuda.is_available():
+        pytest.skip("claimed devices: only where no GPU is initialised for them")
+    i32, f32, i64 = torch.int32, torch.float32, torch.int64
+    with FakeTensorMode():
+        def t(*shape, dtype=i32):
+            return torch.empty(shape, dtype=dtype, device="cuda:0")
+
+        def kv():
+            codes = t(4, 2, 16, 32, dtype=torch.int8)
+            return codes, t(4, 2, 16, 32, dtype=torch.int8), t(4, 2, dtype=f32), t(4, 2, dtype=f32)
+
+        plan = dict(lens=t(2), add=t(2), held=t(2), free_blocks=t(5), free_head=t(1), block_table=t(2, 4), block_size=16,
+                    num_blocks=9, max_tokens=8, status=t(1))
+        rope = dict(q=t(4, 8, 32, dtype=f32), k=t(4, 2, 32, dtype=f32), positions=t(4), table=t(9, 32, dtype=f32),
+                    q_weight=t(32, dtype=f32), k_weight=t(32, dtype=f32), out_q=t(4, 8, 32, dtype=f32),
+                    out_k=t(4, 2, 32, dtype=f32), status=t(1))
+        append = dict(k=t(4, 2, 32, dtype=f32), v=t(4, 2, 32, dtype=f32), slots=t(4, dtype=i64), status=t(1))
+        attend = dict(q=t(4, 8, 32, dtype=f32), start=t(3), lens=t(2), block_table=t(2, 4), out=t(4, 8, 32, dtype=f32),
+                      lse=t(4, 8, dtype=f32), workspace=t(1 << 20, dtype=torch.uint8), status=t(1))
+        probs = dict(p=t(2, 4, 50, dtype=f32), q=t(2, 3, 50, dtype=f32), draft_ids=t(2, 3), uniforms=t(2, 3, dtype=f32),
+                     noise=t(2, 50, dtype=f32), draft_lens=t(2), out_accepted=t(2), out_ids=t(2, 4), status=t(1))
+        calls = [(cache.block_plan, plan), (cache.qk_norm_rope, rope), (lambda **kw: cache.cache_append(kv(), **kw), append),
+                 (lambda **kw: cache.cache_attention(kv(), **kw), attend), (binding.spec_verify_probs, probs)]
+        for call, good in calls:
+            for name, value in list(good.items())[1:]:
+                if isinstance(value, int):
+                    continue
+                other = torch.empty(value.shape, dtype=value.dtype, device="cuda:1")
+                with pytest.raises(binding.SmpError, match="must be on one GPU"):
+                    call(**dict(good, **{name: other}))
