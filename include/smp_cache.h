@@ -187,7 +187,8 @@ size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_heads, int3
  * Scores, sums and the weighted values are held in binary32; a key, a query
  * and a weight enter their products with at least bf16's precision (binary32
  * queries: 22 bits).  Cache positions that a query does not see do not
- * influence its result, whatever bytes they hold.
+ * influence its result, whatever bytes they hold, and neither do the scales of
+ * blocks of which it sees nothing.
  *
  *   q            device, [tokens, q_heads, head_dim] of `dtype`, heads
  *                contiguous, tokens q_stride elements apart.

@@ -694,8 +694,11 @@ __device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnS
     float v_scale[S::kMT];
 #pragma unroll
     for (int mt = 0; mt < S::kMT; ++mt) {
-      const float ks = scales[warp][meta][0][mt];
+      float ks = scales[warp][meta][0][mt];
       v_scale[mt] = scales[warp][meta][1][mt];
+      // a hidden weight is 0 times its value scale: one that is no number counts as 0, and the rows that do see its
+      // tokens get NaN from their scores
+      if (!(fabsf(v_scale[mt]) < INFINITY)) v_scale[mt] = 0.0f, ks = __int_as_float(0x7FC00000);
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
         const uint64_t c = mul2(pair(ks, ks), pair(factor[nt][0], factor[nt][1]));
