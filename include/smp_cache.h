@@ -206,7 +206,8 @@ size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_heads, int3
  * A start out of order or out of range makes its request's queries none, and a
  * length below 0 or above table_stride * block_size is cut to that range
  * (SMP_ROW_BAD_LENGTH); keys of a block id outside [0, num_blocks) are not
- * visible (SMP_ROW_BAD_BLOCK).
+ * visible (SMP_ROW_BAD_BLOCK).  Ids of blocks that the window of every query
+ * has left are not looked at: their pages may have been given back.
  */
 smp_status smp_cache_attention(const smp_cache* cache, const void* q, int32_t tokens, int32_t q_heads,
                                int64_t q_stride, smp_dtype dtype, const int32_t* start, const int32_t* lens,

@@ -483,7 +483,8 @@ __device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnS
   auto load_ids = [&](int k0) {
     const int k = k0 + lane / S::kMT, token = (tile_lo + k) * S::kTile + (warp * S::kMT + lane % S::kMT) * 16;
     int id = -1;
-    if (k < iters && token < len) {
+    // tokens that have left every row's window are not looked up: their pages may be gone
+    if (k < iters && token < len && (a.window == 0 || int64_t(token) + 15 + a.window > p_first)) {
       id = a.table[int64_t(b) * a.stride + (token >> a.shift)];
       if (id < 0 || id >= a.num_blocks) id = -1, flags |= kRowBadBlock;
     }

@@ -1,5 +1,6 @@
 """What a query of the cached step's attention does not see has no part in its
-result: NaN and infinite scales of hidden blocks.  Bounds: those of the attention's other tests (bf16
+result: NaN and infinite scales of hidden blocks, and block ids of pages that
+a window has left behind.  Bounds: those of the attention's other tests (bf16
 queries: 2^-9 of sum p |v| for the weights' two roundings, 2^-16 of the
 largest sum |q k| for the scores, 2^-8 of the result)."""
 
@@ -8,7 +9,7 @@ import pytest
 
 from oracle import step
 from spec_verify_gb300 import binding, cache
-from tests.test_gpu_step import attention_case, check_attention, host, i32, upload
+from tests.test_gpu_step import attention_case, check_attention, host, i32, status, upload
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,19 @@ def test_scales_of_a_later_drafts_block(which, bad, kind, dt):
     assert (np.abs(got[:4] - want[:4]) <= lim + 1e-30).all()
     if which == "v_scale" or np.isnan(bad):
         assert not np.isfinite(got[4:10]).any()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("window", [1, 20, 100, 129])
+def test_block_ids_before_the_window_are_not_reported(window, kind):
+    rng = np.random.default_rng(window)
+    arrays, table, start, lens, q = attention_case(rng, [5, 1, 12], [45, 700, 333], 8, 2, 64, 16, kind, "bf16")
+    freed = table.copy()
+    for b, n in enumerate(np.diff(start)):
+        freed[b, :max(0, lens[b] - n - window + 1) // 16] = -1   # pages given back: nobody sees their tokens
+    check_attention(arrays, kind, q, start, lens, freed, "bf16", window=window, flags=0)
+    b = 1
+    freed[b, max(0, lens[b] - 1 - window + 1) // 16] = -1        # the first page that request 1 does see
+    st = status()
+    cache.cache_attention(upload(arrays, kind), q, i32(start), i32(lens), i32(freed), window=window, status=st)
+    assert int(st) == binding.ROW_BAD_BLOCK
