@@ -186,9 +186,12 @@ size_t smp_cache_attention_workspace_bytes(int32_t tokens, int32_t q_heads, int3
  * over the visible keys; a query that sees none gets zeros (lse -inf).
  * Scores, sums and the weighted values are held in binary32; a key, a query
  * and a weight enter their products with at least bf16's precision (binary32
- * queries: 22 bits).  Cache positions that a query does not see do not
- * influence its result, whatever bytes they hold, and neither do the scales of
- * blocks of which it sees nothing.
+ * queries: 22 bits), weights far below a row's largest (p_j times the value
+ * scale) with an error of at most 2^-33 of it.  That holds for value scales of
+ * 2^-92 to 2^92; for those down to 2^-100, the least that smp_cache_append
+ * writes, the error is at most 2^-25.  Cache positions that a query does not
+ * see do not influence its result, whatever bytes they hold, and neither do
+ * the scales of blocks of which it sees nothing.
  *
  *   q            device, [tokens, q_heads, head_dim] of `dtype`, heads
  *                contiguous, tokens q_stride elements apart.

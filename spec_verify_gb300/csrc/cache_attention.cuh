@@ -9,7 +9,7 @@
 // which moves only when a weight P v passes 2^15, the range of 16-bit floats;
 // it then puts the row's largest weight at 2^8, and l and O are multiplied by
 // 2^(m_old - m_new).  Small weights keep all 11 bits down to 2^-22 of the
-// largest, whatever the blocks' scales; l is summed from binary32 P.
+// largest (value scales below 2^-92: kLeastScale); l is summed from binary32 P.
 //
 // Both products run on the tensor cores with the cache as the 16-row operand
 // (tokens, then head elements) and the query rows as the 8-wide one, so one
@@ -55,7 +55,9 @@ constexpr int kAttnUnitCost = 3;        // a unit's fixed cost, in tiles
 constexpr float kTopWeight = 8.0f;      // a new reference puts a row's largest weight at 2^8
 constexpr float kMostWeight = 15.0f;    // and is replaced once one passes 2^15
 constexpr uint32_t kWeightLimit = 0x7800u;   // that as a 16-bit float
-constexpr float kLeastScale = -60.0f;   // log2 of the smallest value scale that a reference follows: P stays finite
+// The smallest value scale that a reference follows: P stays below 2^107, and the sum of two million such weights
+// finite.  Of smaller scales, the largest weight is as much below 2^8 (2^-100: at 2^0, with 11 bits down to 2^-14 of it).
+constexpr float kLeastScale = 0x1p-92f;
 
 // A unit that is cut: where its rows are, and how many CTAs have parts of it.
 struct alignas(16) AttnJoin {
@@ -763,7 +765,10 @@ __device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnS
     };
     weigh();
     copies_wait<2 * (S::kDepth - 1) - 1>();    // this warp's values of the tile
-    const bool past = (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || has_ref != kAll;
+    bool past = (packed_max & 0xFFFFu) > kWeightLimit || (packed_max >> 16) > kWeightLimit || has_ref != kAll;
+#pragma unroll
+    for (int mt = 0; mt < S::kMT; ++mt)        // P can pass its bound there while P v does not (0 is the scale of no block)
+      past |= __float_as_uint(v_scale[mt]) - 1u < __float_as_uint(kLeastScale) - 1u;
     if (__syncthreads_or(past)) {
       // rare: the rows' largest weights over both warps' keys, and new references where they pass the limit
 #pragma unroll
@@ -773,7 +778,7 @@ __device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnS
           float y = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < S::kMT; ++mt)
-            y = fmaxf(y, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) + fmaxf(__log2f(v_scale[mt]), kLeastScale));
+            y = fmaxf(y, fmaxf(s[mt][nt][c], s[mt][nt][c + 2]) + __log2f(fmaxf(v_scale[mt], kLeastScale)));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(~0u, y, d));
           if (g == 0) row_part[warp][nt * 8 + 2 * t + c] = y;
@@ -788,10 +793,12 @@ __device__ __forceinline__ void attention_segment(const AttnArgs& a, const AttnS
           const uint32_t bit = 1u << (2 * nt + c);
           if ((has_ref & bit) ? y > kMostWeight : y > -INFINITY) {
             const float up = y - kTopWeight;
-            if (has_ref & bit) alpha[c] = exp2_approx(-up);
+            // in two steps: after blocks of the smallest scales, l has to take more than one factor of binary32 can
+            const float half = has_ref & bit ? exp2_approx(-0.5f * up) : 1.0f;
+            alpha[c] = half * half;
             has_ref |= bit;
             m[nt][c] += up;
-            l[nt][c] *= alpha[c];
+            l[nt][c] = l[nt][c] * half * half;
 #pragma unroll
             for (int mt = 0; mt < S::kMT; ++mt) s[mt][nt][c] -= up, s[mt][nt][c + 2] -= up;
           }
@@ -1048,9 +1055,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     float f = 0.0f;
     if (i0 + lane < u.parts) {
       const float m = part(i0 + lane)[rows * kDP + r], l = part(i0 + lane)[rows * (kDP + 1) + r];
-      // a part that saw only NaN has no reference, but a sum
-      f = l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : exp2_approx(m - top);
-      if (l != 0.0f) all += l * f;
+      // a part that saw only NaN has no reference, but a sum; factors in two steps, as in the main kernel
+      const float half = m == -INFINITY ? 1.0f : exp2_approx(0.5f * (m - top));
+      f = l == 0.0f ? 0.0f : half * half;
+      if (l != 0.0f) all += l * half * half;
     }
     const int count = min(32, u.parts - i0);
 #pragma unroll 8
