@@ -126,8 +126,10 @@ def step_module():
         load()
         path = _build.STEP_LIB
         if not os.path.exists(path):
-            raise SmpError(f"smp_step_binding.so is not built ({path}); run "
-                           "`python -m spec_verify_gb300.build` or __graft_entry__.build()")
+            lacks = _build.step_lacks()
+            raise SmpError(f"smp_step_binding.so is not built ({path}); " +
+                           (f"building it takes {lacks}, which this machine lacks" if lacks else
+                            "run `python -m spec_verify_gb300.build` or __graft_entry__.build()"))
         loader = importlib.machinery.ExtensionFileLoader("smp_step_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("smp_step_binding", loader))
         loader.exec_module(module)

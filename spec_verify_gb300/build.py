@@ -6,11 +6,13 @@
 Translation units compile in parallel; the library links the CUDA runtime
 statically, so it loads next to any PyTorch build.  The native marshalling of
 the cached step (csrc/step_binding.cpp) is a separate extension module, built
-against the PyTorch that is installed.
+against the PyTorch that is installed; a machine without what that takes gets
+libsmp.so alone.
 """
 
 import argparse
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -54,9 +56,25 @@ def _newest_input():
     return max(os.path.getmtime(p) for p in paths)
 
 
+def step_lacks():
+    """What the extension module needs and this machine lacks, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return "PyTorch"
+    torch = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return "PyTorch's headers"
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return "a PyTorch built for CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None if shutil.which("g++") else "g++"
+
+
 def up_to_date():
     newest = _newest_input()
-    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in (LIB, STEP_LIB))
+    wanted = (LIB,) if step_lacks() else (LIB, STEP_LIB)
+    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in wanted)
 
 
 def _compile(src, extra):
@@ -97,15 +115,17 @@ def _link_step(obj):
 
 
 def build(force=False, verbose=False, extra=()):
-    """Compile every CUDA source and link libsmp.so; returns the library path."""
+    """Compile every CUDA source and link libsmp.so, and the extension module
+    where this machine has what it takes; returns libsmp.so's path."""
     if not force and up_to_date():
         return LIB
+    lacks = step_lacks()
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra)
     if verbose:
         extra += ["-Xptxas", "-v"]
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        step = pool.submit(_compile_step)
+        step = None if lacks else pool.submit(_compile_step)
         results = list(pool.map(lambda s: _compile(s, extra), SOURCES))
     if verbose:
         for (_, log), src in zip(results, SOURCES):
@@ -117,7 +137,10 @@ def build(force=False, verbose=False, extra=()):
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_step(step.result())
+    if lacks:
+        sys.stderr.write(f"smp_step_binding.so is not built: this machine lacks {lacks} (libsmp.so does not need it)\n")
+    else:
+        _link_step(step.result())
     return LIB
 
 
