@@ -130,6 +130,9 @@ def step_module():
             raise SmpError(f"smp_step_binding.so is not built ({path}); " +
                            (f"building it takes {lacks}, which this machine lacks" if lacks else
                             "run `python -m spec_verify_gb300.build` or __graft_entry__.build()"))
+        if _build.step_version() != _torch().__version__:
+            raise SmpError(f"smp_step_binding.so was built against PyTorch {_build.step_version()}, this is "
+                           f"{_torch().__version__}; run `python -m spec_verify_gb300.build`")
         loader = importlib.machinery.ExtensionFileLoader("smp_step_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("smp_step_binding", loader))
         loader.exec_module(module)

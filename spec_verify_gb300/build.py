@@ -14,6 +14,7 @@ import argparse
 import concurrent.futures
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -71,10 +72,32 @@ def step_lacks():
     return None if shutil.which("g++") else "g++"
 
 
+def _torch_version():
+    """The installed PyTorch's version, where it can be had without importing it."""
+    where = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(where, "version.py")) as f:
+        found = re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M)
+    if found:
+        return found.group(1)
+    import torch
+    return str(torch.__version__)
+
+
+def step_version():
+    """The PyTorch that the extension module was built against, or None."""
+    try:
+        with open(STEP_LIB + ".torch") as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
 def up_to_date():
     newest = _newest_input()
     wanted = (LIB,) if step_lacks() else (LIB, STEP_LIB)
-    return all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in wanted)
+    if not all(os.path.exists(p) and os.path.getmtime(p) >= newest for p in wanted):
+        return False
+    return STEP_LIB not in wanted or step_version() == _torch_version()
 
 
 def _compile(src, extra):
@@ -112,6 +135,8 @@ def _link_step(obj):
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, STEP_LIB)
+    with open(STEP_LIB + ".torch", "w") as f:
+        f.write(_torch_version())
 
 
 def build(force=False, verbose=False, extra=()):

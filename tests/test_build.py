@@ -56,3 +56,20 @@ def test_an_extension_that_does_not_compile_leaves_libsmp_built(elsewhere, monke
     with pytest.raises(RuntimeError, match="not this one"):
         build.build()
     assert os.path.exists(build.LIB) and not os.path.exists(build.STEP_LIB)
+
+
+def test_an_extension_of_another_pytorch_is_not_loaded_but_built_again(elsewhere, monkeypatch):
+    torch = pytest.importorskip("torch")
+    for name in ("libsmp.so", "smp_step_binding.so"):
+        (elsewhere / name).write_text("")
+    stamp = elsewhere / "smp_step_binding.so.torch"
+    stamp.write_text(str(torch.__version__))
+    assert build.up_to_date()
+    stamp.write_text("1.0.0")
+    assert not build.up_to_date()
+    monkeypatch.setattr(binding, "_step", None)
+    monkeypatch.setattr(binding, "load", lambda: None)
+    with pytest.raises(binding.SmpError, match="built against PyTorch 1.0.0"):
+        binding.step_module()
+    stamp.unlink()
+    assert not build.up_to_date()
