@@ -69,7 +69,6 @@ extern "C" smp_status smp_cache_attention(const smp_cache* cache, const void* q,
   a.partial = reinterpret_cast<float*>(a.joins + device_sms(dev) * kAttnMaxCtas);
   a.q_vector = !misaligned(q, 16) && q_stride * int64_t(elem) % 16 == 0;
   a.out_vector = !misaligned(out, 4 * elem) && out_stride % 4 == 0;
-  a.min_share = 2;      // one request of 1 K keys: 13.9 us, 14.6 with 4, 16.5 with 6
   const int64_t rows = attention_rows(tokens, batch, a.group);
   const bool e4m3 = cache->type == SMP_CACHE_E4M3, split = dtype == SMP_F32;
   const cudaError_t err = e4m3 ? split ? attn_launch<SMP_CACHE_E4M3, true>(a, rows, dev, st)
