@@ -130,8 +130,8 @@ smp_status smp_block_plan(const int32_t* lens, const int32_t* add, const int32_t
  *   out_q, out_k   device, like q and k with their own strides; may be q and k
  *                  themselves with the same strides (in place), and must not
  *                  overlap them otherwise.
- *   head_dim 1 .. SMP_MAX_HEAD_DIM; tokens 0 .. 2^31-1; strides at least
- *   heads * head_dim.
+ *   head_dim 1 .. SMP_MAX_HEAD_DIM; tokens * (q_heads + k_heads) 0 .. 2^31-1;
+ *   strides at least heads * head_dim.
  */
 smp_status smp_qk_norm_rope(const void* q, const void* k, int32_t tokens, int32_t q_heads, int32_t k_heads,
                             int32_t head_dim, int64_t q_stride, int64_t k_stride, smp_dtype dtype,

@@ -15,8 +15,8 @@
 // (tokens, then head elements) and the query rows as the 8-wide one, so one
 // to eight rows waste nothing.  8-bit codes become 16-bit floats exactly in
 // registers.  A query row enters as 16-bit floats scaled by a power of two to
-// a largest element near 2^9: for bf16 queries that is exact down to 2^-33 of
-// the row's largest element; binary32 queries and their weights enter as a
+// a largest element near 2^9: a bf16 element's 8 bits are exact down to 2^-26
+// of the row's largest, smaller ones round to 2^-33 of it; binary32 queries and their weights enter as a
 // sum of two 16-bit floats (22 bits).
 //
 // Split.  The keys of all (request, row tile, key head) units form one line of
@@ -30,13 +30,18 @@
 // K and V stream through rings in shared memory by 16-byte asynchronous
 // copies, a tile ahead.
 //
-// Bound: HBM (one byte per code) for up to 8 rows per key head, then issue: the
-// conversions of codes, the softmax and the 8-wide products, whose rate is a
-// third of what the widest ones reach.  Measured on heads of 128 in e4m3, with
-// requests from a quarter of the longest up: 4 requests of up to 128 K keys,
-// int8, 8 rows: 128 us, 5.6 TB/s (83 % of a plain copy); 32 requests of up to
-// 4 K, 4 rows: 39.5 us, 4.0 TB/s; the same of up to 20 rows: 59 us, 2.9 TB/s;
-// 8 requests of up to 64 K, 40 rows: 208 us, 3.3 TB/s and 208 TFLOP/s.
+// Bound: HBM (one byte per code) for up to 8 rows per key head and long
+// contexts; then latency: two warps per scheduler run one tile's chain of
+// products, softmax, barrier and products with little beside it (40 rows: a
+// third of the issue slots and two fifths of the tensor pipe are busy; the
+// warps wait on fixed latencies and on instruction fetch).  Measured on heads
+// of 128 in e4m3, with requests from a quarter of the longest up: 4 requests
+// of up to 128 K keys, int8, 8 rows: 127 us, 5.7 TB/s (83 % of a plain copy);
+// 32 requests of up to 4 K, 4 or 8 rows: 40 us, 4.0 TB/s; the same of up to 20
+// rows: 59.5 us, 2.9 TB/s; 8 requests of up to 64 K, 40 rows: 211 us, 3.2 TB/s
+// and 205 TFLOP/s.  Prompts read and convert the keys again for every 40 rows:
+// 37 chunks of about 443 tokens, four query heads to a key head, over contexts
+// of up to 1.2 K: 1667 us, 73 TFLOP/s.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -52,7 +57,10 @@ namespace smp {
 
 constexpr int kAttnThreads = 64;
 constexpr int kAttnUnitCost = 3;        // a unit's fixed cost, in tiles
-constexpr int kAttnMinShare = 2;        // a CTA's smallest share, in tiles: one request of 1 K keys takes 13.9 us, 14.6 with 4
+// A CTA's smallest share, in tiles, for calls that do not fill the GPU.  More parts to join against fewer tiles in a
+// row: 8 requests of 300 keys take 13.3, 14.6 and 16.1 us with shares of 1, 2 and 4; one of 1 K 15.2, 13.8 and 14.7;
+// of 4 K 26.1, 21.1 and 18.3; of 8 K 28.8, 28.8 and 22.7.
+constexpr int kAttnMinShare = 2;
 constexpr float kTopWeight = 8.0f;      // a new reference puts a row's largest weight at 2^8
 constexpr float kMostWeight = 15.0f;    // and is replaced once one passes 2^15
 constexpr uint32_t kWeightLimit = 0x7800u;   // that as a 16-bit float
@@ -1109,8 +1117,8 @@ cudaError_t attn_launch_shape(const AttnArgs& a, int dev, cudaStream_t st) {
 // Kernels per head size: row tiles of up to 16 rows, whose smaller state leaves
 // room for five CTAs per SM, of 24, and of up to 40 (32 for heads of 256 and
 // binary32 queries), beyond which the registers spill.  8 rows of 32 requests of
-// up to 4 K keys: 39.5 us with the first and 49 with the second; 20 rows: 59 us
-// with the second and 82 with the third.  `rows` is what the host
+// up to 4 K keys: 40 us with the first and 49 with the second; 20 rows: 60 us
+// with the second and 82 to 88 with the third.  `rows` is what the host
 // expects of most requests; the kernel sees the longest itself, and takes
 // several row tiles, which read the keys again, where its largest is too small.
 template <int kType, bool kSplit, int kDP>

@@ -218,7 +218,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_probs_kernel(const ProbsAr
 // CTAs per request: as many as fit beside each other in one wave (four CTAs
 // per SM), while a CTA keeps 2000 elements.  256 rows of 128256: 61 us with 2
 // CTAs a row, 66 with 4 (a second, partial wave), 87 with 1; 32 rows of 32000:
-// 8.1 us with 8, 10.6 with 4, 9.9 with 16, so 16 are left to batches of few rows.
+// 7.6 us with 8, 10.1 with 4, 8.3 with 16 (of 128256: 17.3, 26.2 and 19.0), so
+// 16 are left to batches of few rows: 16 rows of 32000 6.9 us with 8 and 6.0
+// with 16, 1 row 6.6 and 5.2.  The limit is on the low side: 24 rows still take
+// 6.2 us with 16 and 7.2 with 8.
 static int probs_cluster(int batch, int vocab, int sms) {
   int c = 1;
   while (c < 16 && int64_t(batch) * c * 2 <= int64_t(sms) * 4 && vocab / (2 * c) >= 2000) c *= 2;
