@@ -182,6 +182,12 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
+def _needs(t, name, dims):
+    """Refuses what a call cannot take the shape of its own tensors from."""
+    if getattr(t, "is_cuda", None) is None or t.ndim != dims:
+        raise SmpError(f"{name} must be a torch tensor of {dims} dimension{'s' if dims > 1 else ''}")
+
+
 def params_to_device(params, device):
     """A [B] record array of smp_row_params as a device byte tensor."""
     torch = _torch()
@@ -473,6 +479,7 @@ def spec_verify_probs(p, q, draft_ids, uniforms, noise, draft_lens=None, out_acc
     word).  Returns (accepted_len int32 [B], ids int32 [B, K+1])."""
     native, torch = step_module(), _torch()
     if out_accepted is None or out_ids is None:
+        _needs(p, "p", 3)
         with _on(stream):
             if out_accepted is None:
                 out_accepted = torch.empty(p.shape[0], dtype=torch.int32, device=p.device)

@@ -15,7 +15,7 @@ What a call cannot take is refused with SmpError before anything is launched.
 
 import collections
 
-from .binding import _on, _torch, load, step_module
+from .binding import SmpError, _needs, _on, _torch, load, step_module
 
 BlockPlan = collections.namedtuple("BlockPlan", "lens held free_head start position request slot")
 
@@ -54,6 +54,9 @@ def block_plan(lens, add, held, free_blocks, free_head, block_table, block_size,
     native = step_module()
     if out is None:
         torch = _torch()
+        _needs(lens, "lens", 1)
+        if max_tokens < 0:
+            raise SmpError("max_tokens must not be negative")
         b, i32 = lens.shape[0], torch.int32
         new = lambda n, t=i32: torch.empty(n, dtype=t, device=lens.device)  # noqa: E731
         with _on(stream):
@@ -73,6 +76,9 @@ def qk_norm_rope(q, k, positions, table=None, q_weight=None, k_weight=None, eps=
     out_k)."""
     native = step_module()
     if out_q is None or (k is not None and out_k is None):
+        _needs(q, "q", 3)
+        if k is not None:
+            _needs(k, "k", 3)
         with _on(stream):
             if out_q is None:
                 out_q = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
@@ -105,12 +111,20 @@ def cache_attention(cache, q, start, lens, block_table, scale=None, window=0, ou
     native = step_module()
     if out is None or workspace is None:
         torch = _torch()
+        _needs(q, "q", 3)
+        _needs(lens, "lens", 1)
+        if not isinstance(cache, tuple) or len(cache) != 4:
+            raise SmpError("a cache is a tuple (k, v, k_scale, v_scale)")
+        _needs(cache[0], "k", 4)
         with _on(stream):
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             if workspace is None:
                 need = attention_workspace_bytes(q.shape[0], q.shape[1], cache[0].shape[1], q.shape[2], lens.shape[0])
                 workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
-    native.cache_attention(cache, q, start, lens, block_table, q.shape[2] ** -0.5 if scale is None else scale, window,
-                           out, lse, workspace, status, _queue(stream))
+    if scale is None:
+        _needs(q, "q", 3)
+        scale = max(1, q.shape[2]) ** -0.5
+    native.cache_attention(cache, q, start, lens, block_table, scale, window, out, lse, workspace, status,
+                           _queue(stream))
     return out

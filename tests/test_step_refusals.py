@@ -151,3 +151,28 @@ def test_tensors_of_two_gpus_are_refused():
                 other = torch.empty(value.shape, dtype=value.dtype, device="cuda:1")
                 with pytest.raises(binding.SmpError, match="must be on one GPU"):
                     call(**dict(good, **{name: other}))
+
+
+def test_no_outputs_are_made_for_what_is_refused():
+    # outputs and scratch left to the call: their shapes come from arguments that have to be looked at first
+    torch = pytest.importorskip("torch")
+    i32 = torch.int32
+    t = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    kv = (t(3, 2, 16, 32, dtype=torch.int8), t(3, 2, 16, 32, dtype=torch.int8), t(3, 2), t(3, 2))
+    plan = (t(2, dtype=i32), t(2, dtype=i32), t(5, dtype=i32), t(1, dtype=i32), t(2, 4, dtype=i32), 16, 5)
+    attend = (t(3, dtype=i32), t(2, dtype=i32), t(2, 4, dtype=i32))
+    probs = (t(2, 3, 50), t(2, 3, dtype=i32), t(2, 3), t(2, 50))
+    for call in (lambda: cache.block_plan(None, *plan, 8), lambda: cache.block_plan(t(dtype=i32), *plan, 8),
+                 lambda: cache.block_plan(t(2, dtype=i32), *plan, -1),
+                 lambda: cache.qk_norm_rope(None, None, t(4, dtype=i32)),
+                 lambda: cache.qk_norm_rope([[1.0]], None, t(4, dtype=i32)),
+                 lambda: cache.qk_norm_rope(t(4, 8, 32), [1.0], t(4, dtype=i32)),
+                 lambda: cache.cache_attention(kv, None, *attend), lambda: cache.cache_attention(kv, t(4, 8), *attend),
+                 lambda: cache.cache_attention(None, t(4, 8, 32), *attend),
+                 lambda: cache.cache_attention(kv[:1], t(4, 8, 32), *attend),
+                 lambda: cache.cache_attention(kv, t(4, 8, 32), t(3, dtype=i32), None, t(2, 4, dtype=i32)),
+                 lambda: cache.cache_attention(kv, None, *attend, out=t(4, 8, 32), workspace=t(9, dtype=torch.uint8)),
+                 lambda: cache.cache_attention(kv, t(4, 8, 0), *attend, out=t(4, 8, 0), workspace=t(9, dtype=torch.uint8)),
+                 lambda: binding.spec_verify_probs(None, *probs), lambda: binding.spec_verify_probs(t(2), *probs)):
+        with pytest.raises(binding.SmpError):
+            call()
