@@ -122,9 +122,6 @@ def cache_attention(cache, q, start, lens, block_table, scale=None, window=0, ou
             if workspace is None:
                 need = attention_workspace_bytes(q.shape[0], q.shape[1], cache[0].shape[1], q.shape[2], lens.shape[0])
                 workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
-    if scale is None:
-        _needs(q, "q", 3)
-        scale = max(1, q.shape[2]) ** -0.5
     native.cache_attention(cache, q, start, lens, block_table, scale, window, out, lse, workspace, status,
                            _queue(stream))
     return out

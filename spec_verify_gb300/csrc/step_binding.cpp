@@ -6,9 +6,11 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -117,10 +119,12 @@ void* stream_of(PyObject* o) {
 // What every call takes last; with it all tensors have been seen, and their GPU is the current one for the launch.
 struct Launch {
   int32_t* status;
-  c10::cuda::CUDAGuard on;
+  c10::cuda::OptionalCUDAGuard on;   // set where another GPU is current
   void* stream;
-  Launch(PyObject* status_arg, PyObject* stream_arg)
-      : status(status_of(status_arg)), on(c10::DeviceIndex(g_device)), stream(stream_of(stream_arg)) {}
+  Launch(PyObject* status_arg, PyObject* stream_arg) : status(status_of(status_arg)) {
+    if (c10::cuda::current_device() != g_device) on.set_index(c10::DeviceIndex(g_device));
+    stream = stream_of(stream_arg);
+  }
 };
 
 smp_dtype dtype_of(const Tensor& t, const char* name) {
@@ -290,7 +294,7 @@ PyObject* py_cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// cache, q, start, lens, table, scale, window, out, lse, workspace, status, stream
+// cache, q, start, lens, table, scale (None: head_dim^-0.5), window, out, lse, workspace, status, stream
 PyObject* py_cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&] {
     const smp_cache c = cache_of(a[0]);
@@ -308,11 +312,12 @@ PyObject* py_cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     flat(start, "start", at::kInt, {b + 1});
     flat(table, "block_table", at::kInt, {b, -1});
     if (lse) flat(*lse, "lse", at::kFloat, {t, h});
+    const double scale = a[5] == Py_None ? std::pow(double(c.head_dim > 0 ? c.head_dim : 1), -0.5) : number(a[5]);
     flat(work, "workspace", at::kByte, {-1});
     const Launch to(a[10], a[11]);
     check(smp_cache_attention(&c, at_of(q), small(t, "tokens"), small(h, "heads"), qs, dtype_of(q, "q"),
                               ptr<int32_t>(start), ptr<int32_t>(lens), small(b, "batch"), ptr<int32_t>(table),
-                              small(table.size(1), "block_table"), float(number(a[5])), integer32(a[6], "window"),
+                              small(table.size(1), "block_table"), float(scale), integer32(a[6], "window"),
                               at_of(out), os, ptr<float>(lse), to.status, at_of(work), size_t(work.numel()),
                               to.stream));
   });
