@@ -27,13 +27,15 @@ ROW_BAD_DRAFT = 8
 ROW_BAD_LENGTH = 16
 ROW_NO_CAPACITY = 32
 ROW_BAD_BLOCK = 64
+ROW_BAD_TOKEN = 128
 
-# Symbols declared in include/smp.h and include/smp_cache.h.
+# Symbols declared in include/smp.h, include/smp_cache.h and include/smp_scores.h.
 EXPORTS = ("smp_sample", "smp_filter_debug", "smp_sample_processed", "smp_sample_rows", "smp_logit_prepass",
            "smp_beam_topk_workspace_bytes", "smp_beam_topk", "smp_spec_verify_workspace_bytes",
            "smp_spec_verify", "smp_spec_verify_params", "smp_spec_verify_rows", "smp_spec_verify_static",
            "smp_spec_verify_probs", "smp_block_plan", "smp_qk_norm_rope", "smp_cache_append",
-           "smp_cache_attention_workspace_bytes", "smp_cache_attention", "smp_status_string", "smp_last_cuda_error", "smp_abi_version")
+           "smp_cache_attention_workspace_bytes", "smp_cache_attention", "smp_token_logprobs",
+           "smp_token_logprobs_grad", "smp_distill", "smp_status_string", "smp_last_cuda_error", "smp_abi_version")
 
 STATIC_VERIFY_SCRATCH_BYTES = 1 << 20
 
@@ -105,6 +107,12 @@ def load():
     lib.smp_cache_attention.argtypes = [vp, vp, i32, i32, i64, i32, vp, vp, i32, vp, i32, f32, i32, vp, i64, vp, vp,
                                         vp, sz, vp]
     lib.smp_cache_attention.restype = i32
+    lib.smp_token_logprobs.argtypes = [vp, i32, i32, i64, i32, f32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.smp_token_logprobs.restype = i32
+    lib.smp_token_logprobs_grad.argtypes = [vp, i32, i32, i64, i32, f32, vp, vp, i32, vp, vp, vp, i64, vp, vp]
+    lib.smp_token_logprobs_grad.restype = i32
+    lib.smp_distill.argtypes = [vp, i32, i32, i64, i32, f32, vp, vp, vp, i32, i32, vp, vp, vp, i64, vp, vp]
+    lib.smp_distill.restype = i32
     lib.smp_status_string.argtypes = [i32]
     lib.smp_status_string.restype = ctypes.c_char_p
     lib.smp_last_cuda_error.argtypes = []
@@ -116,7 +124,8 @@ def load():
 
 
 def step_module():
-    """The native marshalling of the cached step (csrc/step_binding.cpp)."""
+    """The native marshalling of the cached step and of the calls on rows of
+    logits (csrc/step_binding.cpp)."""
     global _step
     if _step is None:
         import importlib.machinery

@@ -31,9 +31,9 @@ STEP_LIB = os.path.join(BUILD, "smp_step_binding.so")
 
 SOURCES = ["api.cu", "sample.cu", "verify.cu", "prepass.cu", "beam.cu", "verify_probs.cu", "block_plan.cu",
            "norm_rope.cu", "cache_append.cu", "cache_attention.cu", "attention_e4m3_bf16.cu",
-           "attention_e4m3_f32.cu", "attention_i8_bf16.cu", "attention_i8_f32.cu"]
+           "attention_e4m3_f32.cu", "attention_i8_bf16.cu", "attention_i8_f32.cu", "token_logprobs.cu", "distill.cu"]
 HEADERS = ["common.cuh", "row_ops.cuh", "select.cuh", "general.cuh", "launch.h", "exp_table.h", "tma.cuh", "general_bf16.cuh",
-           "cache.cuh", "cache_attention.cuh", "attention_rows.h"]
+           "cache.cuh", "cache_attention.cuh", "attention_rows.h", "scores.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -52,7 +52,7 @@ def nvcc():
 
 def _newest_input():
     paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    paths += [os.path.join(INCLUDE, f) for f in ("smp.h", "smp_cache.h")]
+    paths += [os.path.join(INCLUDE, f) for f in ("smp.h", "smp_cache.h", "smp_scores.h")]
     paths += [os.path.abspath(__file__), STEP_SOURCE]
     return max(os.path.getmtime(p) for p in paths)
 

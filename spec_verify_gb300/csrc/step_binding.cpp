@@ -1,7 +1,8 @@
 // Native marshalling of the cached speculative step's calls (smp_cache.h and
-// smp_spec_verify_probs): torch tensors in, argument checks, one call of the
-// C ABI on the current stream.  A step makes several of these calls, each a
-// few microseconds of kernel, so the checks run here and not in Python.
+// smp_spec_verify_probs) and of those on rows of logits (smp_scores.h): torch
+// tensors in, argument checks, one call of the C ABI on the current stream.  A
+// step makes several of these calls, each a few microseconds of kernel, so the
+// checks run here and not in Python.
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>
@@ -17,6 +18,7 @@
 
 #include "smp.h"
 #include "smp_cache.h"
+#include "smp_scores.h"
 
 namespace {
 
@@ -145,6 +147,34 @@ int64_t heads_of(const Tensor& t, const char* name, const Tensor* like = nullptr
     refuse("the heads of " + std::string(name) + " must be contiguous and its tokens in order");
   return n > 1 ? t.stride(0) : row;
 }
+
+// The row stride of a [rows, vocab] tensor whose rows are contiguous.
+int64_t rows_of(const Tensor& t, const char* name, const Tensor* like = nullptr) {
+  if (t.dim() != 2) refuse(std::string(name) + " must be [rows, vocab]");
+  dtype_of(t, name);
+  if (like && (t.scalar_type() != like->scalar_type() || t.sizes() != like->sizes()))
+    refuse(std::string(name) + " must have the type and shape " + shape_text(like->sizes()) + ", got " +
+           c10::toString(t.scalar_type()) + " " + shape_text(t.sizes()));
+  const int64_t n = t.size(0), v = t.size(1);
+  if ((v > 1 && t.stride(1) != 1) || (n > 1 && t.stride(0) < v))
+    refuse("the rows of " + std::string(name) + " must be contiguous and in order");
+  return n > 1 ? t.stride(0) : v;
+}
+
+// A temperature: a number, or a float32 tensor of one per row.
+struct Temperature {
+  float one = 1.0f;
+  const float* each = nullptr;
+  Temperature(PyObject* o, int64_t rows) {
+    if (THPVariable_Check(o)) {
+      const Tensor& t = tensor(o, "temperature");
+      flat(t, "temperature", at::kFloat, {rows});
+      each = static_cast<const float*>(t.data_ptr());
+    } else {
+      one = float(number(o));
+    }
+  }
+};
 
 smp_cache cache_of(PyObject* o) {
   if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) refuse("a cache is a tuple (k, v, k_scale, v_scale)");
@@ -352,6 +382,89 @@ PyObject* py_spec_verify_probs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// logits, ids, top, temperature, out_logprobs, out_entropy, out_top_ids, out_top_logprobs, status, stream
+PyObject* py_token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&] {
+    const Tensor& logits = tensor(a[0], "logits");
+    const Tensor* ids = optional(a[1], "ids");
+    const int32_t top = integer32(a[2], "top");
+    const Tensor* logprobs = optional(a[4], "out.logprobs");
+    const Tensor* entropy = optional(a[5], "out.entropy");
+    const Tensor* top_ids = optional(a[6], "out.top_ids");
+    const Tensor* top_logprobs = optional(a[7], "out.top_logprobs");
+    const int64_t stride = rows_of(logits, "logits"), rows = logits.size(0);
+    int64_t count = 0;
+    if (ids) {
+      flat(*ids, "ids", at::kInt, {rows, -1});
+      count = ids->size(1);
+    }
+    if (bool(ids) != bool(logprobs)) refuse("out.logprobs goes with ids");
+    if (logprobs) flat(*logprobs, "out.logprobs", at::kFloat, {rows, count});
+    if (entropy) flat(*entropy, "out.entropy", at::kFloat, {rows});
+    if (bool(top_ids) != (top > 0) || bool(top_logprobs) != (top > 0)) refuse("out.top_ids and out.top_logprobs go with top");
+    if (top_ids) flat(*top_ids, "out.top_ids", at::kInt, {rows, top});
+    if (top_logprobs) flat(*top_logprobs, "out.top_logprobs", at::kFloat, {rows, top});
+    const Temperature temperature(a[3], rows);
+    const Launch to(a[8], a[9]);
+    check(smp_token_logprobs(at_of(logits), small(rows, "rows"), small(logits.size(1), "vocab"), stride,
+                             dtype_of(logits, "logits"), temperature.one, temperature.each, ptr<int32_t>(ids),
+                             small(count, "ids"), top, ptr<float>(logprobs), ptr<float>(entropy), ptr<int32_t>(top_ids),
+                             ptr<float>(top_logprobs), to.status, to.stream));
+  });
+}
+
+// logits, ids, grad_logprobs, grad_entropy, temperature, out, status, stream
+PyObject* py_token_logprobs_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const Tensor& logits = tensor(a[0], "logits");
+    const Tensor* ids = optional(a[1], "ids");
+    const Tensor* up = optional(a[2], "grad_logprobs");
+    const Tensor* up_entropy = optional(a[3], "grad_entropy");
+    const Tensor& out = tensor(a[5], "out");
+    const int64_t stride = rows_of(logits, "logits"), out_stride = rows_of(out, "out", &logits), rows = logits.size(0);
+    int64_t count = 0;
+    if (bool(ids) != bool(up)) refuse("grad_logprobs goes with ids");
+    if (ids) {
+      flat(*ids, "ids", at::kInt, {rows, -1});
+      count = ids->size(1);
+      flat(*up, "grad_logprobs", at::kFloat, {rows, count});
+    }
+    if (up_entropy) flat(*up_entropy, "grad_entropy", at::kFloat, {rows});
+    const Temperature temperature(a[4], rows);
+    const Launch to(a[6], a[7]);
+    check(smp_token_logprobs_grad(at_of(logits), small(rows, "rows"), small(logits.size(1), "vocab"), stride,
+                                  dtype_of(logits, "logits"), temperature.one, temperature.each, ptr<int32_t>(ids),
+                                  small(count, "ids"), ptr<float>(up), ptr<float>(up_entropy), at_of(out), out_stride,
+                                  to.status, to.stream));
+  });
+}
+
+// logits, teacher_ids, teacher_logprobs, tail, temperature, weight, out_loss, out (None: the loss alone), status, stream
+PyObject* py_distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&] {
+    const Tensor& logits = tensor(a[0], "logits");
+    const Tensor& ids = tensor(a[1], "teacher_ids");
+    const Tensor& values = tensor(a[2], "teacher_logprobs");
+    const Tensor* weight = optional(a[5], "weight");
+    const Tensor& loss = tensor(a[6], "out_loss");
+    const Tensor* out = optional(a[7], "out");
+    const int64_t stride = rows_of(logits, "logits"), rows = logits.size(0);
+    const int64_t out_stride = out ? rows_of(*out, "out", &logits) : 0;
+    flat(ids, "teacher_ids", at::kInt, {rows, -1});
+    flat(values, "teacher_logprobs", at::kFloat, {rows, ids.size(1)});
+    if (weight) flat(*weight, "weight", at::kFloat, {rows});
+    flat(loss, "out_loss", at::kFloat, {rows});
+    const int tail = PyObject_IsTrue(a[3]);
+    if (tail < 0) throw Refused("");
+    const Temperature temperature(a[4], rows);
+    const Launch to(a[8], a[9]);
+    check(smp_distill(at_of(logits), small(rows, "rows"), small(logits.size(1), "vocab"), stride, dtype_of(logits, "logits"),
+                      temperature.one, temperature.each, ptr<int32_t>(ids), ptr<float>(values),
+                      small(ids.size(1), "teacher_ids"), tail, ptr<float>(weight), ptr<float>(loss), at_of(out), out_stride,
+                      to.status, to.stream));
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -363,6 +476,9 @@ PyMethodDef g_methods[] = {method<py_set_error>("set_error"),
                            method<py_cache_append>("cache_append"),
                            method<py_cache_attention>("cache_attention"),
                            method<py_spec_verify_probs>("spec_verify_probs"),
+                           method<py_token_logprobs>("token_logprobs"),
+                           method<py_token_logprobs_grad>("token_logprobs_grad"),
+                           method<py_distill>("distill"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "smp_step_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,378 @@
+// Log probabilities of given tokens, entropies and likeliest tokens of rows of
+// logits, and the gradient of log probabilities and entropies.
+//
+// Bound: the forward call reads every logit once from HBM, the gradient reads
+// and writes them once (scores.cuh says how a row stays on chip).
+//
+// Likeliest tokens: each CTA finds the `top` largest of its slice before the
+// cluster's barrier, so that the lists travel with the sums.  The n-th largest
+// of its 256 threads' maxima is at most the slice's n-th largest element, since
+// n threads each hold an element that large: everything at or above it (a few
+// more than n) is collected and ranked by comparing packed (value, id) words.
+// The first CTA of the cluster merges the sorted lists by binary search.
+#include <cuda_runtime.h>
+
+#include "scores.cuh"
+
+namespace smp {
+
+constexpr int kCandidates = 512;   // collected before the slow exact way takes over
+
+struct ScoreArgs {
+  RowsArgs rows;
+  const int32_t* ids;
+  int count, top;
+  float* logprobs;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+
+struct ScoreGradArgs {
+  RowsArgs rows;
+  const int32_t* ids;
+  int count;
+  const float* up;           // gradients of the log probabilities
+  const float* up_entropy;
+  void* grad;
+  int64_t grad_stride;
+};
+
+// The `top` largest elements of the slice, in order, as packed words (0: none)
+// to `list` of the cluster's first CTA.
+template <typename T>
+__device__ void slice_top(const Slice<T>& s, float mine, int top, uint64_t* cand, uint64_t* list, int ranks,
+                          uint64_t* scratch, int* found) {
+  const int tid = int(threadIdx.x), lane = tid & 31;
+  // 16 bits of the order key: the largest value that `top` of the threads' maxima reach
+  const uint32_t key = key_of_bits(__float_as_uint(mine)) >> 16;
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int bit = 15; bit >= 0; --bit)
+    if (cta_sync_count(key >= (bound | 1u << bit)) >= top) bound |= 1u << bit;
+  const uint32_t least = max(bound << 16, kKeyNegInf + 1u);
+  if (tid == 0) *found = 0;
+  __syncthreads();
+  // a warp looks through one thread's vectors at a time, all lanes together
+  for (unsigned hits = __ballot_sync(~0u, key >= bound && key >= (least >> 16)); hits; hits &= hits - 1) {
+    const int who = (tid & ~31) + __ffs(hits) - 1;
+    constexpr int kPer = RowVec<T>::kPer;
+    const int own = s.vecs > who ? (s.vecs - who + kThreads - 1) / kThreads : 0;
+    for (int i = lane; i < own * kPer; i += 32) {
+      const int at = (who + (i / kPer) * kThreads) * kPer + i % kPer;
+      const uint32_t k = key_of_bits(Elem<T>::bits(s.buf[at]));
+      if (k >= least) {
+        const int place = atomicAdd(found, 1);
+        if (place < kCandidates) cand[place] = pack_key_id(k, uint32_t(s.first + at));
+      }
+    }
+  }
+  __syncthreads();
+  const int have = *found;
+  const uint32_t to = ranks > 1 ? map_rank(smem_addr(list), 0) : 0;
+  auto put = [&](int place, uint64_t v) {
+    if (ranks > 1) st_cluster_u64(to + uint32_t(place) * 8u, v);
+    else list[place] = v;
+  };
+  if (have <= kCandidates) {
+    for (int i = tid; i < have; i += kThreads) {
+      const uint64_t v = cand[i];
+      int rank = 0;
+      for (int j = 0; j < have; ++j) rank += cand[j] > v;
+      if (rank < top) put(rank, v);
+    }
+    for (int i = have + tid; i < top; i += kThreads) put(i, 0);
+  } else {   // many equal values: one maximum after another, each below the last
+    uint64_t last = ~0ull;
+    for (int n = 0; n < top; ++n) {
+      uint64_t best = 0;
+      for (int j = tid; j < s.vecs * RowVec<T>::kPer; j += kThreads) {
+        const uint32_t k = key_of_bits(Elem<T>::bits(s.buf[j]));
+        const uint64_t v = k > kKeyNegInf ? pack_key_id(k, uint32_t(s.first + j)) : 0;
+        if (v < last && v > best) best = v;
+      }
+      best = block_max_u64(best, scratch);
+      if (tid == 0) put(n, best);
+      if (best == 0) {
+        for (int i = n + 1 + tid; i < top; i += kThreads) put(i, 0);
+        break;
+      }
+      last = best;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ Meeting meet;
+  __shared__ uint64_t bar, scratch[kWarps];
+  __shared__ int found;
+  const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  allow_dependent_launch();
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  cluster_arrive_early(ranks);
+
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  const float temperature = row_temperature(a.rows, row);
+  const int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  const bool wanted = a.entropy || a.top > 0 || __syncthreads_or(id >= 0);
+  const bool fits = temperature_fits(temperature);
+  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
+  uint64_t* cand = reinterpret_cast<uint64_t*>(dynamic + size_t(a.rows.slice) * sizeof(T));
+  uint64_t* lists = cand + kCandidates;
+  const float c = __fdiv_rn(kLog2e, temperature);
+  float* logprobs = a.logprobs + int64_t(row) * a.count;
+
+  if (!wanted) {   // every id is padding
+    cluster_all_run(ranks);
+    if (rank == 0 && tid < a.count) logprobs[tid] = 0.0f;
+    return;
+  }
+  int flags = fits ? 0 : kRowBadParams;
+  Stats all{-INFINITY, 0.0f, 0.0f};
+  if (fits) {
+    s.load(z, a.rows.vocab, &bar);
+    const bool late = slice_is_late(&bar, a.rows.wait_limit);
+    const float mine = thread_top(s);
+    const Stats part = a.entropy ? warp_stats<T, true>(s, mine, temperature, c) : warp_stats<T, false>(s, mine, temperature, c);
+    if (lane == 0) meet.warp[warp] = part;
+    cluster_all_run(ranks);
+    if (a.top > 0) slice_top(s, mine, a.top, cand, lists + rank * a.top, ranks, scratch, &found);
+    __syncthreads();
+    if (warp == 0) {
+      const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
+      post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
+    }
+    cluster_meet(ranks);
+    const float4 p = posted(meet, ranks);
+    all = warp_join(Stats{p.x, p.y, p.z}, c);
+    if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
+    if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
+  } else {
+    cluster_all_run(ranks);
+  }
+  const float nan = __uint_as_float(0x7FC00000u), log_z = logf(all.z);
+  auto logprob = [&](float value) { return __fsub_rn(__fdiv_rn(__fsub_rn(value, all.m), temperature), log_z); };
+  if (tid < a.count) {
+    const bool past = id >= a.rows.vocab;
+    if (flags == 0 && s.holds(id)) logprobs[tid] = logprob(s.at(id));
+    else if (rank == 0 && (id < 0 || past || flags)) logprobs[tid] = id < 0 ? 0.0f : nan;
+    if (rank == 0 && past && a.rows.status) atomicOr(a.rows.status, kRowBadToken);
+  }
+  if (rank != 0) return;
+  if (tid == 0) {
+    if (flags && a.rows.status) atomicOr(a.rows.status, flags);
+    if (a.entropy) a.entropy[row] = flags ? nan : __fsub_rn(log_z, __fdiv_rn(all.s, __fmul_rn(temperature, all.z)));
+  }
+  if (a.top > 0) {
+    int32_t* top_ids = a.top_ids + int64_t(row) * a.top;
+    float* top_logprobs = a.top_logprobs + int64_t(row) * a.top;
+    if (flags) {
+      for (int i = tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = nan;
+      return;
+    }
+    // how many of the lists' entries are tokens, at most `top`
+    int some = 0;
+    for (int e = tid; e < ranks * a.top; e += kThreads) some += lists[e] != 0;
+    if (tid == 0) found = 0;
+    __syncthreads();
+    if (some) atomicAdd(&found, some);
+    for (int e = tid; e < ranks * a.top; e += kThreads) {
+      const uint64_t v = lists[e];
+      if (v == 0) continue;
+      const int from = e / a.top;
+      int place = e - from * a.top;
+      for (int r = 0; r < ranks && place < a.top; ++r) {
+        if (r == from) continue;
+        int lo = 0, hi = a.top;   // the entries of list r above v
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (lists[r * a.top + mid] > v) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
+      }
+      if (place < a.top) {
+        top_ids[place] = int32_t(~uint32_t(v));
+        top_logprobs[place] = logprob(value_of_key(uint32_t(v >> 32)));
+      }
+    }
+    __syncthreads();
+    for (int i = found + tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = -INFINITY;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_grad_kernel(const __grid_constant__ ScoreGradArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ Meeting meet;
+  __shared__ uint64_t bar;
+  __shared__ int ids[kMaxIds];
+  __shared__ float up[kMaxIds];
+  constexpr int kPer = RowVec<T>::kPer;
+  const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  allow_dependent_launch();
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  cluster_arrive_early(ranks);
+
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  T* out = static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride;
+  const float temperature = row_temperature(a.rows, row);
+  int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  const float h = a.up_entropy ? a.up_entropy[row] : 0.0f;
+  if (tid < kMaxIds) {
+    ids[tid] = id;
+    up[tid] = id >= 0 ? a.up[int64_t(row) * a.count + tid] : 0.0f;
+  }
+  const bool wanted = __syncthreads_or(id >= 0) || h != 0.0f;
+  const bool past = __syncthreads_or(id >= a.rows.vocab);
+  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
+  const float c = __fdiv_rn(kLog2e, temperature);
+  int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
+  if (past) flags |= kRowBadToken;
+  if (!wanted || flags) {
+    cluster_all_run(ranks);
+    if (wanted && rank == 0 && tid == 0 && a.rows.status) atomicOr(a.rows.status, flags);
+    s.fill(wanted ? __uint_as_float(0x7FC00000u) : 0.0f);
+    s.store(out);
+    return;
+  }
+  s.load(z, a.rows.vocab, &bar);
+  float sum_here = 0.0f;   // this id's gradients, over all its places
+  const bool first = tid < a.count && first_of_id(ids, up, a.count, tid, sum_here);
+  float g = 0.0f;          // and the row's
+  for (int i = lane; i < a.count; i += 32) g += up[i];
+  g = warp_sum_f(g);
+  const bool late = slice_is_late(&bar, a.rows.wait_limit);
+  const bool own = first && s.holds(id);
+  const float value = own ? s.at(id) : 0.0f;
+  const float mine = thread_top(s);
+  const Stats part = h != 0.0f ? warp_stats<T, true>(s, mine, temperature, c) : warp_stats<T, false>(s, mine, temperature, c);
+  if (lane == 0) meet.warp[warp] = part;
+  cluster_all_run(ranks);
+  __syncthreads();
+  if (warp == 0) {
+    const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
+    post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
+  }
+  cluster_meet(ranks);
+  const float4 p = posted(meet, ranks);
+  const Stats all = warp_join(Stats{p.x, p.y, p.z}, c);
+  if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
+  if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
+  if (flags) {
+    if (rank == 0 && tid == 0 && a.rows.status) atomicOr(a.rows.status, flags);
+    s.fill(__uint_as_float(0x7FC00000u));
+    s.store(out);
+    return;
+  }
+  // ln p_j + H = d / T - S / (T Z):  dz_j = e_j (A + B d_j), the ids' own g besides
+  const float inv_t = __fdiv_rn(1.0f, temperature), inv_z = __fdiv_rn(1.0f, all.z);
+  const float mean_d = __fmul_rn(all.s, inv_z);   // sum p d
+  const float ht = __fmul_rn(h, inv_t);
+  const float ca = -__fmul_rn(__fmul_rn(__fmaf_rn(-ht, mean_d, g), inv_t), inv_z), cb = -__fmul_rn(__fmul_rn(ht, inv_t), inv_z);
+  const uint32_t floor = floor_word<T>(all.m, temperature);
+  auto sweep = [&](auto weighted) {
+    for (int j = tid; j < s.vecs; j += kThreads) {
+      float v[kPer];
+      RowVec<T>::get(s.vec()[j], floor, v);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float d = __fsub_rn(v[i], all.m), e = ex2_approx(__fmul_rn(d, c));
+        v[i] = weighted ? __fmaf_rn(cb, __fmul_rn(e, d), __fmul_rn(e, ca)) : __fmul_rn(e, ca);   // cb d may overflow, e d not
+      }
+      s.vec()[j] = RowVec<T>::put(v);
+    }
+  };
+  if (h != 0.0f && !is_lowest<T>(all.m)) sweep(std::true_type{});
+  else sweep(std::false_type{});
+  __syncthreads();
+  if (own) {
+    const float d = __fsub_rn(value, all.m), e = ex2_approx(__fmul_rn(d, c));
+    const float base = e == 0.0f ? 0.0f : __fmaf_rn(cb, __fmul_rn(e, d), __fmul_rn(e, ca));
+    store1(s.buf + (id - s.first), __fmaf_rn(sum_here, inv_t, base));
+  }
+  s.store(out);
+}
+
+template <typename T>
+static smp_status launch_scores(const ScoreArgs& a, cudaStream_t st) {
+  const size_t extra = a.top > 0 ? (kCandidates + size_t(kMaxRanks) * a.top) * 8 : 0;
+  return launch_rows(reinterpret_cast<const void*>(&token_logprobs_kernel<T>), a, int(sizeof(T)), extra, st);
+}
+template <typename T>
+static smp_status launch_scores_grad(const ScoreGradArgs& a, cudaStream_t st) {
+  return launch_rows(reinterpret_cast<const void*>(&token_logprobs_grad_kernel<T>), a, int(sizeof(T)), 0, st);
+}
+
+}  // namespace smp
+
+extern "C" smp_status smp_token_logprobs(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype,
+                                         float temperature, const float* temperatures, const int32_t* ids, int32_t count,
+                                         int32_t top, float* out_logprobs, float* out_entropy, int32_t* out_top_ids,
+                                         float* out_top_logprobs, int32_t* status, void* stream) {
+  using namespace smp;
+  const smp_status ok = check_rows(logits, rows, vocab, stride, dtype, temperature, temperatures, status);
+  if (ok != SMP_OK) return ok;
+  if (count < 0 || count > SMP_MAX_ROW_IDS || top < 0 || top > SMP_MAX_ROW_IDS) return SMP_ERR_INVALID_ARG;
+  if (count == 0 && top == 0 && !out_entropy) return SMP_ERR_INVALID_ARG;
+  if (rows > 0 && ((count > 0 && (!ids || !out_logprobs)) || (top > 0 && (!out_top_ids || !out_top_logprobs))))
+    return SMP_ERR_INVALID_ARG;
+  if (misaligned(ids, 4) || misaligned(out_logprobs, 4) || misaligned(out_entropy, 4) || misaligned(out_top_ids, 4) ||
+      misaligned(out_top_logprobs, 4))
+    return SMP_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status) {
+    const smp_status rc = clear_status(status, st);
+    if (rc != SMP_OK) return rc;
+  }
+  if (rows == 0) return SMP_OK;
+  ScoreArgs a{};
+  a.rows.logits = logits, a.rows.stride = stride, a.rows.rows = rows, a.rows.vocab = vocab;
+  a.rows.temperature = temperature, a.rows.temperatures = temperatures, a.rows.status = status;
+  a.ids = ids, a.count = count, a.top = top;
+  a.logprobs = out_logprobs, a.entropy = out_entropy, a.top_ids = out_top_ids, a.top_logprobs = out_top_logprobs;
+  return dtype == SMP_F32 ? launch_scores<float>(a, st) : launch_scores<uint16_t>(a, st);
+}
+
+extern "C" smp_status smp_token_logprobs_grad(const void* logits, int32_t rows, int32_t vocab, int64_t stride,
+                                              smp_dtype dtype, float temperature, const float* temperatures,
+                                              const int32_t* ids, int32_t count, const float* grad_logprobs,
+                                              const float* grad_entropy, void* out_grad, int64_t grad_stride,
+                                              int32_t* status, void* stream) {
+  using namespace smp;
+  const smp_status ok = check_rows(logits, rows, vocab, stride, dtype, temperature, temperatures, status);
+  if (ok != SMP_OK) return ok;
+  if (count < 0 || count > SMP_MAX_ROW_IDS) return SMP_ERR_INVALID_ARG;
+  if (count == 0 && !grad_entropy) return SMP_ERR_INVALID_ARG;
+  if (!grad_fits(logits, rows, vocab, stride, out_grad, grad_stride)) return SMP_ERR_INVALID_ARG;
+  if (rows > 0 && (!out_grad || (count > 0 && (!ids || !grad_logprobs)))) return SMP_ERR_INVALID_ARG;
+  if (misaligned(ids, 4) || misaligned(grad_logprobs, 4) || misaligned(grad_entropy, 4) ||
+      misaligned(out_grad, dtype == SMP_F32 ? 4 : 2))
+    return SMP_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (status) {
+    const smp_status rc = clear_status(status, st);
+    if (rc != SMP_OK) return rc;
+  }
+  if (rows == 0) return SMP_OK;
+  ScoreGradArgs a{};
+  a.rows.logits = logits, a.rows.stride = stride, a.rows.rows = rows, a.rows.vocab = vocab;
+  a.rows.temperature = temperature, a.rows.temperatures = temperatures, a.rows.status = status;
+  a.ids = ids, a.count = count, a.up = grad_logprobs, a.up_entropy = grad_entropy;
+  a.grad = out_grad, a.grad_stride = grad_stride;
+  return dtype == SMP_F32 ? launch_scores_grad<float>(a, st) : launch_scores_grad<uint16_t>(a, st);
+}
