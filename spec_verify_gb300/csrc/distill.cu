@@ -90,8 +90,140 @@ __device__ __forceinline__ void read_teacher(const DistillArgs& a, int row, Teac
   }
 }
 
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_constant__ DistillArgs a) {
+// Vector x without the elements whose bits are set.
+__device__ __forceinline__ void erase(uint4& x, uint32_t bits, uint16_t) {
+  uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bits >> (2 * i) & 1u) *w[i] = (*w[i] & 0xFFFF0000u) | 0xFF80u;
+    if (bits >> (2 * i + 1) & 1u) *w[i] = (*w[i] & 0xFFFFu) | 0xFF800000u;
+  }
+}
+__device__ __forceinline__ void erase(uint4& x, uint32_t bits, float) {
+  uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (bits >> i & 1u) *w[i] = RowVec<float>::kNegInf2;
+}
+
+// The row's loss, in one warp, from the joined statistics outside the ids (r)
+// and on them (k); m and zsum: of the whole row.
+__device__ __forceinline__ float row_loss(const Teacher& teach, const float* student, const Stats& r, float m, float zsum,
+                                          float rest, float temperature) {
+  const int lane = int(threadIdx.x) & 31;
+  const float log_z = logf(zsum);
+  float loss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxIds / 32; ++i) {
+    const int n = lane + 32 * i;
+    const float t = teach.t[n];
+    if (t > 0.0f) {   // t (ln t - ln s), with t times a far logit before the division, which it might overflow
+      const float far = __fdiv_rn(__fmul_rn(t, __fsub_rn(student[n], m)), temperature);
+      loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(t, __fadd_rn(teach.log_t[n], log_z)), far));
+    }
+  }
+  loss = warp_sum_f(loss);
+  if (rest > 0.0f) {
+    const float far = __fdiv_rn(__fmul_rn(rest, __fsub_rn(r.m, m)), temperature);
+    loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(rest, __fadd_rn(logf(rest), __fsub_rn(log_z, logf(r.z)))), far));
+  }
+  return loss;
+}
+
+// Both statistics together: m, Z and the factors 2^((m_i - m) c).
+struct Whole {
+  float m, zsum, reach, ids_reach;
+  __device__ __forceinline__ Whole(const Stats& r, const Stats& k, float c) {
+    m = fmaxf(r.m, k.m);
+    reach = r.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(r.m, m), c)) : 0.0f;
+    ids_reach = k.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(k.m, m), c)) : 0.0f;
+    zsum = __fadd_rn(r.z > 0.0f ? __fmul_rn(r.z, reach) : 0.0f, k.z > 0.0f ? __fmul_rn(k.z, ids_reach) : 0.0f);
+  }
+};
+
+// The loss alone: nothing has to stay on chip, so a row streams through one CTA
+// (or the CTAs of a cluster, where rows are few), and a bit per element says
+// which are the teacher's.  The cluster's first CTA holds the teacher's row.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_constant__ DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];   // a bit per element of the part
+  __shared__ Meeting meet;
+  __shared__ Stats ids_warp[kMaxIds / 32];
+  __shared__ Teacher teach;
+  __shared__ float student[kMaxIds];
+  const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  allow_dependent_launch();
+  grid_dependency_wait();
+  cluster_arrive_early(ranks);
+
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  const Part<T> s(z, a.rows.vocab, a.rows.slice, rank);
+  const float temperature = row_temperature(a.rows, row), c = __fdiv_rn(kLog2e, temperature);
+  const int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
+  for (int i = tid; i < (a.rows.slice + 31) / 32; i += kThreads) bits[i] = 0;
+  const bool live = __syncthreads_or(id >= 0), past = __syncthreads_or(id >= a.rows.vocab);
+  int flags = (past ? kRowBadToken : 0) | (temperature_fits(temperature) ? 0 : kRowBadParams);
+  if (!live || flags) {
+    cluster_all_run(ranks);
+    if (rank == 0 && tid == 0) {
+      a.loss[row] = live ? __uint_as_float(0x7FC00000u) : 0.0f;
+      if (live && a.rows.status) atomicOr(a.rows.status, flags);
+    }
+    return;
+  }
+  if (s.holds(id)) atomicOr(&bits[(id - s.first) >> 5], 1u << ((id - s.first) & 31));
+  const float value = rank == 0 && id >= 0 ? clean(load1(z + id)) : -INFINITY;
+  if (rank == 0 && warp == 0) read_teacher(a, row, teach);
+  __syncthreads();
+  Running<T, false> run;
+  const int edge = s.edge();
+  if (edge >= 0 && !(bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u))
+    run.add_one(clean(load1(z + edge)), temperature, c);
+  const unsigned char* bytes = dynamic;
+  stream(
+      s, run, temperature, c,
+      [&](uint4& x, int j) {
+        if (j < s.full1) {
+          const uint32_t b = Part<T>::kPer == 8 ? bytes[j] : bytes[j >> 1] >> (4 * (j & 1)) & 15u;
+          if (b) erase(x, b, T{});
+        }
+      },
+      [](float) {});
+  const Stats part = warp_join(run.stats(), c);
+  if (lane == 0) meet.warp[warp] = part;
+  if (rank == 0 && warp < kMaxIds / 32) {
+    float sum;
+    const bool counts = id >= 0 && value > -INFINITY && first_of_id(teach.ids, teach.t, a.count, tid, sum);
+    const Stats on_ids = warp_join(counts ? Stats{value, 1.0f, 0.0f} : Stats{-INFINITY, 0.0f, 0.0f}, c);
+    if (lane == 0) ids_warp[warp] = on_ids;
+    student[tid] = value;
+  }
+  cluster_all_run(ranks);
+  __syncthreads();
+  const Stats none{-INFINITY, 0.0f, 0.0f};
+  if (warp == 0) {
+    const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : none, c);
+    post(meet, rank, ranks, cta.m, cta.z, 0.0f, 0.0f);
+  }
+  cluster_meet(ranks);
+  if (rank != 0 || warp != 0) return;
+  const float4 p = posted(meet, ranks);
+  const Stats r = warp_join(Stats{p.x, p.y, 0.0f}, c);
+  const Stats k = warp_join(lane < kMaxIds / 32 ? ids_warp[lane] : none, c);
+  const Whole all(r, k, c);
+  flags = teach.flags;
+  if (!flags && !(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
+  const float loss = row_loss(teach, student, r, all.m, all.zsum, r.z > 0.0f ? teach.rest : 0.0f, temperature);
+  if (lane == 0) {
+    a.loss[row] = flags ? __uint_as_float(0x7FC00000u) : loss;
+    if (flags && a.rows.status) atomicOr(a.rows.status, flags);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Meeting meet;
   __shared__ Stats ids_warp[kMaxIds / 32];
@@ -111,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
   cluster_arrive_early(ranks);
 
   const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-  T* out = kGrad ? static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride : nullptr;
+  T* out = static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride;
   const float temperature = row_temperature(a.rows, row), c = __fdiv_rn(kLog2e, temperature);
   const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
   const float nan = __uint_as_float(0x7FC00000u);
@@ -124,14 +256,12 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
       a.loss[row] = teach.live ? nan : 0.0f;
       if (teach.live && a.rows.status) atomicOr(a.rows.status, flags);
     }
-    if (kGrad) {
-      s.fill(teach.live ? nan : 0.0f);
-      s.store(out);
-    }
+    s.fill(teach.live ? nan : 0.0f);
+    s.store(out);
     return;
   }
   s.load(z, a.rows.vocab, &bar);
-  const float weight = kGrad && a.weights ? a.weights[row] : 1.0f;
+  const float weight = a.weights ? a.weights[row] : 1.0f;
   const int id = tid < kMaxIds ? teach.ids[tid] : -1;
   const bool here = s.holds(id);
   float t_here = 0.0f;   // the id's t, over all its places
@@ -160,50 +290,28 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
     post(meet, rank, ranks, r.m, r.z, k.m, late ? -1.0f : k.z);
   }
   cluster_meet(ranks);
-  if (!kGrad && (rank != 0 || warp != 0)) return;
   const float4 p = posted(meet, ranks);
   const Stats r = warp_join(Stats{p.x, p.y, 0.0f}, c), k = warp_join(Stats{p.z, fmaxf(p.w, 0.0f), 0.0f}, c);
-  const float m = fmaxf(r.m, k.m);
-  if (!(fabsf(m) < INFINITY)) flags = kRowNonFinite;
+  const Whole all(r, k, c);
+  if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
   if (__any_sync(~0u, lane < ranks && p.w < 0.0f)) flags = kRowTimeout;
   if (flags) {
     if (rank == 0 && tid == 0) {
       a.loss[row] = nan;
       if (a.rows.status) atomicOr(a.rows.status, flags);
     }
-    if (kGrad) {
-      s.fill(nan);
-      s.store(out);
-    }
+    s.fill(nan);
+    s.store(out);
     return;
   }
-  const float reach = r.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(r.m, m), c)) : 0.0f;   // 2^((m_R - m) c)
-  const float ids_reach = k.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(k.m, m), c)) : 0.0f;
-  const float zsum = __fadd_rn(r.z > 0.0f ? __fmul_rn(r.z, reach) : 0.0f, k.z > 0.0f ? __fmul_rn(k.z, ids_reach) : 0.0f);
   const float rest = r.z > 0.0f ? teach.rest : 0.0f;
   if (rank == 0 && warp == 0) {
-    const float log_z = logf(zsum);
-    float loss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxIds / 32; ++i) {
-      const int n = lane + 32 * i;
-      const float t = teach.t[n];
-      if (t > 0.0f) {   // t (ln t - ln s), with t times a far logit before the division, which it might overflow
-        const float far = __fdiv_rn(__fmul_rn(t, __fsub_rn(student[n], m)), temperature);
-        loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(t, __fadd_rn(teach.log_t[n], log_z)), far));
-      }
-    }
-    loss = warp_sum_f(loss);
-    if (rest > 0.0f) {
-      const float far = __fdiv_rn(__fmul_rn(rest, __fsub_rn(r.m, m)), temperature);
-      loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(rest, __fadd_rn(logf(rest), __fsub_rn(log_z, logf(r.z)))), far));
-    }
+    const float loss = row_loss(teach, student, r, all.m, all.zsum, rest, temperature);
     if (lane == 0) a.loss[row] = loss;
   }
-  if (!kGrad) return;
-  const float scale = __fdiv_rn(weight, temperature), inv_z = __fdiv_rn(1.0f, zsum);
+  const float scale = __fdiv_rn(weight, temperature), inv_z = __fdiv_rn(1.0f, all.zsum);
   const float total = rest > 0.0f ? 1.0f : teach.given;
-  const float outside = r.z > 0.0f ? scale * (total * reach * inv_z - __fdiv_rn(rest, r.z)) : 0.0f;
+  const float outside = r.z > 0.0f ? scale * (total * all.reach * inv_z - __fdiv_rn(rest, r.z)) : 0.0f;
   const float top = r.z > 0.0f ? r.m : 0.0f;   // nothing outside the ids: any finite reference
   const uint32_t floor = floor_word<T>(top, temperature);
   for (int j = tid; j < s.vecs; j += kThreads) {
@@ -215,17 +323,21 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const __grid_const
   }
   __syncthreads();
   if (first) {
-    const float share = value > -INFINITY ? __fmul_rn(ex2_approx(__fmul_rn(__fsub_rn(value, m), c)), inv_z) : 0.0f;
+    const float share = value > -INFINITY ? __fmul_rn(ex2_approx(__fmul_rn(__fsub_rn(value, all.m), c)), inv_z) : 0.0f;
     store1(s.buf + (id - s.first), __fmul_rn(scale, __fmaf_rn(share, total, -t_here)));
   }
   s.store(out);
 }
 
 template <typename T>
-static smp_status launch_distill(const DistillArgs& a, cudaStream_t st) {
-  const void* kernel = a.grad ? reinterpret_cast<const void*>(&distill_kernel<T, true>)
-                              : reinterpret_cast<const void*>(&distill_kernel<T, false>);
-  return launch_rows(kernel, a, int(sizeof(T)), 0, st);
+static smp_status launch_distill(DistillArgs a, cudaStream_t st) {
+  LaunchShape ls;
+  const smp_status ok = a.grad ? shape_slices(a.rows, int(sizeof(T)), ls) : shape_parts(a.rows, int(sizeof(T)), ls);
+  if (ok != SMP_OK) return ok;
+  if (!a.grad) ls.smem = size_t(a.rows.slice + 127) / 128 * 16;
+  return launch_rows(a.grad ? reinterpret_cast<const void*>(&distill_grad_kernel<T>)
+                            : reinterpret_cast<const void*>(&distill_loss_kernel<T>),
+                     a, ls, st);
 }
 
 }  // namespace smp

@@ -238,35 +238,79 @@ __device__ __forceinline__ float warp_sum_f(float v) {
   return v;
 }
 
+// Two binary32 numbers at a time.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return reinterpret_cast<const float2&>(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The running statistics of one thread's elements: a group of vectors is taken
+// in at a time, relative to the largest element so far.
+template <typename T, bool kWeighted>
+struct Running {
+  using V = RowVec<T>;
+  float m = -INFINITY;
+  float2 z = make_float2(0.0f, 0.0f), s = make_float2(0.0f, 0.0f);
+  uint32_t floor = 0;
+
+  // A maximum of the elements that come next.
+  __device__ __forceinline__ void raise(float top, float temperature, float c) {
+    if (top > m) {
+      if (m > -INFINITY) {
+        const float d = __fsub_rn(m, top), w = ex2_approx(__fmul_rn(d, c));
+        if (kWeighted) s = w == 0.0f ? both(0.0f) : mul2(fma2(z, both(d), s), both(w));
+        z = mul2(z, both(w));
+      }
+      m = top;
+      floor = floor_word<T>(m, temperature);
+    }
+  }
+  // A vector none of whose elements is above m; m is not -inf.
+  __device__ __forceinline__ void add(const uint4& x, float c) {
+    float v[V::kPer];
+    V::get(x, floor, v);
+#pragma unroll
+    for (int i = 0; i < V::kPer; i += 2) {
+      const float2 d = add2(make_float2(v[i], v[i + 1]), both(-m)), y = mul2(d, both(c));
+      const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+      z = add2(z, e);
+      if (kWeighted) s = fma2(e, d, s);
+    }
+  }
+  __device__ __forceinline__ void add_one(float v, float temperature, float c) {   // clean
+    if (v > -INFINITY) {
+      raise(v, temperature, c);
+      const float d = __fsub_rn(v, m), e = ex2_approx(__fmul_rn(d, c));
+      z.x += e;
+      if (kWeighted && e > 0.0f) s.x = __fmaf_rn(e, d, s.x);
+    }
+  }
+  __device__ __forceinline__ Stats stats() const {
+    return Stats{m, z.x + z.y, kWeighted && !is_lowest<T>(m) ? s.x + s.y : 0.0f};
+  }
+};
+
 // The largest of this thread's elements (vectors tid, tid + kThreads, ...).
 template <typename T>
 __device__ __forceinline__ float thread_top(const Slice<T>& s) {
   uint32_t m = RowVec<T>::kNegInf2;
   for (int j = int(threadIdx.x); j < s.vecs; j += kThreads) m = RowVec<T>::top(s.vec()[j], m);
   return RowVec<T>::finish(m);
-}
-
-// The statistics of this warp's elements, given its threads' maxima.
-template <typename T, bool kWeighted>
-__device__ __forceinline__ Stats warp_stats(const Slice<T>& s, float mine, float temperature, float c) {
-  constexpr int kPer = RowVec<T>::kPer;
-  Stats out{warp_max_f(mine), 0.0f, 0.0f};
-  if (!(out.m > -INFINITY)) return out;
-  const uint32_t floor = floor_word<T>(out.m, temperature);
-  float z[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
-  for (int j = int(threadIdx.x); j < s.vecs; j += kThreads) {
-    float v[kPer];
-    RowVec<T>::get(s.vec()[j], floor, v);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float d = __fsub_rn(v[i], out.m), e = ex2_approx(__fmul_rn(d, c));
-      z[i & 1] += e;
-      if (kWeighted) w[i & 1] = __fmaf_rn(e, d, w[i & 1]);
-    }
-  }
-  out.z = warp_sum_f(z[0] + z[1]);
-  if (kWeighted && !is_lowest<T>(out.m)) out.s = warp_sum_f(w[0] + w[1]);
-  return out;
 }
 
 // The statistics of the lanes' parts together, in every lane.
@@ -281,6 +325,82 @@ __device__ __forceinline__ Stats warp_join(const Stats& part, float c) {
   }
   out.z = warp_sum_f(z), out.s = warp_sum_f(s);
   return out;
+}
+
+// The statistics of this warp's elements, given its threads' maxima.
+template <typename T, bool kWeighted>
+__device__ __forceinline__ Stats warp_stats(const Slice<T>& s, float mine, float temperature, float c) {
+  Running<T, kWeighted> run;
+  run.raise(mine, temperature, c);
+  if (run.m > -INFINITY)
+    for (int j = int(threadIdx.x); j < s.vecs; j += kThreads) run.add(s.vec()[j], c);
+  return warp_join(run.stats(), c);
+}
+
+// ------------------------------------------------------------------ a part of a row, read once from memory
+
+// Elements [lo, hi) of a row, whole vectors [full0, full1) of 16 bytes counted
+// from element `first`; thread t takes vectors t, t + kThreads, ... and the edge
+// threads one element each outside them.
+template <typename T>
+struct Part {
+  static constexpr int kPer = RowVec<T>::kPer;
+  const T* row;
+  int first, lo, hi, full0, full1;
+
+  __device__ __forceinline__ Part(const T* r, int vocab, int slice, int rank) : row(r) {
+    first = rank * slice - int((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+    lo = max(first, 0), hi = max(lo, min(first + slice, vocab));
+    full0 = first < 0 ? 1 : 0;
+    full1 = hi > lo ? max(full0, (hi - first) / kPer) : full0;
+  }
+  __device__ __forceinline__ bool holds(int id) const { return id >= lo && id < hi; }
+  __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(row + first); }
+  // The id of this thread's edge element, or -1.
+  __device__ __forceinline__ int edge() const {
+    const int t = int(threadIdx.x), id = t < kPer ? first + t : first + full1 * kPer + t - kPer;
+    return t < 2 * kPer && (t >= kPer || full0 == 1) && holds(id) ? id : -1;
+  }
+};
+
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+constexpr int kUnroll = 4;   // vectors of a thread in flight
+
+// Takes the part's whole vectors into `run`, kUnroll vectors per thread at a
+// time.  change(x, j) may alter vector j first; seen(top) gets the largest
+// element of each group.
+template <typename T, bool kWeighted, typename Change, typename Seen>
+__device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, float temperature, float c,
+                                       Change&& change, Seen&& seen) {
+  for (int j0 = int(threadIdx.x); j0 < s.full1; j0 += kUnroll * kThreads) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kThreads;
+      x[u] = make_uint4(RowVec<T>::kNegInf2, RowVec<T>::kNegInf2, RowVec<T>::kNegInf2, RowVec<T>::kNegInf2);
+      if (j >= s.full0 && j < s.full1) x[u] = load_once(s.vec() + j);
+    }
+    uint32_t w = RowVec<T>::kNegInf2;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      change(x[u], j0 + u * kThreads);
+      w = RowVec<T>::top(x[u], w);
+    }
+    const float top = RowVec<T>::finish(w);
+    run.raise(top, temperature, c);
+    if (run.m > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) run.add(x[u], c);
+    }
+    seen(top);
+  }
 }
 
 // What the CTAs of a cluster tell one another, and the room their warps meet in.
@@ -365,34 +485,48 @@ inline bool grad_fits(const void* logits, int32_t rows, int32_t vocab, int64_t s
   return grad != logits || rows <= 1 || grad_stride == stride;
 }
 
-// CTAs per row.
-inline int scores_cluster(int rows, int vocab, int elem, int sms) {
-  const int64_t bytes = int64_t(vocab) * elem;
-  int c = 1;
-  while (c < 16 && bytes > int64_t(c) * 68 * 1024) c *= 2;
-  const int forced = forced_cluster();
-  if (forced && bytes <= int64_t(forced) * 160 * 1024) return forced;
-  while (c < 8 && int64_t(rows) * c * 2 <= int64_t(sms) * 3 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
-  return c;
-}
-
-// Launches `kernel` on every row: `extra` bytes of shared memory behind the
-// slice.  `a` is the kernel's argument, whose first member is its RowsArgs.
-template <typename Args>
-smp_status launch_rows(const void* kernel, Args a, int elem, size_t extra, cudaStream_t st) {
-  RowsArgs& r = a.rows;
+// The launch of a kernel whose CTAs read their parts of a row from memory once:
+// one row per CTA where there are many rows, parts of it where they would leave
+// SMs without work.
+inline smp_status shape_parts(RowsArgs& r, int elem, LaunchShape& ls) {
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
-  LaunchShape ls;
-  ls.pdl = true;
-  ls.cluster = scores_cluster(r.rows, r.vocab, elem, device_sms(dev));
+  const int64_t bytes = int64_t(r.vocab) * elem;
+  int c = 1;
+  while (c < 16 && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 6 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
+  ls.cluster = forced_cluster() ? forced_cluster() : c;
   const int per = 16 / elem;
   r.slice = ((r.vocab + per - 1 + ls.cluster - 1) / ls.cluster + per - 1) / per * per;
-  r.wait_limit = wait_limit_ns();
-  ls.smem = size_t(r.slice) * elem + extra;
+  return SMP_OK;
+}
+
+// The launch of a kernel whose CTAs keep their slices in shared memory.
+inline smp_status shape_slices(RowsArgs& r, int elem, LaunchShape& ls) {
+  const int dev = current_device();
+  if (dev < 0) return fail_cuda(cudaGetLastError());
+  const int64_t bytes = int64_t(r.vocab) * elem;
+  int c = 1;
+  while (c < 16 && bytes > int64_t(c) * 68 * 1024) c *= 2;
+  while (c < 8 && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 3 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
+  const int forced = forced_cluster();
+  ls.cluster = forced && bytes <= int64_t(forced) * 160 * 1024 ? forced : c;
+  const int per = 16 / elem;
+  r.slice = ((r.vocab + per - 1 + ls.cluster - 1) / ls.cluster + per - 1) / per * per;
+  ls.smem = size_t(r.slice) * elem;
+  return SMP_OK;
+}
+
+// Launches `kernel` on every row; `a` is its argument, whose member `rows` is a
+// RowsArgs.
+template <typename Args>
+smp_status launch_rows(const void* kernel, Args a, LaunchShape ls, cudaStream_t st) {
+  const int dev = current_device();
+  if (dev < 0) return fail_cuda(cudaGetLastError());
+  ls.pdl = true;
+  a.rows.wait_limit = wait_limit_ns();
   cudaError_t err = prepare_kernel(kernel, dev, ls);
   if (err != cudaSuccess) return fail_cuda(err);
-  err = launch_cluster(kernel, dim3(unsigned(r.rows) * unsigned(ls.cluster)), dim3(kThreads), ls, st, &a);
+  err = launch_cluster(kernel, dim3(unsigned(a.rows.rows) * unsigned(ls.cluster)), dim3(kThreads), ls, st, &a);
   return err == cudaSuccess ? SMP_OK : fail_cuda(err);
 }
 

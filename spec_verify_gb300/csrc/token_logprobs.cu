@@ -12,6 +12,9 @@
 // The first CTA of the cluster merges the sorted lists by binary search.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "scores.cuh"
 
 namespace smp {
@@ -26,6 +29,7 @@ struct ScoreArgs {
   float* entropy;
   int32_t* top_ids;
   float* top_logprobs;
+  int run_room;   // most runs of any CTA
 };
 
 struct ScoreGradArgs {
@@ -38,12 +42,26 @@ struct ScoreGradArgs {
   int64_t grad_stride;
 };
 
-// The `top` largest elements of the slice, in order, as packed words (0: none)
-// to `list` of the cluster's first CTA.
+// A thread's elements come in up to kRuns runs whose maxima are kept, `groups`
+// groups of kUnroll vectors each.
+constexpr int kRuns = 16;
+
+// What slice_top works with, in shared memory.
+struct TopRoom {
+  int hits[kCandidates];           // thread | run << 8
+  uint64_t cand[kCandidates];
+  uint64_t scratch[kWarps];
+  int hit_count, found;
+};
+
+// The `top` largest elements of the part, in order, as packed words (0: none)
+// to `list` of the cluster's first CTA.  `mine` is the largest of this thread's
+// elements, run_top[run][thread] of each run, `edge` its edge element's id.
 template <typename T>
-__device__ void slice_top(const Slice<T>& s, float mine, int top, uint64_t* cand, uint64_t* list, int ranks,
-                          uint64_t* scratch, int* found) {
-  const int tid = int(threadIdx.x), lane = tid & 31;
+__device__ void slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int groups, int edge, int top,
+                          TopRoom& room, uint64_t* list, int ranks) {
+  constexpr int kPer = RowVec<T>::kPer;
+  const int tid = int(threadIdx.x);
   // 16 bits of the order key: the largest value that `top` of the threads' maxima reach
   const uint32_t key = key_of_bits(__float_as_uint(mine)) >> 16;
   uint32_t bound = 0;
@@ -51,34 +69,50 @@ __device__ void slice_top(const Slice<T>& s, float mine, int top, uint64_t* cand
   for (int bit = 15; bit >= 0; --bit)
     if (cta_sync_count(key >= (bound | 1u << bit)) >= top) bound |= 1u << bit;
   const uint32_t least = max(bound << 16, kKeyNegInf + 1u);
-  if (tid == 0) *found = 0;
+  if (tid == 0) room.hit_count = room.found = 0;
   __syncthreads();
-  // a warp looks through one thread's vectors at a time, all lanes together
-  for (unsigned hits = __ballot_sync(~0u, key >= bound && key >= (least >> 16)); hits; hits &= hits - 1) {
-    const int who = (tid & ~31) + __ffs(hits) - 1;
-    constexpr int kPer = RowVec<T>::kPer;
-    const int own = s.vecs > who ? (s.vecs - who + kThreads - 1) / kThreads : 0;
-    for (int i = lane; i < own * kPer; i += 32) {
-      const int at = (who + (i / kPer) * kThreads) * kPer + i % kPer;
-      const uint32_t k = key_of_bits(Elem<T>::bits(s.buf[at]));
-      if (k >= least) {
-        const int place = atomicAdd(found, 1);
-        if (place < kCandidates) cand[place] = pack_key_id(k, uint32_t(s.first + at));
-      }
+  auto take = [&](uint32_t bits, int id) {
+    const uint32_t k = key_of_bits(bits);
+    if (k >= least) {
+      const int place = atomicAdd(&room.found, 1);
+      if (place < kCandidates) room.cand[place] = pack_key_id(k, uint32_t(id));
     }
+  };
+  if (key >= (least >> 16)) {
+    if (edge >= 0) take(Elem<T>::bits(s.row[edge]), edge);
+    for (int run = 0; run < runs; ++run)
+      if (key_of_bits(__float_as_uint(run_top[run * kThreads + tid])) >= least) {
+        const int place = atomicAdd(&room.hit_count, 1);
+        if (place < kCandidates) room.hits[place] = tid | run << 8;
+      }
   }
   __syncthreads();
-  const int have = *found;
+  const int hits = room.hit_count, run_vecs = groups * kUnroll;
+  bool listed = hits <= kCandidates;
+  if (listed) {   // the runs' vectors again (from L2), every thread one at a time
+    for (int i = tid; i < hits * run_vecs; i += kThreads) {
+      const int hit = room.hits[i / run_vecs], j = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
+      if (j >= s.full0 && j < s.full1) {
+        const uint4 x = s.vec()[j];
+        const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) take(Elem<T>::bits(e[q]), s.first + j * kPer + q);
+      }
+    }
+    __syncthreads();
+    listed = room.found <= kCandidates;
+  }
   const uint32_t to = ranks > 1 ? map_rank(smem_addr(list), 0) : 0;
   auto put = [&](int place, uint64_t v) {
     if (ranks > 1) st_cluster_u64(to + uint32_t(place) * 8u, v);
     else list[place] = v;
   };
-  if (have <= kCandidates) {
+  if (listed) {
+    const int have = room.found;
     for (int i = tid; i < have; i += kThreads) {
-      const uint64_t v = cand[i];
+      const uint64_t v = room.cand[i];
       int rank = 0;
-      for (int j = 0; j < have; ++j) rank += cand[j] > v;
+      for (int j = 0; j < have; ++j) rank += room.cand[j] > v;
       if (rank < top) put(rank, v);
     }
     for (int i = have + tid; i < top; i += kThreads) put(i, 0);
@@ -86,12 +120,12 @@ __device__ void slice_top(const Slice<T>& s, float mine, int top, uint64_t* cand
     uint64_t last = ~0ull;
     for (int n = 0; n < top; ++n) {
       uint64_t best = 0;
-      for (int j = tid; j < s.vecs * RowVec<T>::kPer; j += kThreads) {
-        const uint32_t k = key_of_bits(Elem<T>::bits(s.buf[j]));
-        const uint64_t v = k > kKeyNegInf ? pack_key_id(k, uint32_t(s.first + j)) : 0;
+      for (int id = s.lo + tid; id < s.hi; id += kThreads) {
+        const uint32_t k = key_of_bits(Elem<T>::bits(s.row[id]));
+        const uint64_t v = k > kKeyNegInf ? pack_key_id(k, uint32_t(id)) : 0;
         if (v < last && v > best) best = v;
       }
-      best = block_max_u64(best, scratch);
+      best = block_max_u64(best, room.scratch);
       if (tid == 0) put(n, best);
       if (best == 0) {
         for (int i = n + 1 + tid; i < top; i += kThreads) put(i, 0);
@@ -102,76 +136,82 @@ __device__ void slice_top(const Slice<T>& s, float mine, int top, uint64_t* cand
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ __align__(16) unsigned char dynamic[];
+template <typename T, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];   // with kTop: TopRoom, the runs' maxima, the lists
   __shared__ Meeting meet;
-  __shared__ uint64_t bar, scratch[kWarps];
-  __shared__ int found;
   const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   allow_dependent_launch();
-  if (tid == 0) {
-    mbar_init(&bar, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
   grid_dependency_wait();
   cluster_arrive_early(ranks);
 
   const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-  const float temperature = row_temperature(a.rows, row);
+  const Part<T> s(z, a.rows.vocab, a.rows.slice, rank);
+  const float temperature = row_temperature(a.rows, row), c = __fdiv_rn(kLog2e, temperature);
   const int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
-  const bool wanted = a.entropy || a.top > 0 || __syncthreads_or(id >= 0);
-  const bool fits = temperature_fits(temperature);
-  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
-  uint64_t* cand = reinterpret_cast<uint64_t*>(dynamic + size_t(a.rows.slice) * sizeof(T));
-  uint64_t* lists = cand + kCandidates;
-  const float c = __fdiv_rn(kLog2e, temperature);
   float* logprobs = a.logprobs + int64_t(row) * a.count;
-
-  if (!wanted) {   // every id is padding
+  if (!kEntropy && !kTop && !__syncthreads_or(id >= 0)) {   // every id is padding
     cluster_all_run(ranks);
     if (rank == 0 && tid < a.count) logprobs[tid] = 0.0f;
     return;
   }
-  int flags = fits ? 0 : kRowBadParams;
+  TopRoom& room = *reinterpret_cast<TopRoom*>(dynamic);
+  float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom));
+  const int groups_all = (s.full1 + kThreads * kUnroll - 1) / (kThreads * kUnroll);   // of this CTA
+  const int groups = (groups_all + kRuns - 1) / kRuns, runs = groups ? (groups_all + groups - 1) / groups : 0;
+  uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThreads);
+  int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
   Stats all{-INFINITY, 0.0f, 0.0f};
-  if (fits) {
-    s.load(z, a.rows.vocab, &bar);
-    const bool late = slice_is_late(&bar, a.rows.wait_limit);
-    const float mine = thread_top(s);
-    const Stats part = a.entropy ? warp_stats<T, true>(s, mine, temperature, c) : warp_stats<T, false>(s, mine, temperature, c);
+  const float value = flags == 0 && s.holds(id) ? clean(load1(z + id)) : 0.0f;
+  if (flags == 0) {
+    Running<T, kEntropy> run;
+    const int edge = s.edge();
+    if (edge >= 0) run.add_one(clean(load1(z + edge)), temperature, c);
+    float best = -INFINITY;
+    int in_run = 0, r = 0;
+    stream(s, run, temperature, c, [](uint4&, int) {}, [&](float top) {
+      if (kTop) {
+        best = fmaxf(best, top);
+        if (++in_run == groups) {
+          run_top[r * kThreads + tid] = best;
+          best = -INFINITY, in_run = 0, ++r;
+        }
+      }
+    });
+    if (kTop) {
+      for (; r < runs; ++r, best = -INFINITY) run_top[r * kThreads + tid] = best;
+    }
+    const Stats part = warp_join(run.stats(), c);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
-    if (a.top > 0) slice_top(s, mine, a.top, cand, lists + rank * a.top, ranks, scratch, &found);
+    if (kTop) slice_top(s, run.m, run_top, runs, groups, edge, a.top, room, lists + rank * a.top, ranks);
     __syncthreads();
     if (warp == 0) {
       const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
-      post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
+      post(meet, rank, ranks, cta.m, cta.z, cta.s, 0.0f);
     }
     cluster_meet(ranks);
     const float4 p = posted(meet, ranks);
     all = warp_join(Stats{p.x, p.y, p.z}, c);
     if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
-    if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
   } else {
     cluster_all_run(ranks);
   }
   const float nan = __uint_as_float(0x7FC00000u), log_z = logf(all.z);
-  auto logprob = [&](float value) { return __fsub_rn(__fdiv_rn(__fsub_rn(value, all.m), temperature), log_z); };
+  auto logprob = [&](float v) { return __fsub_rn(__fdiv_rn(__fsub_rn(v, all.m), temperature), log_z); };
   if (tid < a.count) {
     const bool past = id >= a.rows.vocab;
-    if (flags == 0 && s.holds(id)) logprobs[tid] = logprob(s.at(id));
+    if (flags == 0 && s.holds(id)) logprobs[tid] = logprob(value);
     else if (rank == 0 && (id < 0 || past || flags)) logprobs[tid] = id < 0 ? 0.0f : nan;
     if (rank == 0 && past && a.rows.status) atomicOr(a.rows.status, kRowBadToken);
   }
   if (rank != 0) return;
   if (tid == 0) {
     if (flags && a.rows.status) atomicOr(a.rows.status, flags);
-    if (a.entropy) a.entropy[row] = flags ? nan : __fsub_rn(log_z, __fdiv_rn(all.s, __fmul_rn(temperature, all.z)));
+    if (kEntropy) a.entropy[row] = flags ? nan : __fsub_rn(log_z, __fdiv_rn(all.s, __fmul_rn(temperature, all.z)));
   }
-  if (a.top > 0) {
+  if (kTop) {
     int32_t* top_ids = a.top_ids + int64_t(row) * a.top;
     float* top_logprobs = a.top_logprobs + int64_t(row) * a.top;
     if (flags) {
@@ -181,9 +221,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const __gri
     // how many of the lists' entries are tokens, at most `top`
     int some = 0;
     for (int e = tid; e < ranks * a.top; e += kThreads) some += lists[e] != 0;
-    if (tid == 0) found = 0;
+    if (tid == 0) room.found = 0;
     __syncthreads();
-    if (some) atomicAdd(&found, some);
+    if (some) atomicAdd(&room.found, some);
     for (int e = tid; e < ranks * a.top; e += kThreads) {
       const uint64_t v = lists[e];
       if (v == 0) continue;
@@ -205,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const __gri
       }
     }
     __syncthreads();
-    for (int i = found + tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = -INFINITY;
+    for (int i = room.found + tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = -INFINITY;
   }
 }
 
@@ -309,13 +349,28 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_grad_kernel(const 
 }
 
 template <typename T>
-static smp_status launch_scores(const ScoreArgs& a, cudaStream_t st) {
-  const size_t extra = a.top > 0 ? (kCandidates + size_t(kMaxRanks) * a.top) * 8 : 0;
-  return launch_rows(reinterpret_cast<const void*>(&token_logprobs_kernel<T>), a, int(sizeof(T)), extra, st);
+static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
+  const void* kernel =
+      a.entropy ? (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true>)
+                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, false>))
+                : (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, true>)
+                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, false>));
+  LaunchShape ls;
+  const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
+  if (ok != SMP_OK) return ok;
+  if (a.top) {
+    const int per_group = kThreads * kUnroll * RowVec<T>::kPer;
+    a.run_room = std::min(kRuns, (a.rows.slice + per_group - 1) / per_group);
+    ls.smem = sizeof(TopRoom) + size_t(a.run_room) * kThreads * 4 + size_t(ls.cluster) * a.top * 8;
+  }
+  return launch_rows(kernel, a, ls, st);
 }
 template <typename T>
 static smp_status launch_scores_grad(const ScoreGradArgs& a, cudaStream_t st) {
-  return launch_rows(reinterpret_cast<const void*>(&token_logprobs_grad_kernel<T>), a, int(sizeof(T)), 0, st);
+  ScoreGradArgs b = a;
+  LaunchShape ls;
+  const smp_status ok = shape_slices(b.rows, int(sizeof(T)), ls);
+  return ok == SMP_OK ? launch_rows(reinterpret_cast<const void*>(&token_logprobs_grad_kernel<T>), b, ls, st) : ok;
 }
 
 }  // namespace smp
