@@ -179,18 +179,20 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
   __syncthreads();
   Running<T, false> run;
   const int edge = s.edge();
-  if (edge >= 0 && !(bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u))
-    run.add_one(clean(load1(z + edge)), temperature, c);
+  const bool apart = edge >= 0 && (bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u);
+  const float at_edge = edge >= 0 && !apart ? clean(load1(z + edge)) : -INFINITY;
   const unsigned char* bytes = dynamic;
+  uint4 x[2][kUnit];
   stream(
-      s, run, temperature, c,
-      [&](uint4& x, int j) {
+      s, run, x, temperature, c,
+      [&](uint4& y, int j) {
         if (j < s.full1) {
           const uint32_t b = Part<T>::kPer == 8 ? bytes[j] : bytes[j >> 1] >> (4 * (j & 1)) & 15u;
-          if (b) erase(x, b, T{});
+          if (b) erase(y, b, T{});
         }
       },
       [](float) {});
+  run.add_one(at_edge, temperature, c);
   const Stats part = warp_join(run.stats(), c);
   if (lane == 0) meet.warp[warp] = part;
   if (rank == 0 && warp < kMaxIds / 32) {

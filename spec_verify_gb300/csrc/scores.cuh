@@ -16,6 +16,8 @@
 // CTA joins its warps and every CTA the cluster's.
 #pragma once
 
+#include <algorithm>
+
 #include "cache.cuh"
 #include "launch.h"
 #include "smp_scores.h"
@@ -26,6 +28,7 @@ namespace smp {
 constexpr int kRowBadToken = 128;
 constexpr int kMaxIds = SMP_MAX_ROW_IDS;
 constexpr int kMaxRanks = 16;
+constexpr int kMaxParts = 8;   // CTAs of a row that is streamed
 
 // The rows of a call, as every kernel here gets them.
 struct RowsArgs {
@@ -363,6 +366,7 @@ struct Part {
   }
 };
 
+// A vector that is not wanted again soon, past the L1 cache.
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -371,35 +375,51 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
   return v;
 }
 
-constexpr int kUnroll = 4;   // vectors of a thread in flight
+constexpr int kUnit = 4;     // vectors of a thread that are loaded and taken in together
 
-// Takes the part's whole vectors into `run`, kUnroll vectors per thread at a
-// time.  change(x, j) may alter vector j first; seen(top) gets the largest
-// element of each group.
+// Takes the part's whole vectors into `run`, a unit per thread at a time: while
+// one unit is taken in, the next is on its way, in x[0] and x[1], which keep the
+// last two (with one unit in flight 4093 rows of 152064 took 229 us, with two
+// that were loaded together 208 to 221).  change(y, j) may alter vector j first;
+// seen(top) gets the largest element of each unit, in order.
 template <typename T, bool kWeighted, typename Change, typename Seen>
-__device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, float temperature, float c,
-                                       Change&& change, Seen&& seen) {
-  for (int j0 = int(threadIdx.x); j0 < s.full1; j0 += kUnroll * kThreads) {
-    uint4 x[kUnroll];
+__device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, uint4 (&x)[2][kUnit],
+                                       const float& temperature, const float& c, Change&& change, Seen&& seen) {
+  using V = RowVec<T>;
+  const int units = (s.full1 + kUnit * kThreads - 1) / (kUnit * kThreads);
+  auto load = [&](uint4 (&y)[kUnit], int unit) {
+    const int j0 = int(threadIdx.x) + unit * (kUnit * kThreads);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kUnit; ++u) {
       const int j = j0 + u * kThreads;
-      x[u] = make_uint4(RowVec<T>::kNegInf2, RowVec<T>::kNegInf2, RowVec<T>::kNegInf2, RowVec<T>::kNegInf2);
-      if (j >= s.full0 && j < s.full1) x[u] = load_once(s.vec() + j);
+      y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
+      if (j >= s.full0 && j < s.full1) y[u] = load_once(s.vec() + j);
     }
-    uint32_t w = RowVec<T>::kNegInf2;
+  };
+  auto take = [&](uint4 (&y)[kUnit], int unit) {
+    uint32_t w = V::kNegInf2;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      change(x[u], j0 + u * kThreads);
-      w = RowVec<T>::top(x[u], w);
+    for (int u = 0; u < kUnit; ++u) {
+      change(y[u], int(threadIdx.x) + (unit * kUnit + u) * kThreads);
+      w = V::top(y[u], w);
     }
-    const float top = RowVec<T>::finish(w);
+    const float top = V::finish(w);
     run.raise(top, temperature, c);
     if (run.m > -INFINITY) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) run.add(x[u], c);
+      for (int u = 0; u < kUnit; ++u) run.add(y[u], c);
     }
     seen(top);
+  };
+  if (units > 0) load(x[0], 0);
+  if (units > 1) load(x[1], 1);
+  for (int q = 0; q < units; q += 2) {
+    take(x[0], q);
+    if (q + 2 < units) load(x[0], q + 2);
+    if (q + 1 < units) {
+      take(x[1], q + 1);
+      if (q + 3 < units) load(x[1], q + 3);
+    }
   }
 }
 
@@ -493,8 +513,8 @@ inline smp_status shape_parts(RowsArgs& r, int elem, LaunchShape& ls) {
   if (dev < 0) return fail_cuda(cudaGetLastError());
   const int64_t bytes = int64_t(r.vocab) * elem;
   int c = 1;
-  while (c < 16 && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 6 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
-  ls.cluster = forced_cluster() ? forced_cluster() : c;
+  while (c < kMaxParts && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 4 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
+  ls.cluster = forced_cluster() ? std::min(forced_cluster(), kMaxParts) : c;
   const int per = 16 / elem;
   r.slice = ((r.vocab + per - 1 + ls.cluster - 1) / ls.cluster + per - 1) / per * per;
   return SMP_OK;

@@ -42,78 +42,155 @@ struct ScoreGradArgs {
   int64_t grad_stride;
 };
 
-// A thread's elements come in up to kRuns runs whose maxima are kept, `groups`
-// groups of kUnroll vectors each.
+// A thread's units of kUnit vectors come in up to kRuns runs whose maxima are
+// kept, `units` in each.
 constexpr int kRuns = 16;
 
 // What slice_top works with, in shared memory.
 struct TopRoom {
+  alignas(16) uint16_t keys[kThreads];
   int hits[kCandidates];           // thread | run << 8
   uint64_t cand[kCandidates];
   uint64_t scratch[kWarps];
+  uint32_t bound;
   int hit_count, found;
 };
 
+// The largest value that `top` of the 256 keys reach, in one warp: bisection
+// between the smallest and the largest key, which are a few hundred apart in
+// ordinary rows (256 threads that count keys bit by bit behind a barrier each
+// took 1.1 to 2.4 us, this 0.3).
+__device__ __forceinline__ uint32_t nth_key(const uint16_t* keys, int top) {
+  const uint4 w = reinterpret_cast<const uint4*>(keys)[int(threadIdx.x) & 31];
+  const uint32_t k[8] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16, w.z & 0xFFFFu, w.z >> 16, w.w & 0xFFFFu, w.w >> 16};
+  uint32_t lo = k[0], hi = k[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) lo = min(lo, k[i]), hi = max(hi, k[i]);
+  lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
+  if (top == 1) return hi;
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi + 1) >> 1;
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += k[i] >= mid;
+    if (int(__reduce_add_sync(~0u, n)) >= top) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 // The `top` largest elements of the part, in order, as packed words (0: none)
 // to `list` of the cluster's first CTA.  `mine` is the largest of this thread's
-// elements, run_top[run][thread] of each run, `edge` its edge element's id.
+// elements, run_top[run][thread] of each run, `edge` its edge element's id; `x`
+// are the thread's vectors where it has two units of them at most.
 template <typename T>
-__device__ void slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int groups, int edge, int top,
-                          TopRoom& room, uint64_t* list, int ranks) {
-  constexpr int kPer = RowVec<T>::kPer;
+__device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int units, int edge,
+                                          const uint4 (&x)[2][kUnit], int top, TopRoom& room, uint64_t* list, int ranks) {
+  using V = RowVec<T>;
+  constexpr int kPer = V::kPer;
   const int tid = int(threadIdx.x);
-  // 16 bits of the order key: the largest value that `top` of the threads' maxima reach
   const uint32_t key = key_of_bits(__float_as_uint(mine)) >> 16;
-  uint32_t bound = 0;
-#pragma unroll 1
-  for (int bit = 15; bit >= 0; --bit)
-    if (cta_sync_count(key >= (bound | 1u << bit)) >= top) bound |= 1u << bit;
-  const uint32_t least = max(bound << 16, kKeyNegInf + 1u);
+  room.keys[tid] = uint16_t(key);
   if (tid == 0) room.hit_count = room.found = 0;
   __syncthreads();
-  auto take = [&](uint32_t bits, int id) {
-    const uint32_t k = key_of_bits(bits);
-    if (k >= least) {
-      const int place = atomicAdd(&room.found, 1);
-      if (place < kCandidates) room.cand[place] = pack_key_id(k, uint32_t(id));
-    }
-  };
-  if (key >= (least >> 16)) {
-    if (edge >= 0) take(Elem<T>::bits(s.row[edge]), edge);
-    for (int run = 0; run < runs; ++run)
-      if (key_of_bits(__float_as_uint(run_top[run * kThreads + tid])) >= least) {
-        const int place = atomicAdd(&room.hit_count, 1);
-        if (place < kCandidates) room.hits[place] = tid | run << 8;
-      }
+  if (tid < 32) {
+    const uint32_t b = nth_key(room.keys, top);
+    if (tid == 0) room.bound = b;
   }
   __syncthreads();
-  const int hits = room.hit_count, run_vecs = groups * kUnroll;
-  bool listed = hits <= kCandidates;
-  if (listed) {   // the runs' vectors again (from L2), every thread one at a time
-    for (int i = tid; i < hits * run_vecs; i += kThreads) {
-      const int hit = room.hits[i / run_vecs], j = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
-      if (j >= s.full0 && j < s.full1) {
-        const uint4 x = s.vec()[j];
-        const T* e = reinterpret_cast<const T*>(&x);
+  const uint32_t bound = room.bound, least = max(bound << 16, kKeyNegInf + 1u);
+  const float limit = value_of_key(least);
+  auto keep = [&](int place, float v, int id) {
+    if (place < kCandidates) room.cand[place] = pack_key_id(key_of_bits(__float_as_uint(v)), uint32_t(id));
+  };
+  // The elements of kUnit vectors (of the ids at[u], or none: -1) that reach the
+  // limit; one atomic for all of a thread's.
+  auto take = [&](const uint4 (&y)[kUnit], const int (&at)[kUnit]) {
+    uint32_t mask = 0;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) take(Elem<T>::bits(e[q]), s.first + j * kPer + q);
+    for (int u = 0; u < kUnit; ++u) {
+      if (at[u] < 0 || !(V::finish(V::top(y[u], V::kNegInf2)) >= limit)) continue;
+      float v[kPer];
+      V::get(y[u], V::kNegInf2, v);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) mask |= (v[q] >= limit ? 1u : 0u) << (u * kPer + q);
+    }
+    if (mask) {
+      int place = atomicAdd(&room.found, __popc(mask));
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) {
+        if (!(mask >> (u * kPer) & ((1u << kPer) - 1u))) continue;
+        float v[kPer];
+        V::get(y[u], V::kNegInf2, v);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+          if (mask >> (u * kPer + q) & 1u) keep(place++, v[q], at[u] + q);
       }
     }
-    __syncthreads();
-    listed = room.found <= kCandidates;
+  };
+  const bool at_hand = s.full1 <= 2 * kUnit * kThreads;
+  if (mine >= limit) {
+    if (edge >= 0) {
+      const float v = Elem<T>::widen(s.row[edge]);
+      if (v >= limit) keep(atomicAdd(&room.found, 1), v, edge);
+    }
+    if (at_hand) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int at[kUnit];
+#pragma unroll
+        for (int u = 0; u < kUnit; ++u) {
+          const int j = tid + (h * kUnit + u) * kThreads;
+          at[u] = j >= s.full0 && j < s.full1 ? s.first + j * kPer : -1;
+        }
+        take(x[h], at);
+      }
+    } else {
+      uint32_t mask = 0;
+#pragma unroll 4
+      for (int run = 0; run < runs; ++run) mask |= (run_top[run * kThreads + tid] >= limit ? 1u : 0u) << run;
+      int place = mask ? atomicAdd(&room.hit_count, __popc(mask)) : 0;
+      for (; mask; mask &= mask - 1, ++place)
+        if (place < kCandidates) room.hits[place] = tid | (__ffs(mask) - 1) << 8;
+    }
   }
+  __syncthreads();
+  const int hits = room.hit_count, run_vecs = units * kUnit;
+  bool listed = hits <= kCandidates;
+  if (listed && hits) {   // the runs' vectors again (from L2), every thread some at a time
+    for (int i0 = tid; i0 < hits * run_vecs; i0 += kUnit * kThreads) {
+      uint4 y[kUnit];
+      int at[kUnit];
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) {
+        const int i = i0 + u * kThreads;
+        at[u] = -1;
+        if (i < hits * run_vecs) {
+          const int hit = room.hits[i / run_vecs], j = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
+          if (j >= s.full0 && j < s.full1) at[u] = s.first + j * kPer, y[u] = s.vec()[j];
+        }
+      }
+      take(y, at);
+    }
+    __syncthreads();
+  }
+  listed = listed && room.found <= kCandidates;
   const uint32_t to = ranks > 1 ? map_rank(smem_addr(list), 0) : 0;
   auto put = [&](int place, uint64_t v) {
     if (ranks > 1) st_cluster_u64(to + uint32_t(place) * 8u, v);
     else list[place] = v;
   };
-  if (listed) {
+  if (listed) {   // a candidate's place is the number of larger ones: four lanes count for each
     const int have = room.found;
-    for (int i = tid; i < have; i += kThreads) {
-      const uint64_t v = room.cand[i];
-      int rank = 0;
-      for (int j = 0; j < have; ++j) rank += room.cand[j] > v;
-      if (rank < top) put(rank, v);
+    for (int i0 = 0; i0 < have; i0 += kThreads / 4) {
+      const int i = i0 + (tid >> 2);
+      const uint64_t v = i < have ? room.cand[i] : ~0ull;
+      int place = 0;
+#pragma unroll 8
+      for (int j = tid & 3; j < have; j += 4) place += room.cand[j] > v;
+      place += __shfl_xor_sync(~0u, place, 1);
+      place += __shfl_xor_sync(~0u, place, 2);
+      if ((tid & 3) == 0 && i < have && place < top) put(place, v);
     }
     for (int i = have + tid; i < top; i += kThreads) put(i, 0);
   } else {   // many equal values: one maximum after another, each below the last
@@ -158,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
   }
   TopRoom& room = *reinterpret_cast<TopRoom*>(dynamic);
   float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom));
-  const int groups_all = (s.full1 + kThreads * kUnroll - 1) / (kThreads * kUnroll);   // of this CTA
-  const int groups = (groups_all + kRuns - 1) / kRuns, runs = groups ? (groups_all + groups - 1) / groups : 0;
+  const int units_all = (s.full1 + kThreads * kUnit - 1) / (kThreads * kUnit);   // of a thread
+  const int units = (units_all + kRuns - 1) / kRuns, runs = units ? (units_all + units - 1) / units : 0;
   uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThreads);
   int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
   Stats all{-INFINITY, 0.0f, 0.0f};
@@ -167,25 +244,27 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
   if (flags == 0) {
     Running<T, kEntropy> run;
     const int edge = s.edge();
-    if (edge >= 0) run.add_one(clean(load1(z + edge)), temperature, c);
+    const float at_edge = edge >= 0 ? clean(load1(z + edge)) : -INFINITY;
     float best = -INFINITY;
     int in_run = 0, r = 0;
-    stream(s, run, temperature, c, [](uint4&, int) {}, [&](float top) {
+    uint4 x[2][kUnit];
+    stream(s, run, x, temperature, c, [](uint4&, int) {}, [&](float top) {
       if (kTop) {
         best = fmaxf(best, top);
-        if (++in_run == groups) {
+        if (++in_run == units) {
           run_top[r * kThreads + tid] = best;
           best = -INFINITY, in_run = 0, ++r;
         }
       }
     });
+    run.add_one(at_edge, temperature, c);
     if (kTop) {
       for (; r < runs; ++r, best = -INFINITY) run_top[r * kThreads + tid] = best;
     }
     const Stats part = warp_join(run.stats(), c);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
-    if (kTop) slice_top(s, run.m, run_top, runs, groups, edge, a.top, room, lists + rank * a.top, ranks);
+    if (kTop) slice_top(s, run.m, run_top, runs, units, edge, x, a.top, room, lists + rank * a.top, ranks);
     __syncthreads();
     if (warp == 0) {
       const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
@@ -218,34 +297,40 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
       for (int i = tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = nan;
       return;
     }
-    // how many of the lists' entries are tokens, at most `top`
-    int some = 0;
-    for (int e = tid; e < ranks * a.top; e += kThreads) some += lists[e] != 0;
-    if (tid == 0) room.found = 0;
-    __syncthreads();
-    if (some) atomicAdd(&room.found, some);
+    if (ranks == 1) {   // one list, in order
+      for (int i = tid; i < a.top; i += kThreads) {
+        const uint64_t v = lists[i];
+        top_ids[i] = v ? int32_t(~uint32_t(v)) : -1;
+        top_logprobs[i] = v ? logprob(value_of_key(uint32_t(v >> 32))) : -INFINITY;
+      }
+      return;
+    }
+    // A token's place is the number of larger ones in all lists, by bisection in
+    // all of them at once.  An entry that is none finds all tokens larger: those of
+    // list 0 fill the places that are left.
     for (int e = tid; e < ranks * a.top; e += kThreads) {
       const uint64_t v = lists[e];
-      if (v == 0) continue;
-      const int from = e / a.top;
-      int place = e - from * a.top;
-      for (int r = 0; r < ranks && place < a.top; ++r) {
-        if (r == from) continue;
-        int lo = 0, hi = a.top;   // the entries of list r above v
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (lists[r * a.top + mid] > v) lo = mid + 1;
-          else hi = mid;
+      int lo[kMaxParts], hi[kMaxParts];
+#pragma unroll
+      for (int r = 0; r < kMaxParts; ++r) lo[r] = 0, hi[r] = r < ranks ? a.top : 0;
+      for (int left = a.top; left > 0; left >>= 1) {
+#pragma unroll
+        for (int r = 0; r < kMaxParts; ++r) {
+          const int mid = (lo[r] + hi[r]) >> 1;
+          if (lo[r] < hi[r]) {
+            if (lists[r * a.top + mid] > v) lo[r] = mid + 1;
+            else hi[r] = mid;
+          }
         }
-        place += lo;
       }
+      int place = v ? 0 : e < a.top ? e - lo[0] : a.top;
+#pragma unroll
+      for (int r = 0; r < kMaxParts; ++r) place += lo[r];
       if (place < a.top) {
-        top_ids[place] = int32_t(~uint32_t(v));
-        top_logprobs[place] = logprob(value_of_key(uint32_t(v >> 32)));
+        top_ids[place] = v ? int32_t(~uint32_t(v)) : -1;
+        top_logprobs[place] = v ? logprob(value_of_key(uint32_t(v >> 32))) : -INFINITY;
       }
     }
-    __syncthreads();
-    for (int i = room.found + tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = -INFINITY;
   }
 }
 
@@ -359,8 +444,8 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
   const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
   if (ok != SMP_OK) return ok;
   if (a.top) {
-    const int per_group = kThreads * kUnroll * RowVec<T>::kPer;
-    a.run_room = std::min(kRuns, (a.rows.slice + per_group - 1) / per_group);
+    const int unit = kThreads * kUnit * RowVec<T>::kPer;
+    a.run_room = std::min(kRuns, (a.rows.slice + unit - 1) / unit);
     ls.smem = sizeof(TopRoom) + size_t(a.run_room) * kThreads * 4 + size_t(ls.cluster) * a.top * 8;
   }
   return launch_rows(kernel, a, ls, st);
