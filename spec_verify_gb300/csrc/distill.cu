@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
   uint4 x[2][kUnit];
   stream(
       s, run, x, temperature, c,
-      [&](uint4& y, int j) {
+      [&](uint4& y, int k) {
+        const int j = s.full0 + k;
         if (j < s.full1) {
           const uint32_t b = Part<T>::kPer == 8 ? bytes[j] : bytes[j >> 1] >> (4 * (j & 1)) & 15u;
           if (b) erase(y, b, T{});

@@ -343,8 +343,8 @@ __device__ __forceinline__ Stats warp_stats(const Slice<T>& s, float mine, float
 // ------------------------------------------------------------------ a part of a row, read once from memory
 
 // Elements [lo, hi) of a row, whole vectors [full0, full1) of 16 bytes counted
-// from element `first`; thread t takes vectors t, t + kThreads, ... and the edge
-// threads one element each outside them.
+// from element `first`; thread t takes vectors full0 + t, full0 + t + kThreads,
+// ... and the edge threads one element each outside them.
 template <typename T>
 struct Part {
   static constexpr int kPer = RowVec<T>::kPer;
@@ -378,22 +378,26 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
 constexpr int kUnit = 4;     // vectors of a thread that are loaded and taken in together
 
 // Takes the part's whole vectors into `run`, a unit per thread at a time: while
-// one unit is taken in, the next is on its way, in x[0] and x[1], which keep the
-// last two (with one unit in flight 4093 rows of 152064 took 229 us, with two
-// that were loaded together 208 to 221).  change(y, j) may alter vector j first;
-// seen(top) gets the largest element of each unit, in order.
+// one unit is taken in, the next is on its way, in x[0] and x[1], which hold all
+// of the thread's vectors where there are two units at most.  change(y, k) may
+// alter vector k (from the first whole one) first; seen(top) gets the largest
+// element of each unit, in order.
 template <typename T, bool kWeighted, typename Change, typename Seen>
 __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, uint4 (&x)[2][kUnit],
                                        const float& temperature, const float& c, Change&& change, Seen&& seen) {
   using V = RowVec<T>;
-  const int units = (s.full1 + kUnit * kThreads - 1) / (kUnit * kThreads);
-  auto load = [&](uint4 (&y)[kUnit], int unit) {
-    const int j0 = int(threadIdx.x) + unit * (kUnit * kThreads);
+  constexpr int kStep = kUnit * kThreads;
+  const int vecs = s.full1 - s.full0, pairs = vecs / (2 * kStep);
+  const uint4* p = s.vec() + s.full0 + threadIdx.x;
+  auto load = [&](uint4 (&y)[kUnit], const uint4* from) {
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) y[u] = load_once(from + u * kThreads);
+  };
+  auto load_some = [&](uint4 (&y)[kUnit], int unit) {
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
-      const int j = j0 + u * kThreads;
       y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
-      if (j >= s.full0 && j < s.full1) y[u] = load_once(s.vec() + j);
+      if (int(threadIdx.x) + unit * kStep + u * kThreads < vecs) y[u] = load_once(p + unit * kStep + u * kThreads);
     }
   };
   auto take = [&](uint4 (&y)[kUnit], int unit) {
@@ -411,15 +415,24 @@ __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& 
     }
     seen(top);
   };
-  if (units > 0) load(x[0], 0);
-  if (units > 1) load(x[1], 1);
-  for (int q = 0; q < units; q += 2) {
-    take(x[0], q);
-    if (q + 2 < units) load(x[0], q + 2);
-    if (q + 1 < units) {
-      take(x[1], q + 1);
-      if (q + 3 < units) load(x[1], q + 3);
+  if (pairs > 0) {
+    load(x[0], p), load(x[1], p + kStep);
+    for (int q = 0;; ++q) {
+      take(x[0], 2 * q);
+      if (q + 1 == pairs) break;
+      load(x[0], p + (2 * q + 2) * kStep);
+      take(x[1], 2 * q + 1);
+      load(x[1], p + (2 * q + 3) * kStep);
     }
+    load_some(x[0], 2 * pairs);
+    take(x[1], 2 * pairs - 1);
+  } else {
+    load_some(x[0], 0);
+  }
+  if (2 * pairs * kStep < vecs) {   // what two whole units leave
+    load_some(x[1], 2 * pairs + 1);
+    take(x[0], 2 * pairs);
+    if ((2 * pairs + 1) * kStep < vecs) take(x[1], 2 * pairs + 1);
   }
 }
 

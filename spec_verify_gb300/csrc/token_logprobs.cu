@@ -128,7 +128,8 @@ __device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const fl
       }
     }
   };
-  const bool at_hand = s.full1 <= 2 * kUnit * kThreads;
+  const int vecs = s.full1 - s.full0;
+  const bool at_hand = vecs < 2 * kUnit * kThreads;
   if (mine >= limit) {
     if (edge >= 0) {
       const float v = Elem<T>::widen(s.row[edge]);
@@ -140,8 +141,8 @@ __device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const fl
         int at[kUnit];
 #pragma unroll
         for (int u = 0; u < kUnit; ++u) {
-          const int j = tid + (h * kUnit + u) * kThreads;
-          at[u] = j >= s.full0 && j < s.full1 ? s.first + j * kPer : -1;
+          const int k = tid + (h * kUnit + u) * kThreads;
+          at[u] = k < vecs ? s.first + (s.full0 + k) * kPer : -1;
         }
         take(x[h], at);
       }
@@ -166,8 +167,8 @@ __device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const fl
         const int i = i0 + u * kThreads;
         at[u] = -1;
         if (i < hits * run_vecs) {
-          const int hit = room.hits[i / run_vecs], j = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
-          if (j >= s.full0 && j < s.full1) at[u] = s.first + j * kPer, y[u] = s.vec()[j];
+          const int hit = room.hits[i / run_vecs], k = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
+          if (k < vecs) at[u] = s.first + (s.full0 + k) * kPer, y[u] = s.vec()[s.full0 + k];
         }
       }
       take(y, at);
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
   }
   TopRoom& room = *reinterpret_cast<TopRoom*>(dynamic);
   float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom));
-  const int units_all = (s.full1 + kThreads * kUnit - 1) / (kThreads * kUnit);   // of a thread
+  const int units_all = (s.full1 - s.full0 + kThreads * kUnit - 1) / (kThreads * kUnit);   // of a thread
   const int units = (units_all + kRuns - 1) / kRuns, runs = units ? (units_all + units - 1) / units : 0;
   uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThreads);
   int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
