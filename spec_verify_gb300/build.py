@@ -33,7 +33,7 @@ SOURCES = ["api.cu", "sample.cu", "verify.cu", "prepass.cu", "beam.cu", "verify_
            "norm_rope.cu", "cache_append.cu", "cache_attention.cu", "attention_e4m3_bf16.cu",
            "attention_e4m3_f32.cu", "attention_i8_bf16.cu", "attention_i8_f32.cu", "token_logprobs.cu", "distill.cu"]
 HEADERS = ["common.cuh", "row_ops.cuh", "select.cuh", "general.cuh", "launch.h", "exp_table.h", "tma.cuh", "general_bf16.cuh",
-           "cache.cuh", "cache_attention.cuh", "attention_rows.h", "scores.cuh"]
+           "cache.cuh", "cache_attention.cuh", "attention_rows.h", "scores.cuh", "row_grad.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

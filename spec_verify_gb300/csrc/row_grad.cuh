@@ -1,0 +1,468 @@
+// The gradient of a row's loss in its logits, for distillation and for log
+// probabilities with entropies: every logit read once, every gradient written
+// once.
+//
+// A row belongs to the CTAs of one cluster, which each keep a slice of it in shared
+// memory: fetched by bulk copies, summed, turned into gradients in place once the
+// cluster's sums are known, and sent off by bulk copies.  Three CTAs stand on an
+// SM, so that one loads or stores while the others compute.  What the teacher's row
+// gives (or the gradients of the log probabilities) is worked up by a ninth warp
+// while the slice arrives and is summed.
+//
+// Mathematics (scores.cuh for the sums).  Distillation, with R the statistics
+// outside the teacher's ids (whose places hold -inf while the rest is summed, so
+// that the student's mass outside them is a sum of its own and not a difference)
+// and m, Z those of the whole row:
+//   ln s_j = (z_j - m) / T - ln Z,   ln s_rest = (m_R - m) / T + ln Z_R - ln Z,
+//   dz_j = 2^((z_j - m_R) c) (w / T) ((sum t + r) 2^((m_R - m) c) / Z - r / Z_R)
+// outside the ids, (w / T) (s_j (sum t + r) - t) on them.  Log probabilities:
+//   dz_j = 2^((z_j - m) c) (A + B (z_j - m)) + (1 / T) (the id's own g),
+//   B = -h / (T^2 Z),  A = -(G - h S / (T Z)) / (T Z).
+#pragma once
+
+#include "scores.cuh"
+
+namespace smp {
+
+struct RowGradArgs {
+  RowsArgs rows;
+  const int32_t* ids;
+  const float* values;       // the teacher's log probabilities, or the gradients of the log probabilities
+  int count, tail;
+  const float* weights;      // distillation: of the rows; else: the gradients of the entropies
+  float* loss;               // distillation alone
+  void* grad;
+  int64_t grad_stride;
+};
+
+// ------------------------------------------------------------------ the slice of a row
+
+// Elements [lo, hi) of a row in shared memory at `buf`, element `id` at
+// buf[id - first]; the row is laid out as in memory modulo 16 bytes, so that its
+// whole vectors [full0, full1) go by bulk copies.  The edge vectors hold -inf
+// outside the row.
+template <typename T>
+struct Slice {
+  static constexpr int kPer = RowVec<T>::kPer;
+  static constexpr uint32_t kPiece = 16384;
+  T* buf;
+  int first, lo, hi, vecs, full0, full1;
+
+  __device__ __forceinline__ Slice(T* b, const T* row, int vocab, int slice, int rank) : buf(b) {
+    first = rank * slice - int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    lo = max(first, 0), hi = max(lo, min(first + slice, vocab));
+    vecs = hi > lo ? (hi - first + kPer - 1) / kPer : 0;
+    full0 = first < 0 && vecs ? 1 : 0;
+    full1 = vecs ? max(full0, (hi - first) / kPer) : 0;
+  }
+  __device__ __forceinline__ bool holds(int id) const { return id >= lo && id < hi; }
+  __device__ __forceinline__ float at(int id) const { return clean(load1(buf + (id - first))); }
+  __device__ __forceinline__ uint4* vec() const { return reinterpret_cast<uint4*>(buf); }
+  // The id of this lane's edge element, or -1.
+  __device__ __forceinline__ int edge() const {
+    const int lane = int(threadIdx.x) & 31, id = lane < kPer ? first + lane : first + full1 * kPer + lane - kPer;
+    return lane < 2 * kPer && (lane < kPer ? full0 > 0 : full1 < vecs) ? id : INT_MIN;
+  }
+
+  // One warp: starts the copy of the slice, whose bytes `bar` is told to expect,
+  // and fills the edges.
+  __device__ __forceinline__ void fetch(const T* row, int vocab, uint64_t* bar) const {
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t bytes = uint32_t(full1 - full0) * 16u;
+      const uint64_t policy = evict_first_policy();
+      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+      const char* src = reinterpret_cast<const char*>(row + first + full0 * kPer);
+      char* dst = reinterpret_cast<char*>(buf) + full0 * 16;
+      for (uint32_t at = 0; at < bytes; at += kPiece)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+            "%4;" ::"r"(smem_addr(dst + at)),
+            "l"(src + at), "r"(min(kPiece, bytes - at)), "r"(smem_addr(bar)), "l"(policy)
+            : "memory");
+    }
+    const int id = edge();
+    if (id != INT_MIN) buf[id - first] = id >= 0 && id < vocab ? row[id] : RowVec<T>::minus_inf();
+  }
+
+  // All workers: writes the slice to a row of the output, by bulk copies where
+  // that is aligned as the slice is; returns once `buf` has been read.
+  __device__ __forceinline__ void leave(T* row) const {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    cta_sync();
+    if ((reinterpret_cast<uintptr_t>(row + first) & 15u) != 0) {
+      for (int id = lo + int(threadIdx.x); id < hi; id += kThreads) row[id] = buf[id - first];
+    } else if (threadIdx.x < 32) {
+      if (threadIdx.x == 0) {
+        const uint32_t bytes = uint32_t(full1 - full0) * 16u;
+        char* dst = reinterpret_cast<char*>(row + first + full0 * kPer);
+        const char* src = reinterpret_cast<const char*>(buf) + full0 * 16;
+        for (uint32_t at = 0; at < bytes; at += kPiece)
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + at), "r"(smem_addr(src + at)),
+                       "r"(min(kPiece, bytes - at))
+                       : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      const int id = edge();
+      if (holds(id)) row[id] = buf[id - first];
+      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+  }
+  // All workers: the same value everywhere.
+  __device__ __forceinline__ void fill(float x) const {
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = x;
+    const uint4 w = RowVec<T>::put(v);
+    for (int j = int(threadIdx.x); j < vecs; j += kThreads) vec()[j] = w;
+  }
+};
+
+constexpr int kLearner = kWarps, kRowThreads = kThreads + 32;
+
+// ------------------------------------------------------------------ what is known of a row before it is read
+
+struct RowFacts {
+  int flags;                  // found among the values
+  float scale, given, rest, t_log_t;   // distillation: w / T, sum t, r, sum t ln t
+  float sum;                  // else: G
+  Stats on_ids;               // distillation: of the ids' logits
+  alignas(16) int ids[kMaxIds];   // of the places that are the first of their id, -1 elsewhere
+  float add[kMaxIds];         // the sum of t (or of g) over all places of the id
+  float logit[kMaxIds];       // the student's
+};
+
+// Leaves the ids' first places alone, with the sum of `add` over equal ids, and
+// returns how many they are.
+__device__ __forceinline__ int keep_firsts(int* ids, float* add, int count) {
+  const int lane = int(threadIdx.x) & 31;
+  constexpr int kEach = kMaxIds / 32;
+  int id[kEach], place[kEach];   // the id's first place
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    id[i] = 32 * i < count ? ids[lane + 32 * i] : -1;
+    place[i] = lane + 32 * i;
+  }
+  bool again = false;
+#pragma unroll 1
+  for (int n = (count - 1) & ~3; n >= 0; n -= 4) {   // the places behind `count` hold -1
+    const int4 v = *reinterpret_cast<const int4*>(ids + n);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (32 * i >= count) break;
+      place[i] = v.w == id[i] ? n + 3 : place[i];
+      place[i] = v.z == id[i] ? n + 2 : place[i];
+      place[i] = v.y == id[i] ? n + 1 : place[i];
+      place[i] = v.x == id[i] ? n : place[i];
+    }
+  }
+  int firsts = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool repeats = id[i] >= 0 && place[i] < lane + 32 * i;
+    again |= repeats;
+    firsts += __popc(__ballot_sync(~0u, id[i] >= 0 && !repeats));
+  }
+  if (!__any_sync(~0u, again)) return firsts;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (32 * i >= count) break;
+    const int k = lane + 32 * i;
+    float sum = 0.0f;
+    if (id[i] >= 0 && place[i] == k) {
+      for (int n = 0; n < count; ++n)
+        if (ids[n] == id[i]) sum += add[n];
+    }
+    if (place[i] < k) id[i] = -1;
+    __syncwarp();
+    if (id[i] >= 0) add[k] = sum;   // read by no other place any more: theirs are other ids
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (32 * i < count) ids[lane + 32 * i] = id[i];
+  return firsts;
+}
+
+// Fills `f`, of a row whose ids are good (one warp).
+template <typename T, bool kDistill>
+__device__ __forceinline__ void learn_row(const RowGradArgs& a, int row, const T* z, float temperature, float weight,
+                                          RowFacts& f) {
+  const int lane = int(threadIdx.x) & 31;
+  constexpr int kEach = kMaxIds / 32;
+  float v[kEach], logit[kEach];
+  int id[kEach];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = lane + 32 * i;
+    id[i] = k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
+    v[i] = k < a.count ? a.values[int64_t(row) * a.count + k] : 0.0f;
+  }
+  // every CTA has all of the ids' logits: what they add to Z needs no exchange
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    logit[i] = id[i] >= 0 ? clean(load1(z + id[i])) : -INFINITY;
+    if (id[i] < 0) v[i] = kDistill ? -INFINITY : 0.0f;
+  }
+  int flags = 0;
+  float sum = 0.0f;
+  if (kDistill) {
+    float top = -INFINITY, given = 1.0f, rest = 0.0f, log_sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) bad |= !(v[i] < INFINITY), top = fmaxf(top, v[i]);
+    if (a.tail) {   // r = 1 - sum t is a small difference: from fixed-point exponentials, exact to 2^-45 each
+      uint64_t mass = 0;
+      const RowScale unit = make_row_scale_unit(0.0f);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (32 * i < a.count) mass += id[i] >= 0 ? mass_fixed(fminf(v[i], 1.0f), unit, kExp2Table) : 0;
+      mass = warp_sum<uint64_t>(mass);
+      bad |= mass > kFixedOne + (kFixedOne >> 6);
+      given = float(mass) * 0x1p-44f;
+      rest = mass < kFixedOne ? float(kFixedOne - mass) * 0x1p-44f : 0.0f;
+    } else {
+      top = warp_max_f(top);
+      bad |= !(top > -INFINITY);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum += expf(__fsub_rn(v[i], top));
+      log_sum = __fadd_rn(top, logf(warp_sum_f(sum)));
+    }
+    float t_log_t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const float log_t = __fsub_rn(v[i], log_sum), t = id[i] >= 0 ? expf(log_t) : 0.0f;
+      if (t > 0.0f) t_log_t = __fmaf_rn(t, log_t, t_log_t);
+      v[i] = t;
+    }
+    t_log_t = warp_sum_f(t_log_t);
+    if (__any_sync(~0u, bad)) flags |= kRowBadParams;
+    if (lane == 0) f.scale = __fdiv_rn(weight, temperature), f.given = given, f.rest = rest, f.t_log_t = t_log_t;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += v[i];
+    sum = warp_sum_f(sum);
+    if (lane == 0) f.sum = sum;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    f.ids[lane + 32 * i] = id[i], f.add[lane + 32 * i] = v[i], f.logit[lane + 32 * i] = logit[i];
+  __syncwarp();
+  keep_firsts(f.ids, f.add, a.count);
+  if (kDistill) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) top = fmaxf(top, logit[i]);
+    Stats k{warp_max_f(top), 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (f.ids[lane + 32 * i] >= 0 && logit[i] > -INFINITY)
+        k.z += ex2_approx(__fmul_rn(__fsub_rn(logit[i], k.m), __fdiv_rn(kLog2e, temperature)));
+    k.z = warp_sum_f(k.z);
+    if (lane == 0) f.on_ids = k;
+  }
+  if (lane == 0) f.flags = flags;
+}
+
+// ------------------------------------------------------------------ the sweeps
+
+// The statistics of this warp's share of the slice.
+template <typename T, bool kWeighted>
+__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c) {
+  using V = RowVec<T>;
+  Running<T, kWeighted> run;
+  const pair_t c2 = both(c);
+  const uint4* p = s.vec() + threadIdx.x;
+  auto take = [&](const uint4 (&y)[kUnit]) {
+    uint32_t w = V::kNegInf2;
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) w = V::top(y[u], w);
+    run.raise(V::finish(w), temperature, c);
+    if (run.m > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) run.add(y[u], c2);
+    }
+  };
+  int j = 0;
+#pragma unroll 1
+  for (; j + kUnit * kThreads <= s.vecs; j += kUnit * kThreads) {
+    uint4 y[kUnit];
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
+    take(y);
+  }
+  if (j < s.vecs) {
+    uint4 y[kUnit];
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
+      if (int(threadIdx.x) + j + u * kThreads < s.vecs) y[u] = p[j + u * kThreads];
+    }
+    take(y);
+  }
+  return warp_join<kWeighted>(run.stats(), c);
+}
+
+// Replaces the slice's elements z by 2^((z - m) c) (A + B (z - m)).
+template <typename T, bool kWeighted>
+__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb) {
+  using V = RowVec<T>;
+  const uint32_t floor = floor_word<T>(m, temperature);
+  uint4* p = s.vec();
+  const pair_t minus_m = both(-m), c2 = both(c), ca2 = both(ca), cb2 = both(cb);
+  auto turn = [&](const uint4& x) {
+    pair_t v[V::kPer / 2];
+    float r[V::kPer];
+    V::get(x, floor, v);
+#pragma unroll
+    for (int i = 0; i < V::kPer / 2; ++i) {
+      const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c2));
+      const pair_t plain = mul2(e, ca2);
+      parts(kWeighted ? fma2(mul2(e, d), cb2, plain) : plain, r[2 * i], r[2 * i + 1]);   // B d may overflow, e d not
+    }
+    return V::put(r);
+  };
+  int j = int(threadIdx.x);
+#pragma unroll 1
+  for (; j + 3 * kThreads < s.vecs; j += 4 * kThreads) {
+    uint4 y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] = p[j + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) p[j + u * kThreads] = turn(y[u]);
+  }
+#pragma unroll 1
+  for (; j < s.vecs; j += kThreads) p[j] = turn(p[j]);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <typename T, bool kDistill>
+__global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_constant__ RowGradArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];   // the slice
+  __shared__ Meeting meet;
+  __shared__ RowFacts f;
+  __shared__ uint64_t bar;
+  const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  allow_dependent_launch();
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  T* out = static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride;
+  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  grid_dependency_wait();
+  cluster_arrive_early(ranks);
+  const float temperature = row_temperature(a.rows, row);
+  const float weight = a.weights ? a.weights[row] : kDistill ? 1.0f : 0.0f;
+  int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  const bool some = __syncthreads_or(id >= 0) || (!kDistill && weight != 0.0f), past = __syncthreads_or(id >= a.rows.vocab);
+  int flags = !some ? 0 : (past ? kRowBadToken : 0) | (temperature_fits(temperature) ? 0 : kRowBadParams);
+  const bool read = some && !flags;
+  if (read && warp == 0) {
+    s.fetch(z, a.rows.vocab, &bar);
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&bar)) : "memory");
+  }
+  const float nan = __uint_as_float(0x7FC00000u), c = __fdiv_rn(kLog2e, temperature);
+  if (!read) {
+    cluster_all_run(ranks);
+    if (warp == kLearner) {
+      if (rank == 0 && lane == 0) {
+        if (kDistill) a.loss[row] = flags ? nan : 0.0f;
+        if (flags && a.rows.status) atomicOr(a.rows.status, flags);
+      }
+      return;
+    }
+    s.fill(flags ? nan : 0.0f);
+    s.leave(out);
+    return;
+  }
+  bool late = false;
+  if (warp == kLearner) {
+    learn_row<T, kDistill>(a, row, z, temperature, weight, f);
+    cluster_all_run(ranks);
+  } else {
+    late = !wait_full(&bar, 0, a.rows.wait_limit);
+    if (late) wait_full(&bar, 0, kWaitLimitNs);   // the copy lands in this CTA's memory: not before that is over
+    if (kDistill && s.holds(id)) s.buf[id - s.first] = RowVec<T>::minus_inf();
+    late = cta_sync_count(late) > 0;
+    const bool weighted = !kDistill && weight != 0.0f;
+    const Stats part = weighted ? slice_stats<T, true>(s, temperature, c) : slice_stats<T, false>(s, temperature, c);
+    if (lane == 0) meet.warp[warp] = part;
+    cluster_all_run(ranks);
+    cta_sync();
+    if (warp == 0) {
+      const Stats none{-INFINITY, 0.0f, 0.0f}, mine = lane < kWarps ? meet.warp[lane] : none;
+      const Stats cta = weighted ? warp_join<true>(mine, c) : warp_join<false>(mine, c);
+      post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
+    }
+  }
+  cluster_meet(ranks);
+  const float4 p = posted(meet, ranks);
+  if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
+  float m, ca = 0.0f, cb = 0.0f, share = 0.0f;   // share: of this thread's id, by itself
+  id = tid < kMaxIds ? f.ids[tid] : -1;
+  const bool here = s.holds(id);
+  if (kDistill) {
+    const Stats all = warp_join<false>(Stats{p.x, p.y, 0.0f}, c);
+    const Whole whole(all, f.on_ids, c);
+    if (!flags) flags = f.flags ? f.flags : fabsf(whole.m) < INFINITY ? 0 : kRowNonFinite;
+    const float rest = all.z > 0.0f ? f.rest : 0.0f, total = rest > 0.0f ? 1.0f : f.given, inv_z = __frcp_rn(whole.zsum);
+    if (warp == kLearner) {
+      if (rank == 0) {
+        const float loss = row_loss(f.ids, f.add, f.logit, kMaxIds, f.t_log_t, all, whole.m, whole.zsum, rest, temperature);
+        if (lane == 0) a.loss[row] = flags ? nan : loss;
+      }
+    }
+    m = all.z > 0.0f ? all.m : 0.0f;   // nothing outside the ids: any finite reference
+    if (all.z > 0.0f) ca = f.scale * (total * whole.reach * inv_z - __fmul_rn(rest, __frcp_rn(all.z)));
+    if (here) {
+      const float value = f.logit[tid];
+      const float p_id = value > -INFINITY ? __fmul_rn(ex2_approx(__fmul_rn(__fsub_rn(value, whole.m), c)), inv_z) : 0.0f;
+      share = __fmul_rn(f.scale, __fmaf_rn(p_id, total, -f.add[tid]));
+    }
+  } else {
+    const Stats all = weight != 0.0f ? warp_join<true>(Stats{p.x, p.y, p.z}, c) : warp_join<false>(Stats{p.x, p.y, 0.0f}, c);
+    if (!flags && !(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
+    const float inv_t = __frcp_rn(temperature), inv_z = __frcp_rn(all.z), ht = __fmul_rn(weight, inv_t);
+    m = all.m;
+    ca = -__fmul_rn(__fmul_rn(__fmaf_rn(-ht, __fmul_rn(all.s, inv_z), f.sum), inv_t), inv_z);
+    cb = -__fmul_rn(__fmul_rn(ht, inv_t), inv_z);
+    if (here) {
+      const float d = __fsub_rn(f.logit[tid], m), e = ex2_approx(__fmul_rn(d, c));
+      share = __fmaf_rn(f.add[tid], inv_t, e == 0.0f ? 0.0f : __fmaf_rn(cb, __fmul_rn(e, d), __fmul_rn(e, ca)));
+    }
+  }
+  if (warp == kLearner) {
+    if (flags && rank == 0 && lane == 0 && a.rows.status) atomicOr(a.rows.status, flags);
+    return;
+  }
+  if (flags) s.fill(nan);
+  else if (!kDistill && weight != 0.0f && !is_lowest<T>(m)) slice_grad<T, true>(s, m, temperature, c, ca, cb);
+  else slice_grad<T, false>(s, m, temperature, c, ca, 0.0f);
+  cta_sync();
+  if (here && !flags) store1(s.buf + (id - s.first), share);
+  s.leave(out);
+}
+
+template <typename T, bool kDistill>
+smp_status launch_row_grad(RowGradArgs a, cudaStream_t st) {
+  LaunchShape ls;
+  const int dev = current_device();
+  if (dev < 0) return fail_cuda(cudaGetLastError());
+  // As few CTAs per row as let three of them stand on an SM; more where rows are few.
+  const int elem = int(sizeof(T)), per = 16 / elem;
+  auto slice = [&](int c) { return ((a.rows.vocab + per - 1 + c - 1) / c + per - 1) / per * per; };
+  int c = 1;
+  while (c < 16 && slice(c) * elem > 72 * 1024) c *= 2;
+  while (c < 8 && int64_t(a.rows.rows) * c * 2 <= int64_t(device_sms(dev)) * 3 && slice(c) * elem >= 32 * 1024) c *= 2;
+  if (forced_cluster() && slice(forced_cluster()) * elem <= 200 * 1024) c = forced_cluster();
+  ls.cluster = c;
+  a.rows.slice = slice(c);
+  ls.smem = size_t(a.rows.slice) * elem;
+  return launch_rows(reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill>), a, ls, st, kRowThreads);
+}
+
+}  // namespace smp

@@ -8,13 +8,15 @@
 // it out.  The CTAs' sums meet in distributed shared memory; one cluster
 // barrier per row.
 //
-// Mathematics: with m the maximum and c = log2(e) / T,
+// Mathematics: with m near the maximum and c = log2(e) / T,
 //   Z = sum 2^((z - m) c),  S = sum 2^((z - m) c) (z - m),
 //   ln p_j = (z_j - m) / T - ln Z,  H = ln Z - S / (T Z).
-// Parts with maxima m_i join as Z = sum Z_i w_i, S = sum w_i (S_i + Z_i (m_i -
+// Parts with references m_i join as Z = sum Z_i w_i, S = sum w_i (S_i + Z_i (m_i -
 // m)), w_i = 2^((m_i - m) c): a warp takes its own maximum as its reference, a
 // CTA joins its warps and every CTA the cluster's.
 #pragma once
+
+#include <limits.h>
 
 #include <algorithm>
 
@@ -42,8 +44,9 @@ struct RowsArgs {
   uint64_t wait_limit;
 };
 
-// The statistics of some elements: their maximum, sum 2^((z - m) c) and, where
-// wanted, the same weighted by z - m.  No elements: -inf, 0, 0.
+// The statistics of some elements: one of them that none exceeds by much, sum
+// 2^((z - m) c) and, where wanted, the same weighted by z - m.  No elements: -inf,
+// 0, 0; +inf among them: m is +inf.
 struct Stats {
   float m, z, s;
 };
@@ -75,6 +78,12 @@ struct RowVec<uint16_t> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_low(w[i]), v[2 * i + 1] = bf16_high(w[i]);
   }
+  static __device__ __forceinline__ void get(const uint4& x, uint32_t floor, uint64_t (&v)[4]) {
+    const uint32_t w[4] = {max2(x.x, floor), max2(x.y, floor), max2(x.z, floor), max2(x.w, floor)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(bf16_low(w[i])), "f"(bf16_high(w[i])));
+  }
   static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   }
@@ -101,6 +110,10 @@ struct RowVec<float> {
   static __device__ __forceinline__ void get(const uint4& x, uint32_t floor, float (&v)[4]) {
     v[0] = __uint_as_float(max2(x.x, floor)), v[1] = __uint_as_float(max2(x.y, floor));
     v[2] = __uint_as_float(max2(x.z, floor)), v[3] = __uint_as_float(max2(x.w, floor));
+  }
+  static __device__ __forceinline__ void get(const uint4& x, uint32_t floor, uint64_t (&v)[2]) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v[0]) : "r"(max2(x.x, floor)), "r"(max2(x.y, floor)));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v[1]) : "r"(max2(x.z, floor)), "r"(max2(x.w, floor)));
   }
   static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
@@ -138,102 +151,12 @@ __device__ __forceinline__ uint32_t floor_word(float m, float temperature) {
 // A logit as the sampler reads it: NaN is -inf.
 __device__ __forceinline__ float clean(float z) { return z == z ? z : __uint_as_float(0xFF800000u); }
 
-// ------------------------------------------------------------------ the slice of a row
-
-// Elements [lo, hi) of a row in `buf`, element `id` at buf[id - first]; the row
-// is laid out as in memory modulo 16 bytes, so that its whole vectors [full0,
-// full1) go by bulk copies.  The edge vectors hold -inf outside the row.
-template <typename T>
-struct Slice {
-  static constexpr int kPer = RowVec<T>::kPer;
-  T* buf;
-  int first, lo, hi, vecs, full0, full1;
-
-  __device__ __forceinline__ Slice(T* b, const T* row, int vocab, int slice, int rank) : buf(b) {
-    first = rank * slice - int((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    lo = max(first, 0), hi = max(lo, min(first + slice, vocab));
-    vecs = hi > lo ? (hi - first + kPer - 1) / kPer : 0;
-    full0 = first < 0 && vecs ? 1 : 0;
-    full1 = vecs ? max(full0, (hi - first) / kPer) : 0;
-  }
-  __device__ __forceinline__ bool holds(int id) const { return id >= lo && id < hi; }
-  __device__ __forceinline__ float at(int id) const { return clean(load1(buf + (id - first))); }
-  __device__ __forceinline__ uint4* vec() const { return reinterpret_cast<uint4*>(buf); }
-
-  // Starts the copy of the slice (thread 0), and fills the edges (every thread).
-  __device__ __forceinline__ void load(const T* row, int vocab, uint64_t* bar) const {
-    if (threadIdx.x == 0) {
-      const uint32_t bytes = uint32_t(full1 - full0) * 16u;
-      const uint64_t policy = evict_first_policy();
-      asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
-                   : "memory");
-      const char* src = reinterpret_cast<const char*>(row + first + full0 * kPer);
-      char* dst = reinterpret_cast<char*>(buf) + full0 * 16;
-      for (uint32_t at = 0; at < bytes; at += kPiece)
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
-            "%4;" ::"r"(smem_addr(dst + at)),
-            "l"(src + at), "r"(min(kPiece, bytes - at)), "r"(smem_addr(bar)), "l"(policy)
-            : "memory");
-    }
-    if (threadIdx.x < 2 * kPer) {
-      const int i = int(threadIdx.x) % kPer;
-      const bool head = int(threadIdx.x) < kPer;
-      if (head ? full0 > 0 : full1 < vecs) {
-        const int id = first + (head ? 0 : full1 * kPer) + i;
-        buf[id - first] = id >= 0 && id < vocab ? row[id] : RowVec<T>::minus_inf();
-      }
-    }
-  }
-
-  // Writes the slice to a row of the output, whole vectors by a bulk copy where
-  // the output row is aligned as the slice is.  Called by all threads after the
-  // last change of `buf`; returns once `buf` has been read.
-  __device__ __forceinline__ void store(T* row) const {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
-    const bool bulk = (reinterpret_cast<uintptr_t>(row + first) & 15u) == 0;
-    if (bulk) {
-      if (threadIdx.x == 0) {
-        const uint32_t bytes = uint32_t(full1 - full0) * 16u;
-        char* dst = reinterpret_cast<char*>(row + first + full0 * kPer);
-        const char* src = reinterpret_cast<const char*>(buf) + full0 * 16;
-        for (uint32_t at = 0; at < bytes; at += kPiece)
-          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + at),
-                       "r"(smem_addr(src + at)), "r"(min(kPiece, bytes - at))
-                       : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      }
-      if (threadIdx.x < 2 * kPer) {
-        const int i = int(threadIdx.x) % kPer;
-        const bool head = int(threadIdx.x) < kPer;
-        const int id = first + (head ? 0 : full1 * kPer) + i;
-        if ((head ? full0 > 0 : full1 < vecs) && id >= lo && id < hi) row[id] = buf[id - first];
-      }
-      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    } else {
-      for (int id = lo + int(threadIdx.x); id < hi; id += kThreads) row[id] = buf[id - first];
-    }
-  }
-
-  // The same value everywhere (a row that was not read, or an error row).
-  __device__ __forceinline__ void fill(float x) const {
-    float v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = x;
-    const uint4 w = RowVec<T>::put(v);
-    for (int j = int(threadIdx.x); j < vecs; j += kThreads) vec()[j] = w;
-  }
-
-  static constexpr uint32_t kPiece = 16384;
-};
-
 // ------------------------------------------------------------------ sums
 
+// Floats in the order of signed integers (no NaN); its own inverse.
+__device__ __forceinline__ int float_order(int bits) { return bits ^ ((bits >> 31) & 0x7FFFFFFF); }
 __device__ __forceinline__ float warp_max_f(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-  return v;
+  return __int_as_float(float_order(__reduce_max_sync(~0u, float_order(__float_as_int(v)))));
 }
 __device__ __forceinline__ float warp_sum_f(float v) {
 #pragma unroll
@@ -241,56 +164,72 @@ __device__ __forceinline__ float warp_sum_f(float v) {
   return v;
 }
 
-// Two binary32 numbers at a time.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return reinterpret_cast<const float2&>(d);
+// Two binary32 numbers in one register pair, and operations on both.
+typedef uint64_t pair_t;
+__device__ __forceinline__ pair_t pair(float a, float b) {
+  pair_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return reinterpret_cast<const float2&>(d);
+__device__ __forceinline__ pair_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ void parts(pair_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+  pair_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return reinterpret_cast<const float2&>(d);
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+  pair_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+  pair_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum_of(pair_t v) {
+  float a, b;
+  parts(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ pair_t ex2_both(pair_t y) {
+  float a, b;
+  parts(y, a, b);
+  return pair(ex2_approx(a), ex2_approx(b));
+}
 
 // The running statistics of one thread's elements: a group of vectors is taken
-// in at a time, relative to the largest element so far.
+// in at a time, relative to an element m that none exceeds by more than 2^16 of
+// weight (a reference that follows every new maximum changed in some lane of the
+// warp at almost every group: 1.2 of 7.6 instructions per element).
 template <typename T, bool kWeighted>
 struct Running {
   using V = RowVec<T>;
   float m = -INFINITY;
-  float2 z = make_float2(0.0f, 0.0f), s = make_float2(0.0f, 0.0f);
+  pair_t z = 0, s = 0, minus_m = 0;
   uint32_t floor = 0;
 
-  // A maximum of the elements that come next.
+  // The largest of the elements that come next.
   __device__ __forceinline__ void raise(float top, float temperature, float c) {
-    if (top > m) {
+    if (__fmul_rn(__fsub_rn(top, m), c) > 16.0f) {
       if (m > -INFINITY) {
         const float d = __fsub_rn(m, top), w = ex2_approx(__fmul_rn(d, c));
-        if (kWeighted) s = w == 0.0f ? both(0.0f) : mul2(fma2(z, both(d), s), both(w));
+        if (kWeighted) s = w == 0.0f ? 0 : mul2(fma2(z, both(d), s), both(w));
         z = mul2(z, both(w));
       }
       m = top;
+      minus_m = both(-m);
       floor = floor_word<T>(m, temperature);
     }
   }
-  // A vector none of whose elements is above m; m is not -inf.
-  __device__ __forceinline__ void add(const uint4& x, float c) {
-    float v[V::kPer];
+  // A vector that m is fit for; m is not -inf.
+  __device__ __forceinline__ void add(const uint4& x, pair_t c) {
+    pair_t v[V::kPer / 2];
     V::get(x, floor, v);
 #pragma unroll
-    for (int i = 0; i < V::kPer; i += 2) {
-      const float2 d = add2(make_float2(v[i], v[i + 1]), both(-m)), y = mul2(d, both(c));
-      const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+    for (int i = 0; i < V::kPer / 2; ++i) {
+      const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c));
       z = add2(z, e);
       if (kWeighted) s = fma2(e, d, s);
     }
@@ -299,24 +238,17 @@ struct Running {
     if (v > -INFINITY) {
       raise(v, temperature, c);
       const float d = __fsub_rn(v, m), e = ex2_approx(__fmul_rn(d, c));
-      z.x += e;
-      if (kWeighted && e > 0.0f) s.x = __fmaf_rn(e, d, s.x);
+      z = add2(z, pair(e, 0.0f));
+      if (kWeighted && e > 0.0f) s = add2(s, pair(__fmul_rn(e, d), 0.0f));
     }
   }
   __device__ __forceinline__ Stats stats() const {
-    return Stats{m, z.x + z.y, kWeighted && !is_lowest<T>(m) ? s.x + s.y : 0.0f};
+    return Stats{m, sum_of(z), kWeighted && !is_lowest<T>(m) ? sum_of(s) : 0.0f};
   }
 };
 
-// The largest of this thread's elements (vectors tid, tid + kThreads, ...).
-template <typename T>
-__device__ __forceinline__ float thread_top(const Slice<T>& s) {
-  uint32_t m = RowVec<T>::kNegInf2;
-  for (int j = int(threadIdx.x); j < s.vecs; j += kThreads) m = RowVec<T>::top(s.vec()[j], m);
-  return RowVec<T>::finish(m);
-}
-
 // The statistics of the lanes' parts together, in every lane.
+template <bool kWeighted>
 __device__ __forceinline__ Stats warp_join(const Stats& part, float c) {
   Stats out;
   out.m = warp_max_f(part.m);
@@ -324,20 +256,11 @@ __device__ __forceinline__ Stats warp_join(const Stats& part, float c) {
   if (part.z != 0.0f) {
     const float d = __fsub_rn(part.m, out.m), w = ex2_approx(__fmul_rn(d, c));
     z = part.z * w;
-    s = w == 0.0f ? 0.0f : w * __fmaf_rn(part.z, d, part.s);
+    if (kWeighted) s = w == 0.0f ? 0.0f : w * __fmaf_rn(part.z, d, part.s);
   }
-  out.z = warp_sum_f(z), out.s = warp_sum_f(s);
+  out.z = warp_sum_f(z);
+  out.s = kWeighted ? warp_sum_f(s) : 0.0f;
   return out;
-}
-
-// The statistics of this warp's elements, given its threads' maxima.
-template <typename T, bool kWeighted>
-__device__ __forceinline__ Stats warp_stats(const Slice<T>& s, float mine, float temperature, float c) {
-  Running<T, kWeighted> run;
-  run.raise(mine, temperature, c);
-  if (run.m > -INFINITY)
-    for (int j = int(threadIdx.x); j < s.vecs; j += kThreads) run.add(s.vec()[j], c);
-  return warp_join(run.stats(), c);
 }
 
 // ------------------------------------------------------------------ a part of a row, read once from memory
@@ -366,12 +289,28 @@ struct Part {
   }
 };
 
-// A vector that is not wanted again soon, past the L1 cache.
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
+// A vector past the L1 cache; kConst: of memory that the kernel does not write.
+template <bool kConst>
+__device__ __forceinline__ uint4 load_vector(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  if (kConst)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+  return v;
+}
+// A vector that was read before and is not wanted again.
+__device__ __forceinline__ uint4 load_last(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 
@@ -382,22 +321,23 @@ constexpr int kUnit = 4;     // vectors of a thread that are loaded and taken in
 // of the thread's vectors where there are two units at most.  change(y, k) may
 // alter vector k (from the first whole one) first; seen(top) gets the largest
 // element of each unit, in order.
-template <typename T, bool kWeighted, typename Change, typename Seen>
+template <bool kConst, typename T, bool kWeighted, typename Change, typename Seen>
 __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, uint4 (&x)[2][kUnit],
                                        const float& temperature, const float& c, Change&& change, Seen&& seen) {
   using V = RowVec<T>;
   constexpr int kStep = kUnit * kThreads;
   const int vecs = s.full1 - s.full0, pairs = vecs / (2 * kStep);
+  const pair_t c2 = both(c);
   const uint4* p = s.vec() + s.full0 + threadIdx.x;
   auto load = [&](uint4 (&y)[kUnit], const uint4* from) {
 #pragma unroll
-    for (int u = 0; u < kUnit; ++u) y[u] = load_once(from + u * kThreads);
+    for (int u = 0; u < kUnit; ++u) y[u] = load_vector<kConst>(from + u * kThreads);
   };
   auto load_some = [&](uint4 (&y)[kUnit], int unit) {
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
       y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
-      if (int(threadIdx.x) + unit * kStep + u * kThreads < vecs) y[u] = load_once(p + unit * kStep + u * kThreads);
+      if (int(threadIdx.x) + unit * kStep + u * kThreads < vecs) y[u] = load_vector<kConst>(p + unit * kStep + u * kThreads);
     }
   };
   auto take = [&](uint4 (&y)[kUnit], int unit) {
@@ -411,7 +351,7 @@ __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& 
     run.raise(top, temperature, c);
     if (run.m > -INFINITY) {
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) run.add(y[u], c);
+      for (int u = 0; u < kUnit; ++u) run.add(y[u], c2);
     }
     seen(top);
   };
@@ -472,13 +412,6 @@ __device__ __forceinline__ void cluster_meet(int ranks) {
   else __syncthreads();
 }
 
-// Waits for the slice (every thread); true when some thread's wait ran out.
-__device__ __forceinline__ bool slice_is_late(uint64_t* bar, uint64_t limit) {
-  const bool late = !wait_full(bar, 0, limit);
-  if (late) wait_full(bar, 0, kWaitLimitNs);   // the copy lands in this CTA's memory: not before that is over
-  return __syncthreads_or(late);
-}
-
 __device__ __forceinline__ float row_temperature(const RowsArgs& a, int row) {
   return a.temperatures ? a.temperatures[row] : a.temperature;
 }
@@ -495,6 +428,114 @@ __device__ __forceinline__ bool first_of_id(const int* ids, const float* add, in
       sum += add[i];
     }
   return first;
+}
+
+// Vector x without the elements whose bits are set.
+__device__ __forceinline__ void erase(uint4& x, uint32_t bits, uint16_t) {
+  uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bits >> (2 * i) & 1u) *w[i] = (*w[i] & 0xFFFF0000u) | 0xFF80u;
+    if (bits >> (2 * i + 1) & 1u) *w[i] = (*w[i] & 0xFFFFu) | 0xFF800000u;
+  }
+}
+__device__ __forceinline__ void erase(uint4& x, uint32_t bits, float) {
+  uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (bits >> i & 1u) *w[i] = RowVec<float>::kNegInf2;
+}
+
+// The teacher's row: t of each place, r, sum t ln t.
+struct Teacher {
+  int ids[kMaxIds];
+  float t[kMaxIds];
+  float given, rest, t_log_t;   // sum t, ...
+  int flags;
+};
+
+// Fills `teach` but for its ids (one warp).  r = 1 - sum t is a small difference: it is taken
+// from fixed-point exponentials, which are exact to 2^-45 each.
+__device__ __forceinline__ void teacher_row(const int32_t* ids, const float* values, int count, int tail, int row,
+                                            Teacher& teach) {
+  const int lane = int(threadIdx.x) & 31;
+  constexpr int kEach = kMaxIds / 32;
+  float l[kEach];
+  bool live[kEach], bad = false;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = lane + 32 * i;
+    const int id = k < count ? ids[int64_t(row) * count + k] : -1;
+    live[i] = id >= 0;
+    l[i] = live[i] ? values[int64_t(row) * count + k] : -INFINITY;
+    bad |= !(l[i] < INFINITY);
+    top = fmaxf(top, l[i]);
+  }
+  float log_sum = 0.0f, given = 1.0f, rest = 0.0f;
+  if (tail) {
+    uint64_t mass = 0;
+    const RowScale unit = make_row_scale_unit(0.0f);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (live[i]) mass += mass_fixed(fminf(l[i], 1.0f), unit, kExp2Table);
+    mass = warp_sum<uint64_t>(mass);
+    bad |= mass > kFixedOne + (kFixedOne >> 6);
+    given = float(mass) * 0x1p-44f;
+    rest = mass < kFixedOne ? float(kFixedOne - mass) * 0x1p-44f : 0.0f;
+  } else {
+    top = warp_max_f(top);
+    bad |= !(top > -INFINITY);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) sum += expf(__fsub_rn(l[i], top));
+    log_sum = __fadd_rn(top, logf(warp_sum_f(sum)));
+  }
+  float t_log_t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const float log_t = __fsub_rn(l[i], log_sum), t = live[i] ? expf(log_t) : 0.0f;
+    if (t > 0.0f) t_log_t = __fmaf_rn(t, log_t, t_log_t);
+    teach.t[lane + 32 * i] = t;
+  }
+  t_log_t = warp_sum_f(t_log_t);
+  bad = __any_sync(~0u, bad);
+  if (lane == 0) teach.given = given, teach.rest = rest, teach.t_log_t = t_log_t, teach.flags = bad ? kRowBadParams : 0;
+}
+
+// Both statistics together: m, Z and the factors 2^((m_i - m) c).
+struct Whole {
+  float m, zsum, reach, ids_reach;
+  __device__ __forceinline__ Whole(const Stats& r, const Stats& k, float c) {
+    m = fmaxf(r.m, k.m);
+    reach = r.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(r.m, m), c)) : 0.0f;
+    ids_reach = k.z > 0.0f ? ex2_approx(__fmul_rn(__fsub_rn(k.m, m), c)) : 0.0f;
+    zsum = __fadd_rn(r.z > 0.0f ? __fmul_rn(r.z, reach) : 0.0f, k.z > 0.0f ? __fmul_rn(k.z, ids_reach) : 0.0f);
+  }
+};
+
+// The row's loss, in one warp, from the statistics outside the teacher's ids (r)
+// and of the whole row (m, zsum): the places' ids (-1: none), their t and the
+// student's logits there, sum t ln t, and the teacher's mass outside them.
+__device__ __forceinline__ float row_loss(const int* ids, const float* t, const float* student, int room, float t_log_t,
+                                          const Stats& r, float m, float zsum, float rest, float temperature) {
+  const int lane = int(threadIdx.x) & 31;
+  const float log_z = logf(zsum);
+  float loss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxIds / 32; ++i) {
+    const int n = lane + 32 * i;
+    if (n < room && ids[n] >= 0 && t[n] > 0.0f) {   // -t ln s, with t times a far logit before the division, which it might overflow
+      const float far = __fdiv_rn(__fmul_rn(t[n], __fsub_rn(student[n], m)), temperature);
+      loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(t[n], log_z), far));
+    }
+  }
+  loss = __fadd_rn(warp_sum_f(loss), t_log_t);
+  if (rest > 0.0f) {
+    const float far = __fdiv_rn(__fmul_rn(rest, __fsub_rn(r.m, m)), temperature);
+    loss = __fadd_rn(loss, __fsub_rn(__fmul_rn(rest, __fadd_rn(logf(rest), __fsub_rn(log_z, logf(r.z)))), far));
+  }
+  return loss;
 }
 
 // ------------------------------------------------------------------ host
@@ -533,33 +574,17 @@ inline smp_status shape_parts(RowsArgs& r, int elem, LaunchShape& ls) {
   return SMP_OK;
 }
 
-// The launch of a kernel whose CTAs keep their slices in shared memory.
-inline smp_status shape_slices(RowsArgs& r, int elem, LaunchShape& ls) {
-  const int dev = current_device();
-  if (dev < 0) return fail_cuda(cudaGetLastError());
-  const int64_t bytes = int64_t(r.vocab) * elem;
-  int c = 1;
-  while (c < 16 && bytes > int64_t(c) * 68 * 1024) c *= 2;
-  while (c < 8 && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 3 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
-  const int forced = forced_cluster();
-  ls.cluster = forced && bytes <= int64_t(forced) * 160 * 1024 ? forced : c;
-  const int per = 16 / elem;
-  r.slice = ((r.vocab + per - 1 + ls.cluster - 1) / ls.cluster + per - 1) / per * per;
-  ls.smem = size_t(r.slice) * elem;
-  return SMP_OK;
-}
-
 // Launches `kernel` on every row; `a` is its argument, whose member `rows` is a
 // RowsArgs.
 template <typename Args>
-smp_status launch_rows(const void* kernel, Args a, LaunchShape ls, cudaStream_t st) {
+smp_status launch_rows(const void* kernel, Args a, LaunchShape ls, cudaStream_t st, int threads = kThreads) {
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
   ls.pdl = true;
   a.rows.wait_limit = wait_limit_ns();
   cudaError_t err = prepare_kernel(kernel, dev, ls);
   if (err != cudaSuccess) return fail_cuda(err);
-  err = launch_cluster(kernel, dim3(unsigned(a.rows.rows) * unsigned(ls.cluster)), dim3(kThreads), ls, st, &a);
+  err = launch_cluster(kernel, dim3(unsigned(a.rows.rows) * unsigned(ls.cluster)), dim3(unsigned(threads)), ls, st, &a);
   return err == cudaSuccess ? SMP_OK : fail_cuda(err);
 }
 

@@ -13,9 +13,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <type_traits>
 
-#include "scores.cuh"
+#include "row_grad.cuh"
 
 namespace smp {
 
@@ -30,16 +29,6 @@ struct ScoreArgs {
   int32_t* top_ids;
   float* top_logprobs;
   int run_room;   // most runs of any CTA
-};
-
-struct ScoreGradArgs {
-  RowsArgs rows;
-  const int32_t* ids;
-  int count;
-  const float* up;           // gradients of the log probabilities
-  const float* up_entropy;
-  void* grad;
-  int64_t grad_stride;
 };
 
 // A thread's units of kUnit vectors come in up to kRuns runs whose maxima are
@@ -246,12 +235,12 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     Running<T, kEntropy> run;
     const int edge = s.edge();
     const float at_edge = edge >= 0 ? clean(load1(z + edge)) : -INFINITY;
-    float best = -INFINITY;
+    float best = -INFINITY, mine = at_edge;   // the largest of the run, of the thread
     int in_run = 0, r = 0;
     uint4 x[2][kUnit];
-    stream(s, run, x, temperature, c, [](uint4&, int) {}, [&](float top) {
+    stream<true>(s, run, x, temperature, c, [](uint4&, int) {}, [&](float top) {
       if (kTop) {
-        best = fmaxf(best, top);
+        best = fmaxf(best, top), mine = fmaxf(mine, top);
         if (++in_run == units) {
           run_top[r * kThreads + tid] = best;
           best = -INFINITY, in_run = 0, ++r;
@@ -262,18 +251,18 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     if (kTop) {
       for (; r < runs; ++r, best = -INFINITY) run_top[r * kThreads + tid] = best;
     }
-    const Stats part = warp_join(run.stats(), c);
+    const Stats part = warp_join<kEntropy>(run.stats(), c);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
-    if (kTop) slice_top(s, run.m, run_top, runs, units, edge, x, a.top, room, lists + rank * a.top, ranks);
+    if (kTop) slice_top(s, mine, run_top, runs, units, edge, x, a.top, room, lists + rank * a.top, ranks);
     __syncthreads();
     if (warp == 0) {
-      const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
+      const Stats cta = warp_join<kEntropy>(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
       post(meet, rank, ranks, cta.m, cta.z, cta.s, 0.0f);
     }
     cluster_meet(ranks);
     const float4 p = posted(meet, ranks);
-    all = warp_join(Stats{p.x, p.y, p.z}, c);
+    all = warp_join<kEntropy>(Stats{p.x, p.y, p.z}, c);
     if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
   } else {
     cluster_all_run(ranks);
@@ -336,105 +325,6 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) token_logprobs_grad_kernel(const __grid_constant__ ScoreGradArgs a) {
-  extern __shared__ __align__(16) unsigned char dynamic[];
-  __shared__ Meeting meet;
-  __shared__ uint64_t bar;
-  __shared__ int ids[kMaxIds];
-  __shared__ float up[kMaxIds];
-  constexpr int kPer = RowVec<T>::kPer;
-  const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
-  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  allow_dependent_launch();
-  if (tid == 0) {
-    mbar_init(&bar, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  cluster_arrive_early(ranks);
-
-  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-  T* out = static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride;
-  const float temperature = row_temperature(a.rows, row);
-  int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
-  const float h = a.up_entropy ? a.up_entropy[row] : 0.0f;
-  if (tid < kMaxIds) {
-    ids[tid] = id;
-    up[tid] = id >= 0 ? a.up[int64_t(row) * a.count + tid] : 0.0f;
-  }
-  const bool wanted = __syncthreads_or(id >= 0) || h != 0.0f;
-  const bool past = __syncthreads_or(id >= a.rows.vocab);
-  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
-  const float c = __fdiv_rn(kLog2e, temperature);
-  int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
-  if (past) flags |= kRowBadToken;
-  if (!wanted || flags) {
-    cluster_all_run(ranks);
-    if (wanted && rank == 0 && tid == 0 && a.rows.status) atomicOr(a.rows.status, flags);
-    s.fill(wanted ? __uint_as_float(0x7FC00000u) : 0.0f);
-    s.store(out);
-    return;
-  }
-  s.load(z, a.rows.vocab, &bar);
-  float sum_here = 0.0f;   // this id's gradients, over all its places
-  const bool first = tid < a.count && first_of_id(ids, up, a.count, tid, sum_here);
-  float g = 0.0f;          // and the row's
-  for (int i = lane; i < a.count; i += 32) g += up[i];
-  g = warp_sum_f(g);
-  const bool late = slice_is_late(&bar, a.rows.wait_limit);
-  const bool own = first && s.holds(id);
-  const float value = own ? s.at(id) : 0.0f;
-  const float mine = thread_top(s);
-  const Stats part = h != 0.0f ? warp_stats<T, true>(s, mine, temperature, c) : warp_stats<T, false>(s, mine, temperature, c);
-  if (lane == 0) meet.warp[warp] = part;
-  cluster_all_run(ranks);
-  __syncthreads();
-  if (warp == 0) {
-    const Stats cta = warp_join(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
-    post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
-  }
-  cluster_meet(ranks);
-  const float4 p = posted(meet, ranks);
-  const Stats all = warp_join(Stats{p.x, p.y, p.z}, c);
-  if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
-  if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
-  if (flags) {
-    if (rank == 0 && tid == 0 && a.rows.status) atomicOr(a.rows.status, flags);
-    s.fill(__uint_as_float(0x7FC00000u));
-    s.store(out);
-    return;
-  }
-  // ln p_j + H = d / T - S / (T Z):  dz_j = e_j (A + B d_j), the ids' own g besides
-  const float inv_t = __fdiv_rn(1.0f, temperature), inv_z = __fdiv_rn(1.0f, all.z);
-  const float mean_d = __fmul_rn(all.s, inv_z);   // sum p d
-  const float ht = __fmul_rn(h, inv_t);
-  const float ca = -__fmul_rn(__fmul_rn(__fmaf_rn(-ht, mean_d, g), inv_t), inv_z), cb = -__fmul_rn(__fmul_rn(ht, inv_t), inv_z);
-  const uint32_t floor = floor_word<T>(all.m, temperature);
-  auto sweep = [&](auto weighted) {
-    for (int j = tid; j < s.vecs; j += kThreads) {
-      float v[kPer];
-      RowVec<T>::get(s.vec()[j], floor, v);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float d = __fsub_rn(v[i], all.m), e = ex2_approx(__fmul_rn(d, c));
-        v[i] = weighted ? __fmaf_rn(cb, __fmul_rn(e, d), __fmul_rn(e, ca)) : __fmul_rn(e, ca);   // cb d may overflow, e d not
-      }
-      s.vec()[j] = RowVec<T>::put(v);
-    }
-  };
-  if (h != 0.0f && !is_lowest<T>(all.m)) sweep(std::true_type{});
-  else sweep(std::false_type{});
-  __syncthreads();
-  if (own) {
-    const float d = __fsub_rn(value, all.m), e = ex2_approx(__fmul_rn(d, c));
-    const float base = e == 0.0f ? 0.0f : __fmaf_rn(cb, __fmul_rn(e, d), __fmul_rn(e, ca));
-    store1(s.buf + (id - s.first), __fmaf_rn(sum_here, inv_t, base));
-  }
-  s.store(out);
-}
-
-template <typename T>
 static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
   const void* kernel =
       a.entropy ? (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true>)
@@ -451,14 +341,6 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
   }
   return launch_rows(kernel, a, ls, st);
 }
-template <typename T>
-static smp_status launch_scores_grad(const ScoreGradArgs& a, cudaStream_t st) {
-  ScoreGradArgs b = a;
-  LaunchShape ls;
-  const smp_status ok = shape_slices(b.rows, int(sizeof(T)), ls);
-  return ok == SMP_OK ? launch_rows(reinterpret_cast<const void*>(&token_logprobs_grad_kernel<T>), b, ls, st) : ok;
-}
-
 }  // namespace smp
 
 extern "C" smp_status smp_token_logprobs(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype,
@@ -510,10 +392,10 @@ extern "C" smp_status smp_token_logprobs_grad(const void* logits, int32_t rows, 
     if (rc != SMP_OK) return rc;
   }
   if (rows == 0) return SMP_OK;
-  ScoreGradArgs a{};
+  RowGradArgs a{};
   a.rows.logits = logits, a.rows.stride = stride, a.rows.rows = rows, a.rows.vocab = vocab;
   a.rows.temperature = temperature, a.rows.temperatures = temperatures, a.rows.status = status;
-  a.ids = ids, a.count = count, a.up = grad_logprobs, a.up_entropy = grad_entropy;
+  a.ids = ids, a.count = count, a.values = grad_logprobs, a.weights = grad_entropy;
   a.grad = out_grad, a.grad_stride = grad_stride;
-  return dtype == SMP_F32 ? launch_scores_grad<float>(a, st) : launch_scores_grad<uint16_t>(a, st);
+  return dtype == SMP_F32 ? launch_row_grad<float, false>(a, st) : launch_row_grad<uint16_t, false>(a, st);
 }
