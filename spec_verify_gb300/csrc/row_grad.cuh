@@ -184,26 +184,12 @@ __device__ __forceinline__ int keep_firsts(int* ids, float* add, int count) {
 }
 
 // Fills `f`, of a row whose ids are good (one warp).
-template <typename T, bool kDistill>
-__device__ __forceinline__ void learn_row(const RowGradArgs& a, int row, const T* z, float temperature, float weight,
-                                          RowFacts& f) {
+template <bool kDistill>
+__device__ __forceinline__ void learn_row(const RowGradArgs& a, const int (&id)[kMaxIds / 32], float (&v)[kMaxIds / 32],
+                                          const float (&logit)[kMaxIds / 32], float temperature, float weight, RowFacts& f) {
   const int lane = int(threadIdx.x) & 31;
   constexpr int kEach = kMaxIds / 32;
-  float v[kEach], logit[kEach];
-  int id[kEach];
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int k = lane + 32 * i;
-    id[i] = k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
-    v[i] = k < a.count ? a.values[int64_t(row) * a.count + k] : 0.0f;
-  }
-  // every CTA has all of the ids' logits: what they add to Z needs no exchange
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    logit[i] = id[i] >= 0 ? clean(load1(z + id[i])) : -INFINITY;
-    if (id[i] < 0) v[i] = kDistill ? -INFINITY : 0.0f;
-  }
   int flags = 0;
   float sum = 0.0f;
   if (kDistill) {
@@ -265,73 +251,121 @@ __device__ __forceinline__ void learn_row(const RowGradArgs& a, int row, const T
 
 // ------------------------------------------------------------------ the sweeps
 
-// The statistics of this warp's share of the slice.
-template <typename T, bool kWeighted>
-__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c) {
+// Calls take(vectors, first) for this thread's vectors of the slice, kUnit at a
+// time, -inf in the places of those that are not there.
+template <typename T, typename Take>
+__device__ __forceinline__ void each_unit(const Slice<T>& s, Take&& take) {
   using V = RowVec<T>;
-  Running<T, kWeighted> run;
-  const pair_t c2 = both(c);
-  const uint4* p = s.vec() + threadIdx.x;
-  auto take = [&](const uint4 (&y)[kUnit]) {
-    uint32_t w = V::kNegInf2;
-#pragma unroll
-    for (int u = 0; u < kUnit; ++u) w = V::top(y[u], w);
-    run.raise(V::finish(w), temperature, c);
-    if (run.m > -INFINITY) {
-#pragma unroll
-      for (int u = 0; u < kUnit; ++u) run.add(y[u], c2);
-    }
-  };
-  int j = 0;
+  const uint4* p = s.vec();
 #pragma unroll 1
-  for (; j + kUnit * kThreads <= s.vecs; j += kUnit * kThreads) {
+  for (int j = int(threadIdx.x); j < s.vecs; j += kUnit * kThreads) {
     uint4 y[kUnit];
+    if (j + (kUnit - 1) * kThreads < s.vecs) {
 #pragma unroll
-    for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
-    take(y);
-  }
-  if (j < s.vecs) {
-    uint4 y[kUnit];
+      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
+    } else {
 #pragma unroll
-    for (int u = 0; u < kUnit; ++u) {
-      y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
-      if (int(threadIdx.x) + j + u * kThreads < s.vecs) y[u] = p[j + u * kThreads];
+      for (int u = 0; u < kUnit; ++u) {
+        y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
+        if (j + u * kThreads < s.vecs) y[u] = p[j + u * kThreads];
+      }
     }
-    take(y);
+    take(y, j == int(threadIdx.x));
   }
-  return warp_join<kWeighted>(run.stats(), c);
 }
 
-// Replaces the slice's elements z by 2^((z - m) c) (A + B (z - m)).
-template <typename T, bool kWeighted>
-__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb) {
+// The statistics of this warp's share of the slice.  Where no element is NaN, +inf
+// or further above the thread's first ones than binary32 reaches (2^127 of
+// weight), nothing has to be looked at before it enters the sum: 2^(z c - m c) in
+// one fused multiply-add, m the largest of the first unit.  The sum says whether
+// that held (it is finite); otherwise the share is summed again with care, and
+// `plain` is false.
+template <typename T>
+__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c, bool weighted, bool& plain) {
   using V = RowVec<T>;
-  const uint32_t floor = floor_word<T>(m, temperature);
+  if (!weighted) {
+    float m = 0.0f;
+    pair_t z = 0, shift = 0;
+    const pair_t c2 = both(c);
+    each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool first) {
+      if (first) {
+        uint32_t w = V::kNegInf2;
+#pragma unroll
+        for (int u = 0; u < kUnit; ++u) w = V::top(y[u], w);
+        m = V::finish(w);
+        shift = both(-__fmul_rn(m, c));
+      }
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) {
+        pair_t v[V::kPer / 2];
+        V::raw(y[u], v);
+#pragma unroll
+        for (int i = 0; i < V::kPer / 2; ++i) z = add2(z, ex2_both(fma2(v[i], c2, shift)));
+      }
+    });
+    const float sum = sum_of(z), at_m = __fmul_rn(m, c);
+    const bool none = int(threadIdx.x) >= s.vecs;
+    plain = __all_sync(~0u, none || (sum < INFINITY && fabsf(at_m) < 0x1p20f));
+    if (plain)   // the sum is relative to the rounded m c
+      return warp_join<false>(none ? Stats{-INFINITY, 0.0f, 0.0f} : Stats{m, sum * ex2_approx(-__fmaf_rn(m, c, -at_m)), 0.0f}, c);
+    Running<T, false> run;
+    each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
+    return warp_join<false>(run.stats(), c);
+  }
+  plain = false;
+  Running<T, true> run;
+  each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
+  return warp_join<true>(run.stats(), c);
+}
+
+// Replaces the slice's elements z by 2^((z - m) c) (A + B (z - m)); plain: as
+// slice_stats found them.
+template <typename T>
+__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb,
+                                           bool weighted, bool plain) {
+  using V = RowVec<T>;
   uint4* p = s.vec();
-  const pair_t minus_m = both(-m), c2 = both(c), ca2 = both(ca), cb2 = both(cb);
-  auto turn = [&](const uint4& x) {
+  const pair_t c2 = both(c);
+  auto turn_all = [&](auto&& turn) {
+    int j = int(threadIdx.x);
+#pragma unroll 1
+    for (; j + (kUnit - 1) * kThreads < s.vecs; j += kUnit * kThreads) {
+      uint4 y[kUnit];
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < kUnit; ++u) p[j + u * kThreads] = turn(y[u]);
+    }
+#pragma unroll 1
+    for (; j < s.vecs; j += kThreads) p[j] = turn(p[j]);
+  };
+  if (plain && !weighted && fabsf(__fmul_rn(m, c)) < 128.0f) {
+    // 2^(z c - m c + log2 |A|), with A's sign; the constant is below 128 + 150, its rounding at most 2^-16
+    const pair_t shift = both(__fmaf_rn(-m, c, log2f(fabsf(ca))));
+    const uint32_t sign = ca < 0.0f ? V::kSign : 0u;
+    turn_all([&](const uint4& x) {
+      pair_t v[V::kPer / 2];
+      float r[V::kPer];
+      V::raw(x, v);
+#pragma unroll
+      for (int i = 0; i < V::kPer / 2; ++i) parts(ex2_both(fma2(v[i], c2, shift)), r[2 * i], r[2 * i + 1]);
+      return V::put(r, sign);
+    });
+    return;
+  }
+  const uint32_t floor = floor_word<T>(m, temperature);
+  const pair_t minus_m = both(-m), ca2 = both(ca), cb2 = both(weighted ? cb : 0.0f);
+  turn_all([&](const uint4& x) {
     pair_t v[V::kPer / 2];
     float r[V::kPer];
     V::get(x, floor, v);
 #pragma unroll
     for (int i = 0; i < V::kPer / 2; ++i) {
-      const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c2));
-      const pair_t plain = mul2(e, ca2);
-      parts(kWeighted ? fma2(mul2(e, d), cb2, plain) : plain, r[2 * i], r[2 * i + 1]);   // B d may overflow, e d not
+      const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c2)), even = mul2(e, ca2);
+      parts(weighted ? fma2(mul2(e, d), cb2, even) : even, r[2 * i], r[2 * i + 1]);   // B d may overflow, e d not
     }
     return V::put(r);
-  };
-  int j = int(threadIdx.x);
-#pragma unroll 1
-  for (; j + 3 * kThreads < s.vecs; j += 4 * kThreads) {
-    uint4 y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) y[u] = p[j + u * kThreads];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) p[j + u * kThreads] = turn(y[u]);
-  }
-#pragma unroll 1
-  for (; j < s.vecs; j += kThreads) p[j] = turn(p[j]);
+  });
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -357,6 +391,23 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   const float temperature = row_temperature(a.rows, row);
   const float weight = a.weights ? a.weights[row] : kDistill ? 1.0f : 0.0f;
   int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  int ids[kMaxIds / 32];
+  float values[kMaxIds / 32];
+  T logits[kMaxIds / 32];
+  if (warp == kLearner) {
+#pragma unroll
+    for (int i = 0; i < kMaxIds / 32; ++i) {
+      const int k = lane + 32 * i;
+      ids[i] = k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
+      values[i] = k < a.count ? a.values[int64_t(row) * a.count + k] : 0.0f;
+    }
+    // every CTA has all of the ids' logits: what they add to Z needs no exchange
+#pragma unroll
+    for (int i = 0; i < kMaxIds / 32; ++i) {
+      logits[i] = RowVec<T>::minus_inf();
+      if (ids[i] >= 0 && ids[i] < a.rows.vocab) logits[i] = z[ids[i]];   // not looked at before the barrier
+    }
+  }
   const bool some = __syncthreads_or(id >= 0) || (!kDistill && weight != 0.0f), past = __syncthreads_or(id >= a.rows.vocab);
   int flags = !some ? 0 : (past ? kRowBadToken : 0) | (temperature_fits(temperature) ? 0 : kRowBadParams);
   const bool read = some && !flags;
@@ -379,9 +430,15 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     s.leave(out);
     return;
   }
-  bool late = false;
+  bool late = false, plain = false;
   if (warp == kLearner) {
-    learn_row<T, kDistill>(a, row, z, temperature, weight, f);
+    float logit[kMaxIds / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxIds / 32; ++i) {
+      logit[i] = clean(load1(&logits[i]));
+      if (ids[i] < 0) values[i] = kDistill ? -INFINITY : 0.0f;
+    }
+    learn_row<kDistill>(a, ids, values, logit, temperature, weight, f);
     cluster_all_run(ranks);
   } else {
     late = !wait_full(&bar, 0, a.rows.wait_limit);
@@ -389,7 +446,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     if (kDistill && s.holds(id)) s.buf[id - s.first] = RowVec<T>::minus_inf();
     late = cta_sync_count(late) > 0;
     const bool weighted = !kDistill && weight != 0.0f;
-    const Stats part = weighted ? slice_stats<T, true>(s, temperature, c) : slice_stats<T, false>(s, temperature, c);
+    const Stats part = slice_stats<T>(s, temperature, c, weighted, plain);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
     cta_sync();
@@ -440,8 +497,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     return;
   }
   if (flags) s.fill(nan);
-  else if (!kDistill && weight != 0.0f && !is_lowest<T>(m)) slice_grad<T, true>(s, m, temperature, c, ca, cb);
-  else slice_grad<T, false>(s, m, temperature, c, ca, 0.0f);
+  else slice_grad<T>(s, m, temperature, c, ca, cb, !kDistill && weight != 0.0f && !is_lowest<T>(m), plain);
   cta_sync();
   if (here && !flags) store1(s.buf + (id - s.first), share);
   s.leave(out);

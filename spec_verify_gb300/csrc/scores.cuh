@@ -84,6 +84,19 @@ struct RowVec<uint16_t> {
     for (int i = 0; i < 4; ++i)
       asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(bf16_low(w[i])), "f"(bf16_high(w[i])));
   }
+  // The eight values as they are.
+  static __device__ __forceinline__ void raw(const uint4& x, uint64_t (&v)[4]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(bf16_low(w[i])), "f"(bf16_high(w[i])));
+  }
+  // The values rounded, their signs turned by `sign` (of both halves of a word).
+  static __device__ __forceinline__ uint4 put(const float (&v)[8], uint32_t sign) {
+    return make_uint4(pack_bf16(v[0], v[1]) ^ sign, pack_bf16(v[2], v[3]) ^ sign, pack_bf16(v[4], v[5]) ^ sign,
+                      pack_bf16(v[6], v[7]) ^ sign);
+  }
+  static constexpr uint32_t kSign = 0x80008000u;
   static __device__ __forceinline__ uint4 put(const float (&v)[8]) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   }
@@ -115,6 +128,15 @@ struct RowVec<float> {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v[0]) : "r"(max2(x.x, floor)), "r"(max2(x.y, floor)));
     asm("mov.b64 %0, {%1, %2};" : "=l"(v[1]) : "r"(max2(x.z, floor)), "r"(max2(x.w, floor)));
   }
+  static __device__ __forceinline__ void raw(const uint4& x, uint64_t (&v)[2]) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v[0]) : "r"(x.x), "r"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v[1]) : "r"(x.z), "r"(x.w));
+  }
+  static __device__ __forceinline__ uint4 put(const float (&v)[4], uint32_t sign) {
+    return make_uint4(__float_as_uint(v[0]) ^ sign, __float_as_uint(v[1]) ^ sign, __float_as_uint(v[2]) ^ sign,
+                      __float_as_uint(v[3]) ^ sign);
+  }
+  static constexpr uint32_t kSign = 0x80000000u;
   static __device__ __forceinline__ uint4 put(const float (&v)[4]) {
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
@@ -232,6 +254,18 @@ struct Running {
       const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c));
       z = add2(z, e);
       if (kWeighted) s = fma2(e, d, s);
+    }
+  }
+  // Some vectors.
+  template <int kN>
+  __device__ __forceinline__ void take(const uint4 (&y)[kN], float temperature, float c) {
+    uint32_t w = V::kNegInf2;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) w = V::top(y[u], w);
+    raise(V::finish(w), temperature, c);
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kN; ++u) add(y[u], both(c));
     }
   }
   __device__ __forceinline__ void add_one(float v, float temperature, float c) {   // clean
