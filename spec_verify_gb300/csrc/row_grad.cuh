@@ -33,6 +33,7 @@ struct RowGradArgs {
   float* loss;               // distillation alone
   void* grad;
   int64_t grad_stride;
+  int ahead;                 // rows between a CTA's and that of the CTA that takes its place on the SM
 };
 
 // ------------------------------------------------------------------ the slice of a row
@@ -276,53 +277,54 @@ __device__ __forceinline__ void each_unit(const Slice<T>& s, Take&& take) {
 
 // The statistics of this warp's share of the slice.  Where no element is NaN, +inf
 // or further above the thread's first ones than binary32 reaches (2^127 of
-// weight), nothing has to be looked at before it enters the sum: 2^(z c - m c) in
-// one fused multiply-add, m the largest of the first unit.  The sum says whether
-// that held (it is finite); otherwise the share is summed again with care, and
-// `plain` is false.
-template <typename T>
-__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c, bool weighted, bool& plain) {
+// weight), and with weights none is -inf, nothing has to be looked at before it
+// enters the sums: y = z c - m c in one fused multiply-add, m the largest of the
+// first unit.  The sums say whether that held (they are finite); otherwise the
+// share is summed again with care, and `plain` is false.
+template <typename T, bool kWeighted>
+__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c, bool& plain) {
   using V = RowVec<T>;
-  if (!weighted) {
-    float m = 0.0f;
-    pair_t z = 0, shift = 0;
-    const pair_t c2 = both(c);
-    each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool first) {
-      if (first) {
-        uint32_t w = V::kNegInf2;
+  float m = 0.0f;
+  pair_t z = 0, zy = 0, shift = 0;
+  const pair_t c2 = both(c);
+  each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool first) {
+    if (first) {
+      uint32_t w = V::kNegInf2;
 #pragma unroll
-        for (int u = 0; u < kUnit; ++u) w = V::top(y[u], w);
-        m = V::finish(w);
-        shift = both(-__fmul_rn(m, c));
+      for (int u = 0; u < kUnit; ++u) w = V::top(y[u], w);
+      m = V::finish(w);
+      shift = both(-__fmul_rn(m, c));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      pair_t v[V::kPer / 2];
+      V::raw(y[u], v);
+#pragma unroll
+      for (int i = 0; i < V::kPer / 2; ++i) {
+        const pair_t x = fma2(v[i], c2, shift), e = ex2_both(x);
+        z = add2(z, e);
+        if (kWeighted) zy = fma2(e, x, zy);
       }
-#pragma unroll
-      for (int u = 0; u < kUnit; ++u) {
-        pair_t v[V::kPer / 2];
-        V::raw(y[u], v);
-#pragma unroll
-        for (int i = 0; i < V::kPer / 2; ++i) z = add2(z, ex2_both(fma2(v[i], c2, shift)));
-      }
-    });
-    const float sum = sum_of(z), at_m = __fmul_rn(m, c);
-    const bool none = int(threadIdx.x) >= s.vecs;
-    plain = __all_sync(~0u, none || (sum < INFINITY && fabsf(at_m) < 0x1p20f));
-    if (plain)   // the sum is relative to the rounded m c
-      return warp_join<false>(none ? Stats{-INFINITY, 0.0f, 0.0f} : Stats{m, sum * ex2_approx(-__fmaf_rn(m, c, -at_m)), 0.0f}, c);
-    Running<T, false> run;
-    each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
-    return warp_join<false>(run.stats(), c);
+    }
+  });
+  const float sum = sum_of(z), sum_y = kWeighted ? sum_of(zy) : 0.0f, at_m = __fmul_rn(m, c);
+  const bool none = int(threadIdx.x) >= s.vecs;
+  plain = __all_sync(~0u, none || (sum < INFINITY && fabsf(sum_y) < INFINITY && fabsf(at_m) < 0x1p20f));
+  if (plain) {   // the sums are relative to the rounded m c: y = (z - m) c + off
+    const float off = __fmaf_rn(m, c, -at_m), back = ex2_approx(-off);
+    Stats part{-INFINITY, 0.0f, 0.0f};
+    if (!none) part = Stats{m, sum * back, kWeighted ? __fdiv_rn(__fmaf_rn(-off, sum, sum_y), c) * back : 0.0f};
+    return warp_join<kWeighted>(part, c);
   }
-  plain = false;
-  Running<T, true> run;
+  Running<T, kWeighted> run;
   each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
-  return warp_join<true>(run.stats(), c);
+  return warp_join<kWeighted>(run.stats(), c);
 }
 
 // Replaces the slice's elements z by 2^((z - m) c) (A + B (z - m)); plain: as
 // slice_stats found them.
-template <typename T>
-__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb,
-                                           bool weighted, bool plain) {
+template <typename T, bool kWeighted>
+__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb, bool plain) {
   using V = RowVec<T>;
   uint4* p = s.vec();
   const pair_t c2 = both(c);
@@ -339,22 +341,36 @@ __device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float tem
 #pragma unroll 1
     for (; j < s.vecs; j += kThreads) p[j] = turn(p[j]);
   };
-  if (plain && !weighted && fabsf(__fmul_rn(m, c)) < 128.0f) {
-    // 2^(z c - m c + log2 |A|), with A's sign; the constant is below 128 + 150, its rounding at most 2^-16
-    const pair_t shift = both(__fmaf_rn(-m, c, log2f(fabsf(ca))));
-    const uint32_t sign = ca < 0.0f ? V::kSign : 0u;
-    turn_all([&](const uint4& x) {
-      pair_t v[V::kPer / 2];
-      float r[V::kPer];
-      V::raw(x, v);
+  if (plain && fabsf(__fmul_rn(m, c)) < 128.0f) {
+    if (kWeighted) {   // 2^y (A + (B / c) y), y = z c - m c
+      const pair_t shift = both(-__fmul_rn(m, c)), ca2 = both(ca), cb2 = both(__fdiv_rn(cb, c));
+      turn_all([&](const uint4& x) {
+        pair_t v[V::kPer / 2];
+        float r[V::kPer];
+        V::raw(x, v);
 #pragma unroll
-      for (int i = 0; i < V::kPer / 2; ++i) parts(ex2_both(fma2(v[i], c2, shift)), r[2 * i], r[2 * i + 1]);
-      return V::put(r, sign);
-    });
+        for (int i = 0; i < V::kPer / 2; ++i) {
+          const pair_t y = fma2(v[i], c2, shift);
+          parts(mul2(ex2_both(y), fma2(y, cb2, ca2)), r[2 * i], r[2 * i + 1]);
+        }
+        return V::put(r);
+      });
+    } else {   // 2^(z c - m c + log2 |A|), with A's sign; the constant is below 128 + 150, its rounding at most 2^-16
+      const pair_t shift = both(__fmaf_rn(-m, c, log2f(fabsf(ca))));
+      const uint32_t sign = ca < 0.0f ? V::kSign : 0u;
+      turn_all([&](const uint4& x) {
+        pair_t v[V::kPer / 2];
+        float r[V::kPer];
+        V::raw(x, v);
+#pragma unroll
+        for (int i = 0; i < V::kPer / 2; ++i) parts(ex2_both(fma2(v[i], c2, shift)), r[2 * i], r[2 * i + 1]);
+        return V::put(r, sign);
+      });
+    }
     return;
   }
   const uint32_t floor = floor_word<T>(m, temperature);
-  const pair_t minus_m = both(-m), ca2 = both(ca), cb2 = both(weighted ? cb : 0.0f);
+  const pair_t minus_m = both(-m), ca2 = both(ca), cb2 = both(cb);
   turn_all([&](const uint4& x) {
     pair_t v[V::kPer / 2];
     float r[V::kPer];
@@ -362,13 +378,32 @@ __device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float tem
 #pragma unroll
     for (int i = 0; i < V::kPer / 2; ++i) {
       const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c2)), even = mul2(e, ca2);
-      parts(weighted ? fma2(mul2(e, d), cb2, even) : even, r[2 * i], r[2 * i + 1]);   // B d may overflow, e d not
+      parts(kWeighted ? fma2(mul2(e, d), cb2, even) : even, r[2 * i], r[2 * i + 1]);   // B d may overflow, e d not
     }
     return V::put(r);
   });
 }
 
 // ------------------------------------------------------------------ the kernel
+
+// Asks L2 for what the CTA will want that comes when this one has gone: its slice,
+// if the row is read, and the values of its ids (one warp).  HBM is then busy while
+// the CTAs of an SM happen to compute, and a slice arrives sooner.
+template <typename T, bool kDistill>
+__device__ __forceinline__ void look_ahead(const RowGradArgs& a, int row, int rank) {
+  const int lane = int(threadIdx.x) & 31;
+  if (row >= a.rows.rows - a.ahead) return;
+  row += a.ahead;
+  bool some = !kDistill && a.weights && a.weights[row] != 0.0f;
+  for (int k = lane; k < a.count; k += 32) some |= a.ids[int64_t(row) * a.count + k] >= 0;
+  if (!__any_sync(~0u, some)) return;
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  const Slice<T> s(nullptr, z, a.rows.vocab, a.rows.slice, rank);
+  const uintptr_t from = reinterpret_cast<uintptr_t>(z + s.first + s.full0 * Slice<T>::kPer);
+  const uint32_t bytes = uint32_t(s.full1 - s.full0) * 16u, at = uint32_t(lane) * Slice<T>::kPiece;
+  if (at < bytes) prefetch_l2(from + at, min(Slice<T>::kPiece, bytes - at));
+  for (int k = lane; k < a.count; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.values + int64_t(row) * a.count + k));
+}
 
 template <typename T, bool kDistill>
 __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_constant__ RowGradArgs a) {
@@ -424,6 +459,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
         if (kDistill) a.loss[row] = flags ? nan : 0.0f;
         if (flags && a.rows.status) atomicOr(a.rows.status, flags);
       }
+      look_ahead<T, kDistill>(a, row, rank);
       return;
     }
     s.fill(flags ? nan : 0.0f);
@@ -446,7 +482,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     if (kDistill && s.holds(id)) s.buf[id - s.first] = RowVec<T>::minus_inf();
     late = cta_sync_count(late) > 0;
     const bool weighted = !kDistill && weight != 0.0f;
-    const Stats part = slice_stats<T>(s, temperature, c, weighted, plain);
+    const Stats part = weighted ? slice_stats<T, !kDistill>(s, temperature, c, plain) : slice_stats<T, false>(s, temperature, c, plain);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
     cta_sync();
@@ -494,10 +530,12 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   }
   if (warp == kLearner) {
     if (flags && rank == 0 && lane == 0 && a.rows.status) atomicOr(a.rows.status, flags);
+    look_ahead<T, kDistill>(a, row, rank);
     return;
   }
   if (flags) s.fill(nan);
-  else slice_grad<T>(s, m, temperature, c, ca, cb, !kDistill && weight != 0.0f && !is_lowest<T>(m), plain);
+  else if (!kDistill && weight != 0.0f && !is_lowest<T>(m)) slice_grad<T, !kDistill>(s, m, temperature, c, ca, cb, plain);
+  else slice_grad<T, false>(s, m, temperature, c, ca, 0.0f, plain);
   cta_sync();
   if (here && !flags) store1(s.buf + (id - s.first), share);
   s.leave(out);
@@ -518,6 +556,8 @@ smp_status launch_row_grad(RowGradArgs a, cudaStream_t st) {
   ls.cluster = c;
   a.rows.slice = slice(c);
   ls.smem = size_t(a.rows.slice) * elem;
+  const int on_sm = std::max<int>(1, std::min<int>(3, int(227 * 1024 / (ls.smem + 3 * 1024))));
+  a.ahead = std::max(1, device_sms(dev) * on_sm / c);
   return launch_rows(reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill>), a, ls, st, kRowThreads);
 }
 
