@@ -132,77 +132,50 @@ struct RowFacts {
   float logit[kMaxIds];       // the student's
 };
 
-// Leaves the ids' first places alone, with the sum of `add` over equal ids, and
-// returns how many they are.
-__device__ __forceinline__ int keep_firsts(int* ids, float* add, int count) {
-  const int lane = int(threadIdx.x) & 31;
-  constexpr int kEach = kMaxIds / 32;
-  int id[kEach], place[kEach];   // the id's first place
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    id[i] = 32 * i < count ? ids[lane + 32 * i] : -1;
-    place[i] = lane + 32 * i;
-  }
-  bool again = false;
-#pragma unroll 1
-  for (int n = (count - 1) & ~3; n >= 0; n -= 4) {   // the places behind `count` hold -1
-    const int4 v = *reinterpret_cast<const int4*>(ids + n);
+// A row's small inputs in one warp: places lane, lane + 32, ...
+template <typename T, int kEach>
+struct Inputs {
+  int id[kEach];
+  float value[kEach];
+  T logit[kEach];
+  __device__ __forceinline__ void ask(const RowGradArgs& a, int row, const T* z) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      if (32 * i >= count) break;
-      place[i] = v.w == id[i] ? n + 3 : place[i];
-      place[i] = v.z == id[i] ? n + 2 : place[i];
-      place[i] = v.y == id[i] ? n + 1 : place[i];
-      place[i] = v.x == id[i] ? n : place[i];
+      const int k = (int(threadIdx.x) & 31) + 32 * i;
+      id[i] = k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
+      value[i] = k < a.count ? a.values[int64_t(row) * a.count + k] : 0.0f;
+    }
+    // every CTA has all of the ids' logits: what they add to Z needs no exchange
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      logit[i] = RowVec<T>::minus_inf();
+      if (id[i] >= 0 && id[i] < a.rows.vocab) logit[i] = z[id[i]];
     }
   }
-  int firsts = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const bool repeats = id[i] >= 0 && place[i] < lane + 32 * i;
-    again |= repeats;
-    firsts += __popc(__ballot_sync(~0u, id[i] >= 0 && !repeats));
-  }
-  if (!__any_sync(~0u, again)) return firsts;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    if (32 * i >= count) break;
-    const int k = lane + 32 * i;
-    float sum = 0.0f;
-    if (id[i] >= 0 && place[i] == k) {
-      for (int n = 0; n < count; ++n)
-        if (ids[n] == id[i]) sum += add[n];
-    }
-    if (place[i] < k) id[i] = -1;
-    __syncwarp();
-    if (id[i] >= 0) add[k] = sum;   // read by no other place any more: theirs are other ids
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (32 * i < count) ids[lane + 32 * i] = id[i];
-  return firsts;
-}
+};
 
 // Fills `f`, of a row whose ids are good (one warp).
-template <bool kDistill>
-__device__ __forceinline__ void learn_row(const RowGradArgs& a, const int (&id)[kMaxIds / 32], float (&v)[kMaxIds / 32],
-                                          const float (&logit)[kMaxIds / 32], float temperature, float weight, RowFacts& f) {
+template <bool kDistill, typename T, int kEach>
+__device__ __forceinline__ void learn_row(const Inputs<T, kEach>& in, int count, bool tail, float temperature, float weight,
+                                          RowFacts& f) {
   const int lane = int(threadIdx.x) & 31;
-  constexpr int kEach = kMaxIds / 32;
-  bool bad = false;
-  int flags = 0;
-  float sum = 0.0f;
+  float v[kEach], logit[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    v[i] = in.id[i] >= 0 ? in.value[i] : kDistill ? -INFINITY : 0.0f;
+    logit[i] = clean(load1(&in.logit[i]));
+    f.ids[lane + 32 * i] = in.id[i], f.logit[lane + 32 * i] = logit[i];
+  }
   if (kDistill) {
-    float top = -INFINITY, given = 1.0f, rest = 0.0f, log_sum = 0.0f;
+    float top = -INFINITY, given = 1.0f, rest = 0.0f, log_sum = 0.0f, t_log_t = 0.0f;
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) bad |= !(v[i] < INFINITY), top = fmaxf(top, v[i]);
-    if (a.tail) {   // r = 1 - sum t is a small difference: from fixed-point exponentials, exact to 2^-45 each
-      uint64_t mass = 0;
+    if (tail) {   // r = 1 - sum t is a small difference: from fixed-point exponentials, exact to 2^-45 each
       const RowScale unit = make_row_scale_unit(0.0f);
+      uint64_t mass = 0;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (32 * i < a.count) mass += id[i] >= 0 ? mass_fixed(fminf(v[i], 1.0f), unit, kExp2Table) : 0;
+      for (int i = 0; i < kEach; ++i) mass += mass_fixed(fminf(v[i], 1.0f), unit, kExp2Table);   // 0 for -inf
       mass = warp_sum<uint64_t>(mass);
       bad |= mass > kFixedOne + (kFixedOne >> 6);
       given = float(mass) * 0x1p-44f;
@@ -210,44 +183,73 @@ __device__ __forceinline__ void learn_row(const RowGradArgs& a, const int (&id)[
     } else {
       top = warp_max_f(top);
       bad |= !(top > -INFINITY);
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) sum += expf(__fsub_rn(v[i], top));
       log_sum = __fadd_rn(top, logf(warp_sum_f(sum)));
     }
-    float t_log_t = 0.0f;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const float log_t = __fsub_rn(v[i], log_sum), t = id[i] >= 0 ? expf(log_t) : 0.0f;
-      if (t > 0.0f) t_log_t = __fmaf_rn(t, log_t, t_log_t);
-      v[i] = t;
+      const float log_t = __fsub_rn(v[i], log_sum);
+      v[i] = in.id[i] >= 0 ? expf(log_t) : 0.0f;
+      if (v[i] > 0.0f) t_log_t = __fmaf_rn(v[i], log_t, t_log_t);
     }
     t_log_t = warp_sum_f(t_log_t);
-    if (__any_sync(~0u, bad)) flags |= kRowBadParams;
-    if (lane == 0) f.scale = __fdiv_rn(weight, temperature), f.given = given, f.rest = rest, f.t_log_t = t_log_t;
+    bad = __any_sync(~0u, bad);
+    if (lane == 0) {
+      f.flags = bad ? kRowBadParams : 0;
+      f.scale = __fdiv_rn(weight, temperature), f.given = given, f.rest = rest, f.t_log_t = t_log_t;
+    }
   } else {
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) sum += v[i];
     sum = warp_sum_f(sum);
-    if (lane == 0) f.sum = sum;
+    if (lane == 0) f.sum = sum, f.flags = 0;
   }
 #pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    f.ids[lane + 32 * i] = id[i], f.add[lane + 32 * i] = v[i], f.logit[lane + 32 * i] = logit[i];
+  for (int i = 0; i < kEach; ++i) f.add[lane + 32 * i] = v[i];
   __syncwarp();
-  keep_firsts(f.ids, f.add, a.count);
-  if (kDistill) {
-    float top = -INFINITY;
+  // Only the first place of an id stays, with the sum over all of them.
+  bool first[kEach], again = false;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) top = fmaxf(top, logit[i]);
-    Stats k{warp_max_f(top), 0.0f, 0.0f};
+  for (int i = 0; i < kEach; ++i) {
+    const unsigned same = __match_any_sync(~0u, in.id[i]);   // all lanes together, whatever their ids
+    first[i] = in.id[i] >= 0 && (same & ((1u << lane) - 1u)) == 0;
+#pragma unroll
+    for (int n = 0; n < 32 * i; n += 4) {
+      const int4 w = *reinterpret_cast<const int4*>(f.ids + n);
+      first[i] &= w.x != in.id[i] && w.y != in.id[i] && w.z != in.id[i] && w.w != in.id[i];
+    }
+    again |= in.id[i] >= 0 && !first[i];
+  }
+  Stats k{-INFINITY, 0.0f, 0.0f};
+  if (kDistill) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) k.m = fmaxf(k.m, logit[i]);
+    k.m = warp_max_f(k.m);
+    const float c = __fdiv_rn(kLog2e, temperature);
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if (f.ids[lane + 32 * i] >= 0 && logit[i] > -INFINITY)
-        k.z += ex2_approx(__fmul_rn(__fsub_rn(logit[i], k.m), __fdiv_rn(kLog2e, temperature)));
+      if (first[i] && logit[i] > -INFINITY) k.z += ex2_approx(__fmul_rn(__fsub_rn(logit[i], k.m), c));
     k.z = warp_sum_f(k.z);
     if (lane == 0) f.on_ids = k;
   }
-  if (lane == 0) f.flags = flags;
+  if (__any_sync(~0u, again)) {
+    float sum[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      sum[i] = 0.0f;
+      if (first[i])
+        for (int n = 0; n < count; ++n) sum[i] += f.ids[n] == in.id[i] ? f.add[n] : 0.0f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      f.add[lane + 32 * i] = sum[i];
+      if (!first[i]) f.ids[lane + 32 * i] = -1;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ the sweeps
@@ -386,26 +388,40 @@ __device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float tem
 
 // ------------------------------------------------------------------ the kernel
 
-// Asks L2 for what the CTA will want that comes when this one has gone: its slice,
-// if the row is read, and the values of its ids (one warp).  HBM is then busy while
-// the CTAs of an SM happen to compute, and a slice arrives sooner.
-template <typename T, bool kDistill>
-__device__ __forceinline__ void look_ahead(const RowGradArgs& a, int row, int rank) {
-  const int lane = int(threadIdx.x) & 31;
-  if (row >= a.rows.rows - a.ahead) return;
-  row += a.ahead;
-  bool some = !kDistill && a.weights && a.weights[row] != 0.0f;
-  for (int k = lane; k < a.count; k += 32) some |= a.ids[int64_t(row) * a.count + k] >= 0;
-  if (!__any_sync(~0u, some)) return;
-  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-  const Slice<T> s(nullptr, z, a.rows.vocab, a.rows.slice, rank);
-  const uintptr_t from = reinterpret_cast<uintptr_t>(z + s.first + s.full0 * Slice<T>::kPer);
-  const uint32_t bytes = uint32_t(s.full1 - s.full0) * 16u, at = uint32_t(lane) * Slice<T>::kPiece;
-  if (at < bytes) prefetch_l2(from + at, min(Slice<T>::kPiece, bytes - at));
-  for (int k = lane; k < a.count; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.values + int64_t(row) * a.count + k));
-}
+// What the CTA will want that comes when this one has gone, asked of L2: its slice,
+// if the row is read, and the values of its ids.  HBM is then busy while the CTAs
+// of an SM happen to compute, and a slice arrives sooner (4096 rows of 128256: 367
+// us, 415 without).  In two steps of one warp, so that nothing waits in between.
+template <typename T, bool kDistill, int kEach>
+struct LookAhead {
+  int row, ids[kEach];
+  float weight;
+  __device__ __forceinline__ void ask(const RowGradArgs& a, int now) {
+    row = now < a.rows.rows - a.ahead ? now + a.ahead : -1;
+    weight = !kDistill && a.weights && row >= 0 ? a.weights[row] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int k = (int(threadIdx.x) & 31) + 32 * i;
+      ids[i] = row >= 0 && k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
+    }
+  }
+  __device__ __forceinline__ void fetch(const RowGradArgs& a, int rank) const {
+    bool some = weight != 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) some |= ids[i] >= 0;
+    if (!__any_sync(~0u, some)) return;
+    const int lane = int(threadIdx.x) & 31;
+    const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+    const Slice<T> s(nullptr, z, a.rows.vocab, a.rows.slice, rank);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(z + s.first + s.full0 * Slice<T>::kPer);
+    const uint32_t bytes = uint32_t(s.full1 - s.full0) * 16u, at = uint32_t(lane) * Slice<T>::kPiece;
+    if (at < bytes) prefetch_l2(from + at, min(Slice<T>::kPiece, bytes - at));
+    for (int k = lane; k < a.count; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.values + int64_t(row) * a.count + k));
+  }
+};
 
-template <typename T, bool kDistill>
+// kEach: places per lane, count rounded up to whole warps.
+template <typename T, bool kDistill, int kEach>
 __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_constant__ RowGradArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];   // the slice
   __shared__ Meeting meet;
@@ -426,23 +442,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   const float temperature = row_temperature(a.rows, row);
   const float weight = a.weights ? a.weights[row] : kDistill ? 1.0f : 0.0f;
   int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
-  int ids[kMaxIds / 32];
-  float values[kMaxIds / 32];
-  T logits[kMaxIds / 32];
-  if (warp == kLearner) {
-#pragma unroll
-    for (int i = 0; i < kMaxIds / 32; ++i) {
-      const int k = lane + 32 * i;
-      ids[i] = k < a.count ? a.ids[int64_t(row) * a.count + k] : -1;
-      values[i] = k < a.count ? a.values[int64_t(row) * a.count + k] : 0.0f;
-    }
-    // every CTA has all of the ids' logits: what they add to Z needs no exchange
-#pragma unroll
-    for (int i = 0; i < kMaxIds / 32; ++i) {
-      logits[i] = RowVec<T>::minus_inf();
-      if (ids[i] >= 0 && ids[i] < a.rows.vocab) logits[i] = z[ids[i]];   // not looked at before the barrier
-    }
-  }
+  Inputs<T, kEach> in;
+  if (warp == kLearner) in.ask(a, row, z);
   const bool some = __syncthreads_or(id >= 0) || (!kDistill && weight != 0.0f), past = __syncthreads_or(id >= a.rows.vocab);
   int flags = !some ? 0 : (past ? kRowBadToken : 0) | (temperature_fits(temperature) ? 0 : kRowBadParams);
   const bool read = some && !flags;
@@ -452,6 +453,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&bar)) : "memory");
   }
   const float nan = __uint_as_float(0x7FC00000u), c = __fdiv_rn(kLog2e, temperature);
+  LookAhead<T, kDistill, kEach> next;
+  if (warp == kLearner) next.ask(a, row);
   if (!read) {
     cluster_all_run(ranks);
     if (warp == kLearner) {
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
         if (kDistill) a.loss[row] = flags ? nan : 0.0f;
         if (flags && a.rows.status) atomicOr(a.rows.status, flags);
       }
-      look_ahead<T, kDistill>(a, row, rank);
+      next.fetch(a, rank);
       return;
     }
     s.fill(flags ? nan : 0.0f);
@@ -468,13 +471,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   }
   bool late = false, plain = false;
   if (warp == kLearner) {
-    float logit[kMaxIds / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxIds / 32; ++i) {
-      logit[i] = clean(load1(&logits[i]));
-      if (ids[i] < 0) values[i] = kDistill ? -INFINITY : 0.0f;
-    }
-    learn_row<kDistill>(a, ids, values, logit, temperature, weight, f);
+    learn_row<kDistill>(in, a.count, a.tail != 0, temperature, weight, f);
+    next.fetch(a, rank);
     cluster_all_run(ranks);
   } else {
     late = !wait_full(&bar, 0, a.rows.wait_limit);
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   const float4 p = posted(meet, ranks);
   if (__any_sync(~0u, lane < ranks && p.w != 0.0f)) flags = kRowTimeout;
   float m, ca = 0.0f, cb = 0.0f, share = 0.0f;   // share: of this thread's id, by itself
-  id = tid < kMaxIds ? f.ids[tid] : -1;
+  id = tid < 32 * kEach ? f.ids[tid] : -1;
   const bool here = s.holds(id);
   if (kDistill) {
     const Stats all = warp_join<false>(Stats{p.x, p.y, 0.0f}, c);
@@ -505,7 +503,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     const float rest = all.z > 0.0f ? f.rest : 0.0f, total = rest > 0.0f ? 1.0f : f.given, inv_z = __frcp_rn(whole.zsum);
     if (warp == kLearner) {
       if (rank == 0) {
-        const float loss = row_loss(f.ids, f.add, f.logit, kMaxIds, f.t_log_t, all, whole.m, whole.zsum, rest, temperature);
+        const float loss = row_loss(f.ids, f.add, f.logit, 32 * kEach, f.t_log_t, all, whole.m, whole.zsum, rest, temperature);
         if (lane == 0) a.loss[row] = flags ? nan : loss;
       }
     }
@@ -530,7 +528,6 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   }
   if (warp == kLearner) {
     if (flags && rank == 0 && lane == 0 && a.rows.status) atomicOr(a.rows.status, flags);
-    look_ahead<T, kDistill>(a, row, rank);
     return;
   }
   if (flags) s.fill(nan);
@@ -558,7 +555,10 @@ smp_status launch_row_grad(RowGradArgs a, cudaStream_t st) {
   ls.smem = size_t(a.rows.slice) * elem;
   const int on_sm = std::max<int>(1, std::min<int>(3, int(227 * 1024 / (ls.smem + 3 * 1024))));
   a.ahead = std::max(1, device_sms(dev) * on_sm / c);
-  return launch_rows(reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill>), a, ls, st, kRowThreads);
+  const void* kernel = a.count <= 32   ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 1>)
+                       : a.count <= 64 ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 2>)
+                                       : reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 4>);
+  return launch_rows(kernel, a, ls, st, kRowThreads);
 }
 
 }  // namespace smp
