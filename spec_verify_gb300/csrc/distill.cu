@@ -67,9 +67,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
   const bool apart = edge >= 0 && (bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u);
   const float at_edge = edge >= 0 && !apart ? clean(load1(z + edge)) : -INFINITY;
   const unsigned char* bytes = dynamic;
-  uint4 x[2][kUnit];
   stream<true>(
-      s, run, x, temperature, c,
+      s, run, temperature, c,
       [&](uint4& y, int k) {
         const int j = s.full0 + k;
         if (j < s.full1) {

@@ -351,17 +351,17 @@ __device__ __forceinline__ uint4 load_last(const uint4* p) {
 constexpr int kUnit = 4;     // vectors of a thread that are loaded and taken in together
 
 // Takes the part's whole vectors into `run`, a unit per thread at a time: while
-// one unit is taken in, the next is on its way, in x[0] and x[1], which hold all
-// of the thread's vectors where there are two units at most.  change(y, k) may
-// alter vector k (from the first whole one) first; seen(top) gets the largest
-// element of each unit, in order.
+// one unit is taken in, the next is on its way.  change(y, k) may alter vector k
+// (from the first whole one) first; seen(top) gets the largest element of each
+// unit, in order.
 template <bool kConst, typename T, bool kWeighted, typename Change, typename Seen>
-__device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, uint4 (&x)[2][kUnit],
-                                       const float& temperature, const float& c, Change&& change, Seen&& seen) {
+__device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, float temperature,
+                                       float c, Change&& change, Seen&& seen) {
   using V = RowVec<T>;
   constexpr int kStep = kUnit * kThreads;
   const int vecs = s.full1 - s.full0, pairs = vecs / (2 * kStep);
   const pair_t c2 = both(c);
+  uint4 x[2][kUnit];
   const uint4* p = s.vec() + s.full0 + threadIdx.x;
   auto load = [&](uint4 (&y)[kUnit], const uint4* from) {
 #pragma unroll

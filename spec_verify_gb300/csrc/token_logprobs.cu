@@ -9,7 +9,9 @@
 // of its 256 threads' maxima is at most the slice's n-th largest element, since
 // n threads each hold an element that large: everything at or above it (a few
 // more than n) is collected and ranked by comparing packed (value, id) words.
-// The first CTA of the cluster merges the sorted lists by binary search.
+// The first CTA of the cluster puts the CTAs' candidates in order, by counting for
+// each the larger ones, or by bisection in lists that the CTAs have ordered where
+// many alternatives are wanted.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -19,6 +21,7 @@
 namespace smp {
 
 constexpr int kCandidates = 512;   // collected before the slow exact way takes over
+constexpr int kShortLists = 32;    // most alternatives whose candidates are only put in order at the end
 
 struct ScoreArgs {
   RowsArgs rows;
@@ -29,10 +32,11 @@ struct ScoreArgs {
   int32_t* top_ids;
   float* top_logprobs;
   int run_room;   // most runs of any CTA
+  int list_room;  // words of a CTA's list
 };
 
-// A thread's units of kUnit vectors come in up to kRuns runs whose maxima are
-// kept, `units` in each.
+// A thread's units of kUnit vectors come in up to kRuns runs whose maxima are kept.
+static_assert(kUnit == 4, "runs are counted in shifts");
 constexpr int kRuns = 16;
 
 // What slice_top works with, in shared memory.
@@ -55,7 +59,7 @@ __device__ __forceinline__ uint32_t nth_key(const uint16_t* keys, int top) {
   uint32_t lo = k[0], hi = k[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) lo = min(lo, k[i]), hi = max(hi, k[i]);
-  lo = __reduce_min_sync(~0u, lo), hi = __reduce_max_sync(~0u, hi);
+  lo = __reduce_min_sync(~0u, top <= 32 ? hi : lo), hi = __reduce_max_sync(~0u, hi);   // 32 keys reach the lanes' least maximum
   if (top == 1) return hi;
   while (lo < hi) {
     const uint32_t mid = (lo + hi + 1) >> 1;
@@ -68,13 +72,14 @@ __device__ __forceinline__ uint32_t nth_key(const uint16_t* keys, int top) {
   return lo;
 }
 
-// The `top` largest elements of the part, in order, as packed words (0: none)
-// to `list` of the cluster's first CTA.  `mine` is the largest of this thread's
-// elements, run_top[run][thread] of each run, `edge` its edge element's id; `x`
-// are the thread's vectors where it has two units of them at most.
+// The candidates for a part's `top` largest elements, as packed words in
+// room.cand; returns how many, at least the `top` largest (or all that are
+// finite) among them.  `mine` is the largest of this thread's elements,
+// run_top[run][thread] of each run of 2^run_bits units, `edge` its edge element's
+// id.
 template <typename T>
-__device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int units, int edge,
-                                          const uint4 (&x)[2][kUnit], int top, TopRoom& room, uint64_t* list, int ranks) {
+__device__ __forceinline__ int slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int run_bits, int edge,
+                                         int top, TopRoom& room) {
   using V = RowVec<T>;
   constexpr int kPer = V::kPer;
   const int tid = int(threadIdx.x);
@@ -118,74 +123,42 @@ __device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const fl
     }
   };
   const int vecs = s.full1 - s.full0;
-  const bool at_hand = vecs < 2 * kUnit * kThreads;
   if (mine >= limit) {
     if (edge >= 0) {
       const float v = Elem<T>::widen(s.row[edge]);
       if (v >= limit) keep(atomicAdd(&room.found, 1), v, edge);
     }
-    if (at_hand) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int at[kUnit];
-#pragma unroll
-        for (int u = 0; u < kUnit; ++u) {
-          const int k = tid + (h * kUnit + u) * kThreads;
-          at[u] = k < vecs ? s.first + (s.full0 + k) * kPer : -1;
-        }
-        take(x[h], at);
-      }
-    } else {
-      uint32_t mask = 0;
+    uint32_t mask = 0;
 #pragma unroll 4
-      for (int run = 0; run < runs; ++run) mask |= (run_top[run * kThreads + tid] >= limit ? 1u : 0u) << run;
-      int place = mask ? atomicAdd(&room.hit_count, __popc(mask)) : 0;
-      for (; mask; mask &= mask - 1, ++place)
-        if (place < kCandidates) room.hits[place] = tid | (__ffs(mask) - 1) << 8;
-    }
+    for (int run = 0; run < runs; ++run) mask |= (run_top[run * kThreads + tid] >= limit ? 1u : 0u) << run;
+    int place = mask ? atomicAdd(&room.hit_count, __popc(mask)) : 0;
+    for (; mask; mask &= mask - 1, ++place)
+      if (place < kCandidates) room.hits[place] = tid | (__ffs(mask) - 1) << 8;
   }
   __syncthreads();
-  const int hits = room.hit_count, run_vecs = units * kUnit;
-  bool listed = hits <= kCandidates;
-  if (listed && hits) {   // the runs' vectors again (from L2), every thread some at a time
-    for (int i0 = tid; i0 < hits * run_vecs; i0 += kUnit * kThreads) {
-      uint4 y[kUnit];
-      int at[kUnit];
+  // The vectors of the runs that reach the limit again, from L2, spread over the
+  // threads (each thread its own runs: 3.0 us where this takes 1.9).
+  const int vectors = min(room.hit_count, kCandidates) << (run_bits + 2);
+  for (int i0 = tid; i0 < vectors; i0 += kUnit * kThreads) {
+    uint4 y[kUnit];
+    int at[kUnit];
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) {
-        const int i = i0 + u * kThreads;
-        at[u] = -1;
-        if (i < hits * run_vecs) {
-          const int hit = room.hits[i / run_vecs], k = (hit & 255) + ((hit >> 8) * run_vecs + i % run_vecs) * kThreads;
-          if (k < vecs) at[u] = s.first + (s.full0 + k) * kPer, y[u] = s.vec()[s.full0 + k];
-        }
+    for (int u = 0; u < kUnit; ++u) {
+      const int i = i0 + u * kThreads;
+      at[u] = -1;
+      if (i < vectors) {
+        const int hit = room.hits[i >> (run_bits + 2)], of = i & ((kUnit << run_bits) - 1);
+        const int k = (hit & 255) + (((hit >> 8) << (run_bits + 2)) + of) * kThreads;
+        if (k < vecs) at[u] = s.first + (s.full0 + k) * kPer, y[u] = s.vec()[s.full0 + k];
       }
-      take(y, at);
     }
-    __syncthreads();
+    take(y, at);
   }
-  listed = listed && room.found <= kCandidates;
-  const uint32_t to = ranks > 1 ? map_rank(smem_addr(list), 0) : 0;
-  auto put = [&](int place, uint64_t v) {
-    if (ranks > 1) st_cluster_u64(to + uint32_t(place) * 8u, v);
-    else list[place] = v;
-  };
-  if (listed) {   // a candidate's place is the number of larger ones: four lanes count for each
-    const int have = room.found;
-    for (int i0 = 0; i0 < have; i0 += kThreads / 4) {
-      const int i = i0 + (tid >> 2);
-      const uint64_t v = i < have ? room.cand[i] : ~0ull;
-      int place = 0;
-#pragma unroll 8
-      for (int j = tid & 3; j < have; j += 4) place += room.cand[j] > v;
-      place += __shfl_xor_sync(~0u, place, 1);
-      place += __shfl_xor_sync(~0u, place, 2);
-      if ((tid & 3) == 0 && i < have && place < top) put(place, v);
-    }
-    for (int i = have + tid; i < top; i += kThreads) put(i, 0);
-  } else {   // many equal values: one maximum after another, each below the last
+  __syncthreads();
+  int have = room.found;
+  if (have > kCandidates || room.hit_count > kCandidates) {   // many equal values: one maximum after another, each below the last
     uint64_t last = ~0ull;
-    for (int n = 0; n < top; ++n) {
+    for (have = 0; have < top; ++have) {
       uint64_t best = 0;
       for (int id = s.lo + tid; id < s.hi; id += kThreads) {
         const uint32_t k = key_of_bits(Elem<T>::bits(s.row[id]));
@@ -193,14 +166,23 @@ __device__ __forceinline__ void slice_top(const Part<T>& s, float mine, const fl
         if (v < last && v > best) best = v;
       }
       best = block_max_u64(best, room.scratch);
-      if (tid == 0) put(n, best);
-      if (best == 0) {
-        for (int i = n + 1 + tid; i < top; i += kThreads) put(i, 0);
-        break;
-      }
+      if (best == 0) break;
+      if (tid == 0) room.cand[have] = best;
       last = best;
     }
+    __syncthreads();
   }
+  return have;
+}
+
+// How many of the `count` words of `list` are above v; four neighbouring lanes
+// count together, and all of them get it.
+__device__ __forceinline__ int count_above(const uint64_t* list, int count, uint64_t v) {
+  int n = 0;
+#pragma unroll 8
+  for (int j = int(threadIdx.x) & 3; j < count; j += 4) n += list[j] > v;
+  n += __shfl_xor_sync(~0u, n, 1);
+  return n + __shfl_xor_sync(~0u, n, 2);
 }
 
 template <typename T, bool kEntropy, bool kTop>
@@ -226,10 +208,12 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
   TopRoom& room = *reinterpret_cast<TopRoom*>(dynamic);
   float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom));
   const int units_all = (s.full1 - s.full0 + kThreads * kUnit - 1) / (kThreads * kUnit);   // of a thread
-  const int units = (units_all + kRuns - 1) / kRuns, runs = units ? (units_all + units - 1) / units : 0;
+  const int run_bits = units_all <= kRuns ? 0 : 32 - __clz((units_all - 1) / kRuns);   // 2^run_bits units in a run
+  const int runs = (units_all + (1 << run_bits) - 1) >> run_bits;
   uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThreads);
   int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
   Stats all{-INFINITY, 0.0f, 0.0f};
+  int have = 0, theirs = 0;   // candidates of this CTA, of the CTA of this lane's number
   const float value = flags == 0 && s.holds(id) ? clean(load1(z + id)) : 0.0f;
   if (flags == 0) {
     Running<T, kEntropy> run;
@@ -237,11 +221,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     const float at_edge = edge >= 0 ? clean(load1(z + edge)) : -INFINITY;
     float best = -INFINITY, mine = at_edge;   // the largest of the run, of the thread
     int in_run = 0, r = 0;
-    uint4 x[2][kUnit];
-    stream<true>(s, run, x, temperature, c, [](uint4&, int) {}, [&](float top) {
+    stream<true>(s, run, temperature, c, [](uint4&, int) {}, [&](float top) {
       if (kTop) {
         best = fmaxf(best, top), mine = fmaxf(mine, top);
-        if (++in_run == units) {
+        if (++in_run == 1 << run_bits) {
           run_top[r * kThreads + tid] = best;
           best = -INFINITY, in_run = 0, ++r;
         }
@@ -254,15 +237,33 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
     const Stats part = warp_join<kEntropy>(run.stats(), c);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
-    if (kTop) slice_top(s, mine, run_top, runs, units, edge, x, a.top, room, lists + rank * a.top, ranks);
+    if (kTop) {
+      have = slice_top(s, mine, run_top, runs, run_bits, edge, a.top, room);
+      if (ranks > 1) {
+        const uint32_t to = map_rank(smem_addr(lists + rank * a.list_room), 0);
+        if (have <= a.list_room && a.top <= kShortLists) {   // as they are: the first CTA puts them in order
+          for (int i = tid; i < have; i += kThreads) st_cluster_u64(to + uint32_t(i) * 8u, room.cand[i]);
+        } else {
+          for (int i0 = 0; i0 < have; i0 += kThreads / 4) {
+            const int i = i0 + (tid >> 2);
+            const uint64_t v = i < have ? room.cand[i] : ~0ull;
+            const int place = count_above(room.cand, have, v);
+            if ((tid & 3) == 0 && i < have && place < a.top) st_cluster_u64(to + uint32_t(place) * 8u, v);
+          }
+          have = min(have, a.top);
+          for (int i = have + tid; i < a.top; i += kThreads) st_cluster_u64(to + uint32_t(i) * 8u, 0);
+        }
+      }
+    }
     __syncthreads();
     if (warp == 0) {
       const Stats cta = warp_join<kEntropy>(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
-      post(meet, rank, ranks, cta.m, cta.z, cta.s, 0.0f);
+      post(meet, rank, ranks, cta.m, cta.z, cta.s, float(have));
     }
     cluster_meet(ranks);
     const float4 p = posted(meet, ranks);
     all = warp_join<kEntropy>(Stats{p.x, p.y, p.z}, c);
+    theirs = lane < ranks ? int(p.w) : 0;
     if (!(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
   } else {
     cluster_all_run(ranks);
@@ -287,12 +288,32 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
       for (int i = tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = nan;
       return;
     }
-    if (ranks == 1) {   // one list, in order
-      for (int i = tid; i < a.top; i += kThreads) {
-        const uint64_t v = lists[i];
-        top_ids[i] = v ? int32_t(~uint32_t(v)) : -1;
-        top_logprobs[i] = v ? logprob(value_of_key(uint32_t(v >> 32))) : -INFINITY;
+    auto emit = [&](int place, uint64_t v) {   // 0: no token
+      if (place < a.top) {
+        top_ids[place] = v ? int32_t(~uint32_t(v)) : -1;
+        top_logprobs[place] = v ? logprob(value_of_key(uint32_t(v >> 32))) : -INFINITY;
       }
+    };
+    if (ranks == 1 || a.top <= kShortLists) {   // a token's place is the number of larger ones
+      int total = have;
+      if (ranks > 1) {   // the lists one after the other in room.cand
+        const int upto = int(warp_inclusive_scan<uint32_t>(uint32_t(theirs)));
+        total = __shfl_sync(~0u, upto, 31);
+        for (int e = tid; e < ranks * a.list_room; e += kThreads) {   // a warp's words are of one list
+          const int from = e / (2 * kShortLists), i = e % (2 * kShortLists), n = __shfl_sync(~0u, theirs, from);
+          const int at = __shfl_sync(~0u, upto, from) - n + i;
+          if (i < n) room.cand[at] = lists[e];
+        }
+        __syncthreads();
+      }
+      for (int e = tid; e < total; e += kThreads) {
+        const uint64_t v = room.cand[e];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < total; ++j) place += room.cand[j] > v;
+        emit(place, v);
+      }
+      for (int i = total + tid; i < a.top; i += kThreads) emit(i, 0);
       return;
     }
     // A token's place is the number of larger ones in all lists, by bisection in
@@ -316,10 +337,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
       int place = v ? 0 : e < a.top ? e - lo[0] : a.top;
 #pragma unroll
       for (int r = 0; r < kMaxParts; ++r) place += lo[r];
-      if (place < a.top) {
-        top_ids[place] = v ? int32_t(~uint32_t(v)) : -1;
-        top_logprobs[place] = v ? logprob(value_of_key(uint32_t(v >> 32))) : -INFINITY;
-      }
+      emit(place, v);
     }
   }
 }
@@ -335,9 +353,10 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
   const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
   if (ok != SMP_OK) return ok;
   if (a.top) {
+    a.list_room = a.top <= kShortLists ? 2 * kShortLists : a.top;
     const int unit = kThreads * kUnit * RowVec<T>::kPer;
     a.run_room = std::min(kRuns, (a.rows.slice + unit - 1) / unit);
-    ls.smem = sizeof(TopRoom) + size_t(a.run_room) * kThreads * 4 + size_t(ls.cluster) * a.top * 8;
+    ls.smem = sizeof(TopRoom) + size_t(a.run_room) * kThreads * 4 + (ls.cluster > 1 ? size_t(ls.cluster) * a.list_room * 8 : 0);
   }
   return launch_rows(kernel, a, ls, st);
 }
