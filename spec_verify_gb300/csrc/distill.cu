@@ -17,24 +17,15 @@
 
 namespace smp {
 
-struct DistillArgs {
-  RowsArgs rows;
-  const int32_t* ids;
-  const float* values;
-  int count, tail;
-  float* loss;
-};
-
 // The loss alone: nothing has to stay on chip, so a row streams through one CTA
 // (or the CTAs of a cluster, where rows are few), and a bit per element says
-// which are the teacher's.  The cluster's first CTA holds the teacher's row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_constant__ DistillArgs a) {
+// which are the teacher's.  A ninth warp of the cluster's first CTA works up the
+// teacher's row meanwhile.
+template <typename T, int kEach>
+__global__ void __launch_bounds__(kRowThreads, 3) distill_loss_kernel(const __grid_constant__ RowGradArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];   // a bit per element of the part
   __shared__ Meeting meet;
-  __shared__ Stats ids_warp[kMaxIds / 32];
-  __shared__ Teacher teach;
-  __shared__ float student[kMaxIds];
+  __shared__ RowFacts f;
   const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   allow_dependent_launch();
@@ -45,8 +36,10 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
   const Part<T> s(z, a.rows.vocab, a.rows.slice, rank);
   const float temperature = row_temperature(a.rows, row), c = __fdiv_rn(kLog2e, temperature);
   const int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
+  Inputs<T, kEach> in;
+  if (warp == kLearner && rank == 0) in.ask(a, row, z);
   uint32_t* bits = reinterpret_cast<uint32_t*>(dynamic);
-  for (int i = tid; i < (a.rows.slice + 31) / 32; i += kThreads) bits[i] = 0;
+  for (int i = tid; i < (a.rows.slice + 31) / 32; i += kRowThreads) bits[i] = 0;
   const bool live = __syncthreads_or(id >= 0), past = __syncthreads_or(id >= a.rows.vocab);
   int flags = (past ? kRowBadToken : 0) | (temperature_fits(temperature) ? 0 : kRowBadParams);
   if (!live || flags) {
@@ -57,52 +50,45 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
     }
     return;
   }
-  if (s.holds(id)) atomicOr(&bits[(id - s.first) >> 5], 1u << ((id - s.first) & 31));
-  const float value = rank == 0 && id >= 0 ? clean(load1(z + id)) : -INFINITY;
-  if (tid < kMaxIds) teach.ids[tid] = id;
-  if (rank == 0 && warp == 0) teacher_row(a.ids, a.values, a.count, a.tail, row, teach);
-  __syncthreads();
-  Running<T, false> run;
-  const int edge = s.edge();
-  const bool apart = edge >= 0 && (bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u);
-  const float at_edge = edge >= 0 && !apart ? clean(load1(z + edge)) : -INFINITY;
-  const unsigned char* bytes = dynamic;
-  stream<true>(
-      s, run, temperature, c,
-      [&](uint4& y, int k) {
-        const int j = s.full0 + k;
-        if (j < s.full1) {
-          const uint32_t b = Part<T>::kPer == 8 ? bytes[j] : bytes[j >> 1] >> (4 * (j & 1)) & 15u;
-          if (b) erase(y, b, T{});
-        }
-      },
-      [](float) {});
-  run.add_one(at_edge, temperature, c);
-  const Stats part = warp_join<false>(run.stats(), c);
-  if (lane == 0) meet.warp[warp] = part;
-  if (rank == 0 && warp < kMaxIds / 32) {
-    float sum;
-    const bool counts = id >= 0 && value > -INFINITY && first_of_id(teach.ids, teach.t, a.count, tid, sum);
-    const Stats on_ids = warp_join<false>(counts ? Stats{value, 1.0f, 0.0f} : Stats{-INFINITY, 0.0f, 0.0f}, c);
-    if (lane == 0) ids_warp[warp] = on_ids;
-    student[tid] = value;
-  }
-  cluster_all_run(ranks);
-  __syncthreads();
-  const Stats none{-INFINITY, 0.0f, 0.0f};
-  if (warp == 0) {
-    const Stats cta = warp_join<false>(lane < kWarps ? meet.warp[lane] : none, c);
-    post(meet, rank, ranks, cta.m, cta.z, 0.0f, 0.0f);
+  if (warp == kLearner) {
+    if (rank == 0) learn_row<true>(in, a.count, a.tail != 0, temperature, 1.0f, f);
+    cluster_all_run(ranks);
+  } else {
+    if (s.holds(id)) atomicOr(&bits[(id - s.first) >> 5], 1u << ((id - s.first) & 31));
+    const int edge = s.edge();
+    const float at_edge = edge >= 0 ? clean(load1(z + edge)) : -INFINITY;
+    cta_sync();
+    Running<T, false> run;
+    const unsigned char* bytes = dynamic;
+    stream<true>(
+        s, run, temperature, c,
+        [&](uint4& y, int k) {
+          const int j = s.full0 + k;
+          if (j < s.full1) {
+            const uint32_t b = Part<T>::kPer == 8 ? bytes[j] : bytes[j >> 1] >> (4 * (j & 1)) & 15u;
+            if (b) erase(y, b, T{});
+          }
+        },
+        [](float) {});
+    if (edge >= 0 && !(bits[(edge - s.first) >> 5] >> ((edge - s.first) & 31) & 1u)) run.add_one(at_edge, temperature, c);
+    const Stats part = warp_join<false>(run.stats(), c);
+    if (lane == 0) meet.warp[warp] = part;
+    cluster_all_run(ranks);
+    cta_sync();
+    if (warp == 0) {
+      const Stats cta = warp_join<false>(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
+      post(meet, rank, ranks, cta.m, cta.z, 0.0f, 0.0f);
+    }
   }
   cluster_meet(ranks);
-  if (rank != 0 || warp != 0) return;
+  if (rank != 0 || warp != kLearner) return;
   const float4 p = posted(meet, ranks);
   const Stats r = warp_join<false>(Stats{p.x, p.y, 0.0f}, c);
-  const Stats k = warp_join<false>(lane < kMaxIds / 32 ? ids_warp[lane] : none, c);
-  const Whole all(r, k, c);
-  flags = teach.flags;
+  const Whole all(r, f.on_ids, c);
+  flags = f.flags;
   if (!flags && !(fabsf(all.m) < INFINITY)) flags = kRowNonFinite;
-  const float loss = row_loss(teach.ids, teach.t, student, kMaxIds, teach.t_log_t, r, all.m, all.zsum, r.z > 0.0f ? teach.rest : 0.0f, temperature);
+  const float loss = row_loss(f.ids, f.add, f.logit, 32 * kEach, f.t_log_t, r, all.m, all.zsum, r.z > 0.0f ? f.rest : 0.0f,
+                              temperature);
   if (lane == 0) {
     a.loss[row] = flags ? __uint_as_float(0x7FC00000u) : loss;
     if (flags && a.rows.status) atomicOr(a.rows.status, flags);
@@ -110,12 +96,15 @@ __global__ void __launch_bounds__(kThreads, 4) distill_loss_kernel(const __grid_
 }
 
 template <typename T>
-static smp_status launch_distill_loss(DistillArgs a, cudaStream_t st) {
+static smp_status launch_distill_loss(RowGradArgs a, cudaStream_t st) {
   LaunchShape ls;
   const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
   if (ok != SMP_OK) return ok;
   ls.smem = size_t(a.rows.slice + 127) / 128 * 16;
-  return launch_rows(reinterpret_cast<const void*>(&distill_loss_kernel<T>), a, ls, st);
+  const void* kernel = a.count <= 32   ? reinterpret_cast<const void*>(&distill_loss_kernel<T, 1>)
+                       : a.count <= 64 ? reinterpret_cast<const void*>(&distill_loss_kernel<T, 2>)
+                                       : reinterpret_cast<const void*>(&distill_loss_kernel<T, 4>);
+  return launch_rows(kernel, a, ls, st, kRowThreads);
 }
 
 }  // namespace smp
@@ -139,13 +128,11 @@ extern "C" smp_status smp_distill(const void* logits, int32_t rows, int32_t voca
     if (rc != SMP_OK) return rc;
   }
   if (rows == 0) return SMP_OK;
-  DistillArgs a{};
+  RowGradArgs a{};
   a.rows.logits = logits, a.rows.stride = stride, a.rows.rows = rows, a.rows.vocab = vocab;
   a.rows.temperature = temperature, a.rows.temperatures = temperatures, a.rows.status = status;
-  a.ids = teacher_ids, a.values = teacher_logprobs, a.count = count, a.tail = tail, a.loss = out_loss;
+  a.ids = teacher_ids, a.values = teacher_logprobs, a.count = count, a.tail = tail;
+  a.weights = weights, a.loss = out_loss, a.grad = out_grad, a.grad_stride = grad_stride;
   if (!out_grad) return dtype == SMP_F32 ? launch_distill_loss<float>(a, st) : launch_distill_loss<uint16_t>(a, st);
-  RowGradArgs g{};
-  g.rows = a.rows, g.ids = a.ids, g.values = a.values, g.count = count, g.tail = tail;
-  g.weights = weights, g.loss = out_loss, g.grad = out_grad, g.grad_stride = grad_stride;
-  return dtype == SMP_F32 ? launch_row_grad<float, true>(g, st) : launch_row_grad<uint16_t, true>(g, st);
+  return dtype == SMP_F32 ? launch_row_grad<float, true>(a, st) : launch_row_grad<uint16_t, true>(a, st);
 }

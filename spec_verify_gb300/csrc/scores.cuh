@@ -451,19 +451,6 @@ __device__ __forceinline__ float row_temperature(const RowsArgs& a, int row) {
 }
 __device__ __forceinline__ bool temperature_fits(float t) { return t >= SMP_MIN_TEMPERATURE && t <= SMP_MAX_TEMPERATURE; }
 
-// First occurrence of each id in `ids` and the sum of `add` over its places:
-// what thread k < count gets for id k.
-__device__ __forceinline__ bool first_of_id(const int* ids, const float* add, int count, int k, float& sum) {
-  bool first = true;
-  sum = 0.0f;
-  for (int i = 0; i < count; ++i)
-    if (ids[i] == ids[k]) {
-      first &= i >= k;
-      sum += add[i];
-    }
-  return first;
-}
-
 // Vector x without the elements whose bits are set.
 __device__ __forceinline__ void erase(uint4& x, uint32_t bits, uint16_t) {
   uint32_t* w[4] = {&x.x, &x.y, &x.z, &x.w};
@@ -478,63 +465,6 @@ __device__ __forceinline__ void erase(uint4& x, uint32_t bits, float) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (bits >> i & 1u) *w[i] = RowVec<float>::kNegInf2;
-}
-
-// The teacher's row: t of each place, r, sum t ln t.
-struct Teacher {
-  int ids[kMaxIds];
-  float t[kMaxIds];
-  float given, rest, t_log_t;   // sum t, ...
-  int flags;
-};
-
-// Fills `teach` but for its ids (one warp).  r = 1 - sum t is a small difference: it is taken
-// from fixed-point exponentials, which are exact to 2^-45 each.
-__device__ __forceinline__ void teacher_row(const int32_t* ids, const float* values, int count, int tail, int row,
-                                            Teacher& teach) {
-  const int lane = int(threadIdx.x) & 31;
-  constexpr int kEach = kMaxIds / 32;
-  float l[kEach];
-  bool live[kEach], bad = false;
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int k = lane + 32 * i;
-    const int id = k < count ? ids[int64_t(row) * count + k] : -1;
-    live[i] = id >= 0;
-    l[i] = live[i] ? values[int64_t(row) * count + k] : -INFINITY;
-    bad |= !(l[i] < INFINITY);
-    top = fmaxf(top, l[i]);
-  }
-  float log_sum = 0.0f, given = 1.0f, rest = 0.0f;
-  if (tail) {
-    uint64_t mass = 0;
-    const RowScale unit = make_row_scale_unit(0.0f);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (live[i]) mass += mass_fixed(fminf(l[i], 1.0f), unit, kExp2Table);
-    mass = warp_sum<uint64_t>(mass);
-    bad |= mass > kFixedOne + (kFixedOne >> 6);
-    given = float(mass) * 0x1p-44f;
-    rest = mass < kFixedOne ? float(kFixedOne - mass) * 0x1p-44f : 0.0f;
-  } else {
-    top = warp_max_f(top);
-    bad |= !(top > -INFINITY);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) sum += expf(__fsub_rn(l[i], top));
-    log_sum = __fadd_rn(top, logf(warp_sum_f(sum)));
-  }
-  float t_log_t = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const float log_t = __fsub_rn(l[i], log_sum), t = live[i] ? expf(log_t) : 0.0f;
-    if (t > 0.0f) t_log_t = __fmaf_rn(t, log_t, t_log_t);
-    teach.t[lane + 32 * i] = t;
-  }
-  t_log_t = warp_sum_f(t_log_t);
-  bad = __any_sync(~0u, bad);
-  if (lane == 0) teach.given = given, teach.rest = rest, teach.t_log_t = t_log_t, teach.flags = bad ? kRowBadParams : 0;
 }
 
 // Both statistics together: m, Z and the factors 2^((m_i - m) c).
