@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_loss_kernel(const __gr
 template <typename T>
 static smp_status launch_distill_loss(RowGradArgs a, cudaStream_t st) {
   LaunchShape ls;
-  const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
+  const smp_status ok = shape_parts(a.rows, int(sizeof(T)), 8 * 1024, ls);
   if (ok != SMP_OK) return ok;
   ls.smem = size_t(a.rows.slice + 127) / 128 * 16;
   const void* kernel = a.count <= 32   ? reinterpret_cast<const void*>(&distill_loss_kernel<T, 1>)

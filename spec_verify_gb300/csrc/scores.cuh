@@ -523,15 +523,20 @@ inline bool grad_fits(const void* logits, int32_t rows, int32_t vocab, int64_t s
   return grad != logits || rows <= 1 || grad_stride == stride;
 }
 
-// The launch of a kernel whose CTAs read their parts of a row from memory once:
-// one row per CTA where there are many rows, parts of it where they would leave
-// SMs without work.
-inline smp_status shape_parts(RowsArgs& r, int elem, LaunchShape& ls) {
+// The launch of a kernel whose CTAs read their parts of a row from memory once: a
+// row per CTA, or parts of it while all of them fit on the SMs together, three on
+// each, and are of 30 KB at least, or of `least` while each has an SM of its own.
+// Losses of 150 rows of 32000 in bf16: 6.5 us with two CTAs a row, 7.2 with one,
+// 8.1 with four (a second wave); of 8192 in binary32: 4.6, 4.6 and 6.7; of 8 rows of
+// 32000 in bf16 4.2 with four and 4.6 with two.  Log probabilities of a row of
+// 128256 with eight: 7.0, with one 11.4; of 8192 in bf16 with one 5.5, with two 6.1.
+inline smp_status shape_parts(RowsArgs& r, int elem, int least, LaunchShape& ls) {
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
-  const int64_t bytes = int64_t(r.vocab) * elem;
+  const int64_t bytes = int64_t(r.vocab) * elem, sms = device_sms(dev);
   int c = 1;
-  while (c < kMaxParts && int64_t(r.rows) * c * 2 <= int64_t(device_sms(dev)) * 4 && bytes >= int64_t(c) * 16 * 1024) c *= 2;
+  auto may = [&](int64_t room, int64_t part) { return c < kMaxParts && int64_t(r.rows) * c * 2 <= room && bytes >= 2 * c * part; };
+  while (may(3 * sms, 30 * 1024) || may(sms, least)) c *= 2;
   ls.cluster = forced_cluster() ? std::min(forced_cluster(), kMaxParts) : c;
   const int per = 16 / elem;
   r.slice = ((r.vocab + per - 1 + ls.cluster - 1) / ls.cluster + per - 1) / per * per;

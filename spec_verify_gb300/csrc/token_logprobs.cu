@@ -21,6 +21,7 @@
 namespace smp {
 
 constexpr int kCandidates = 512;   // collected before the slow exact way takes over
+constexpr int kAheadVectors = 1024;   // of the successor's part
 constexpr int kShortLists = 32;    // most alternatives whose candidates are only put in order at the end
 
 struct ScoreArgs {
@@ -33,6 +34,7 @@ struct ScoreArgs {
   float* top_logprobs;
   int run_room;   // most runs of any CTA
   int list_room;  // words of a CTA's list
+  int ahead;      // rows between a CTA's and that of the CTA that takes its place on the SM
 };
 
 // A thread's units of kUnit vectors come in up to kRuns runs whose maxima are kept.
@@ -185,8 +187,12 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int count, uint
   return n + __shfl_xor_sync(~0u, n, 2);
 }
 
-template <typename T, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
+// kOnSm: CTAs on an SM.  Four where there are more rows than three would hold, so
+// that some stream while others are at their alternatives (4093 x 152064: 200 us,
+// 207 with three); three, with more registers each, for few rows (160 x 32000 in
+// binary32: 10.4 us, 11.1 with four).
+template <typename T, bool kEntropy, bool kTop, int kOnSm>
+__global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];   // with kTop: TopRoom, the runs' maxima, the lists
   __shared__ Meeting meet;
   const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
@@ -230,6 +236,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
         }
       }
     });
+    if (tid == 0 && (kTop || kEntropy) && row < a.rows.rows - a.ahead) {   // L2 is asked for the start of the successor's part
+      const Part<T> next(z + a.ahead * a.rows.stride, a.rows.vocab, a.rows.slice, rank);
+      prefetch_l2(reinterpret_cast<uintptr_t>(next.vec() + next.full0), uint32_t(min(next.full1 - next.full0, kAheadVectors)) * 16u);
+    }
     run.add_one(at_edge, temperature, c);
     if (kTop) {
       for (; r < runs; ++r, best = -INFINITY) run_top[r * kThreads + tid] = best;
@@ -342,16 +352,30 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const __gri
   }
 }
 
+template <typename T, int kOnSm>
+static const void* score_kernel(bool entropy, bool top) {
+  return entropy ? (top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true, kOnSm>)
+                        : reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, false, kOnSm>))
+                 : (top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, true, kOnSm>)
+                        : reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, false, kOnSm>));
+}
+
 template <typename T>
 static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
-  const void* kernel =
-      a.entropy ? (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true>)
-                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, false>))
-                : (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, true>)
-                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, false>));
   LaunchShape ls;
-  const smp_status ok = shape_parts(a.rows, int(sizeof(T)), ls);
+  const smp_status ok = shape_parts(a.rows, int(sizeof(T)), 30 * 1024, ls);
   if (ok != SMP_OK) return ok;
+  const int sms = device_sms(current_device());
+  // Halves of long rows where four on an SM hold them: 256 rows of 128256 in bf16 20.9 us, whole ones with three on an
+  // SM 22.5; 300 rows of 32000 in binary32 12.2 and 11.9.
+  if (ls.cluster == 1 && !forced_cluster() && a.rows.rows <= 2 * sms && int64_t(a.rows.vocab) * int(sizeof(T)) >= 200 * 1024) {
+    constexpr int kPer = RowVec<T>::kPer;
+    ls.cluster = 2;
+    a.rows.slice = ((a.rows.vocab + kPer - 1 + 1) / 2 + kPer - 1) / kPer * kPer;
+  }
+  const bool many = int64_t(a.rows.rows) * ls.cluster > int64_t(sms) * 3;
+  const void* kernel = many ? score_kernel<T, 4>(a.entropy != nullptr, a.top > 0) : score_kernel<T, 3>(a.entropy != nullptr, a.top > 0);
+  a.ahead = std::max(1, sms * 4 / ls.cluster);
   if (a.top) {
     a.list_room = a.top <= kShortLists ? 2 * kShortLists : a.top;
     const int unit = kThreads * kUnit * RowVec<T>::kPer;
