@@ -42,7 +42,7 @@ struct RowGradArgs {
 // buf[id - first]; the row is laid out as in memory modulo 16 bytes, so that its
 // whole vectors [full0, full1) go by bulk copies.  The edge vectors hold -inf
 // outside the row.
-template <typename T>
+template <typename T, int kThr>
 struct Slice {
   static constexpr int kPer = RowVec<T>::kPer;
   static constexpr uint32_t kPiece = 16384;
@@ -89,9 +89,9 @@ struct Slice {
   // that is aligned as the slice is; returns once `buf` has been read.
   __device__ __forceinline__ void leave(T* row) const {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    cta_sync();
+    workers_sync<kThr>();
     if ((reinterpret_cast<uintptr_t>(row + first) & 15u) != 0) {
-      for (int id = lo + int(threadIdx.x); id < hi; id += kThreads) row[id] = buf[id - first];
+      for (int id = lo + int(threadIdx.x); id < hi; id += kThr) row[id] = buf[id - first];
     } else if (threadIdx.x < 32) {
       if (threadIdx.x == 0) {
         const uint32_t bytes = uint32_t(full1 - full0) * 16u;
@@ -114,11 +114,9 @@ struct Slice {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = x;
     const uint4 w = RowVec<T>::put(v);
-    for (int j = int(threadIdx.x); j < vecs; j += kThreads) vec()[j] = w;
+    for (int j = int(threadIdx.x); j < vecs; j += kThr) vec()[j] = w;
   }
 };
-
-constexpr int kLearner = kWarps, kRowThreads = kThreads + 32;
 
 // ------------------------------------------------------------------ what is known of a row before it is read
 
@@ -256,21 +254,21 @@ __device__ __forceinline__ void learn_row(const Inputs<T, kEach>& in, int count,
 
 // Calls take(vectors, first) for this thread's vectors of the slice, kUnit at a
 // time, -inf in the places of those that are not there.
-template <typename T, typename Take>
-__device__ __forceinline__ void each_unit(const Slice<T>& s, Take&& take) {
+template <typename T, int kThr, typename Take>
+__device__ __forceinline__ void each_unit(const Slice<T, kThr>& s, Take&& take) {
   using V = RowVec<T>;
   const uint4* p = s.vec();
 #pragma unroll 1
-  for (int j = int(threadIdx.x); j < s.vecs; j += kUnit * kThreads) {
+  for (int j = int(threadIdx.x); j < s.vecs; j += kUnit * kThr) {
     uint4 y[kUnit];
-    if (j + (kUnit - 1) * kThreads < s.vecs) {
+    if (j + (kUnit - 1) * kThr < s.vecs) {
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
+      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThr];
     } else {
 #pragma unroll
       for (int u = 0; u < kUnit; ++u) {
         y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
-        if (j + u * kThreads < s.vecs) y[u] = p[j + u * kThreads];
+        if (j + u * kThr < s.vecs) y[u] = p[j + u * kThr];
       }
     }
     take(y, j == int(threadIdx.x));
@@ -283,13 +281,13 @@ __device__ __forceinline__ void each_unit(const Slice<T>& s, Take&& take) {
 // enters the sums: y = z c - m c in one fused multiply-add, m the largest of the
 // first unit.  The sums say whether that held (they are finite); otherwise the
 // share is summed again with care, and `plain` is false.
-template <typename T, bool kWeighted>
-__device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperature, float c, bool& plain) {
+template <bool kWeighted, typename T, int kThr>
+__device__ __forceinline__ Stats slice_stats(const Slice<T, kThr>& s, float temperature, float c, bool& plain) {
   using V = RowVec<T>;
   float m = 0.0f;
   pair_t z = 0, zy = 0, shift = 0;
   const pair_t c2 = both(c);
-  each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool first) {
+  each_unit(s, [&](const uint4 (&y)[kUnit], bool first) {
     if (first) {
       uint32_t w = V::kNegInf2;
 #pragma unroll
@@ -319,29 +317,29 @@ __device__ __forceinline__ Stats slice_stats(const Slice<T>& s, float temperatur
     return warp_join<kWeighted>(part, c);
   }
   Running<T, kWeighted> run;
-  each_unit<T>(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
+  each_unit(s, [&](const uint4 (&y)[kUnit], bool) { run.take(y, temperature, c); });
   return warp_join<kWeighted>(run.stats(), c);
 }
 
 // Replaces the slice's elements z by 2^((z - m) c) (A + B (z - m)); plain: as
 // slice_stats found them.
-template <typename T, bool kWeighted>
-__device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float temperature, float c, float ca, float cb, bool plain) {
+template <bool kWeighted, typename T, int kThr>
+__device__ __forceinline__ void slice_grad(const Slice<T, kThr>& s, float m, float temperature, float c, float ca, float cb, bool plain) {
   using V = RowVec<T>;
   uint4* p = s.vec();
   const pair_t c2 = both(c);
   auto turn_all = [&](auto&& turn) {
     int j = int(threadIdx.x);
 #pragma unroll 1
-    for (; j + (kUnit - 1) * kThreads < s.vecs; j += kUnit * kThreads) {
+    for (; j + (kUnit - 1) * kThr < s.vecs; j += kUnit * kThr) {
       uint4 y[kUnit];
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThreads];
+      for (int u = 0; u < kUnit; ++u) y[u] = p[j + u * kThr];
 #pragma unroll
-      for (int u = 0; u < kUnit; ++u) p[j + u * kThreads] = turn(y[u]);
+      for (int u = 0; u < kUnit; ++u) p[j + u * kThr] = turn(y[u]);
     }
 #pragma unroll 1
-    for (; j < s.vecs; j += kThreads) p[j] = turn(p[j]);
+    for (; j < s.vecs; j += kThr) p[j] = turn(p[j]);
   };
   if (plain && fabsf(__fmul_rn(m, c)) < 128.0f) {
     if (kWeighted) {   // 2^y (A + (B / c) y), y = z c - m c
@@ -392,7 +390,7 @@ __device__ __forceinline__ void slice_grad(const Slice<T>& s, float m, float tem
 // if the row is read, and the values of its ids.  HBM is then busy while the CTAs
 // of an SM happen to compute, and a slice arrives sooner (4096 rows of 128256: 367
 // us, 415 without).  In two steps of one warp, so that nothing waits in between.
-template <typename T, bool kDistill, int kEach>
+template <typename T, bool kDistill, int kEach, int kThr>
 struct LookAhead {
   int row, ids[kEach];
   float weight;
@@ -412,17 +410,18 @@ struct LookAhead {
     if (!__any_sync(~0u, some)) return;
     const int lane = int(threadIdx.x) & 31;
     const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-    const Slice<T> s(nullptr, z, a.rows.vocab, a.rows.slice, rank);
-    const uintptr_t from = reinterpret_cast<uintptr_t>(z + s.first + s.full0 * Slice<T>::kPer);
-    const uint32_t bytes = uint32_t(s.full1 - s.full0) * 16u, at = uint32_t(lane) * Slice<T>::kPiece;
-    if (at < bytes) prefetch_l2(from + at, min(Slice<T>::kPiece, bytes - at));
+    const Slice<T, kThr> s(nullptr, z, a.rows.vocab, a.rows.slice, rank);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(z + s.first + s.full0 * Slice<T, kThr>::kPer);
+    const uint32_t bytes = uint32_t(s.full1 - s.full0) * 16u, at = uint32_t(lane) * Slice<T, kThr>::kPiece;
+    if (at < bytes) prefetch_l2(from + at, min(Slice<T, kThr>::kPiece, bytes - at));
     for (int k = lane; k < a.count; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.values + int64_t(row) * a.count + k));
   }
 };
 
-// kEach: places per lane, count rounded up to whole warps.
-template <typename T, bool kDistill, int kEach>
-__global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_constant__ RowGradArgs a) {
+// kEach: places per lane, count rounded up to whole warps.  kThr: threads that work
+// on the slice, before the warp that works up the row's small inputs.
+template <typename T, bool kDistill, int kEach, int kThr, int kOnSm>
+__global__ void __launch_bounds__(kThr + 32, kOnSm) row_grad_kernel(const __grid_constant__ RowGradArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];   // the slice
   __shared__ Meeting meet;
   __shared__ RowFacts f;
@@ -432,7 +431,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
   allow_dependent_launch();
   const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
   T* out = static_cast<T*>(a.grad) + int64_t(row) * a.grad_stride;
-  const Slice<T> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
+  constexpr int kLearner = kThr / 32;
+  const Slice<T, kThr> s(reinterpret_cast<T*>(dynamic), z, a.rows.vocab, a.rows.slice, rank);
   if (tid == 0) {
     mbar_init(&bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     if (lane == 0) asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&bar)) : "memory");
   }
   const float nan = __uint_as_float(0x7FC00000u), c = __fdiv_rn(kLog2e, temperature);
-  LookAhead<T, kDistill, kEach> next;
+  LookAhead<T, kDistill, kEach, kThr> next;
   if (warp == kLearner) next.ask(a, row);
   if (!read) {
     cluster_all_run(ranks);
@@ -478,14 +478,14 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     late = !wait_full(&bar, 0, a.rows.wait_limit);
     if (late) wait_full(&bar, 0, kWaitLimitNs);   // the copy lands in this CTA's memory: not before that is over
     if (kDistill && s.holds(id)) s.buf[id - s.first] = RowVec<T>::minus_inf();
-    late = cta_sync_count(late) > 0;
+    late = workers_any<kThr>(late);
     const bool weighted = !kDistill && weight != 0.0f;
-    const Stats part = weighted ? slice_stats<T, !kDistill>(s, temperature, c, plain) : slice_stats<T, false>(s, temperature, c, plain);
+    const Stats part = weighted ? slice_stats<!kDistill>(s, temperature, c, plain) : slice_stats<false>(s, temperature, c, plain);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
-    cta_sync();
+    workers_sync<kThr>();
     if (warp == 0) {
-      const Stats none{-INFINITY, 0.0f, 0.0f}, mine = lane < kWarps ? meet.warp[lane] : none;
+      const Stats none{-INFINITY, 0.0f, 0.0f}, mine = lane < kThr / 32 ? meet.warp[lane] : none;
       const Stats cta = weighted ? warp_join<true>(mine, c) : warp_join<false>(mine, c);
       post(meet, rank, ranks, cta.m, cta.z, cta.s, late ? 1.0f : 0.0f);
     }
@@ -531,11 +531,19 @@ __global__ void __launch_bounds__(kRowThreads, 3) row_grad_kernel(const __grid_c
     return;
   }
   if (flags) s.fill(nan);
-  else if (!kDistill && weight != 0.0f && !is_lowest<T>(m)) slice_grad<T, !kDistill>(s, m, temperature, c, ca, cb, plain);
-  else slice_grad<T, false>(s, m, temperature, c, ca, 0.0f, plain);
-  cta_sync();
+  else if (!kDistill && weight != 0.0f && !is_lowest<T>(m)) slice_grad<!kDistill>(s, m, temperature, c, ca, cb, plain);
+  else slice_grad<false>(s, m, temperature, c, ca, 0.0f, plain);
+  workers_sync<kThr>();
   if (here && !flags) store1(s.buf + (id - s.first), share);
   s.leave(out);
+}
+
+template <typename T, bool kDistill, int kThr, int kOnSm>
+smp_status launch_row_grad_of(const RowGradArgs& a, const LaunchShape& ls, cudaStream_t st) {
+  const void* kernel = a.count <= 32   ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 1, kThr, kOnSm>)
+                       : a.count <= 64 ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 2, kThr, kOnSm>)
+                                       : reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 4, kThr, kOnSm>);
+  return launch_rows(kernel, a, ls, st, kThr + 32);
 }
 
 template <typename T, bool kDistill>
@@ -543,25 +551,29 @@ smp_status launch_row_grad(RowGradArgs a, cudaStream_t st) {
   LaunchShape ls;
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
-  // As few CTAs per row as let three of them stand on an SM.  More where rows are few, while each has an SM of its
-  // own (two of a pair may share one) and 8 KB at least: 37 rows of 32000 in bf16 5.4 us with four CTAs a row, 6.0 with
-  // two, 5.7 with eight; 76 rows in binary32 7.6 with two and 8.7 with four; 150 in bf16 9.4 with one and 8.6 with two.
+  // As few CTAs per row as let three of them stand on an SM.  More where rows are few and longer than 32 KB, while each
+  // CTA has an SM of its own (two of a pair may share one, and two with 60 KB each) and 15 KB: 37 rows of 32000 in bf16
+  // 5.3 us with four CTAs a row, 6.0 with two, 5.7 with eight; of 128256 9.5 with eight and 10.0 with four; of 8192 4.0
+  // with one and 4.8 with two; 76 rows of 32000 in binary32 7.6 with two and 8.7 with four; 150 in bf16 9.4 with one and
+  // 8.6 with two.
   const int elem = int(sizeof(T)), per = 16 / elem;
   auto slice = [&](int c) { return ((a.rows.vocab + per - 1 + c - 1) / c + per - 1) / per * per; };
   int c = 1;
   while (c < 16 && slice(c) * elem > 72 * 1024) c *= 2;
-  while (c < 8 && int64_t(a.rows.rows) * c * 2 <= int64_t(device_sms(dev)) * (c == 1 ? 2 : 1) && slice(c) * elem >= 16000)
-    c *= 2;
+  auto may = [&](int64_t room, int64_t least) { return int64_t(a.rows.rows) * c * 2 <= room && slice(c) * elem > least; };
+  const int64_t sms = device_sms(dev);
+  while (c < 8 && (c == 1 ? may(2 * sms, 32 * 1024) : may(sms, 15 * 1024) || may(2 * sms, 60 * 1024))) c *= 2;
   if (forced_cluster() && slice(forced_cluster()) * elem <= 200 * 1024) c = forced_cluster();
   ls.cluster = c;
   a.rows.slice = slice(c);
   ls.smem = size_t(a.rows.slice) * elem;
-  const int on_sm = std::max<int>(1, std::min<int>(3, int(227 * 1024 / (ls.smem + 3 * 1024))));
-  a.ahead = std::max(1, device_sms(dev) * on_sm / c);
-  const void* kernel = a.count <= 32   ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 1>)
-                       : a.count <= 64 ? reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 2>)
-                                       : reinterpret_cast<const void*>(&row_grad_kernel<T, kDistill, 4>);
-  return launch_rows(kernel, a, ls, st, kRowThreads);
+  // Five CTAs of 128 threads on an SM instead of three of 256 where slices are small enough for that and more than
+  // stand at once: 1200 rows of 152064 in bf16 132 us and not 143, 4096 of 8192 28 and not 39; but 300 of 8192 6.1 and
+  // not 5.2, and with 128 threads on slices of 64 KB 4096 rows of 32000 86 and not 84 (117 and not 100 with entropies).
+  const bool small = ls.smem <= 42 * 1024 && int64_t(a.rows.rows) * c > 3 * sms;
+  const int on_sm = small ? 5 : std::max<int>(1, std::min<int>(3, int(227 * 1024 / (ls.smem + 3 * 1024))));
+  a.ahead = std::max(1, int(sms) * on_sm / c);
+  return small ? launch_row_grad_of<T, kDistill, 128, 5>(a, ls, st) : launch_row_grad_of<T, kDistill, kThreads, 3>(a, ls, st);
 }
 
 }  // namespace smp

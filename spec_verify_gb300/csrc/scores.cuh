@@ -245,28 +245,34 @@ struct Running {
       floor = floor_word<T>(m, temperature);
     }
   }
-  // A vector that m is fit for; m is not -inf.
-  __device__ __forceinline__ void add(const uint4& x, pair_t c) {
-    pair_t v[V::kPer / 2];
-    V::get(x, floor, v);
+  // Vectors that m is fit for; m is not -inf.  Their weights are summed before they
+  // enter the thread's sums, which so take a rounding per call and not one per
+  // element.
+  template <int kN>
+  __device__ __forceinline__ void add(const uint4 (&y)[kN], float c) {
+    pair_t sum = 0, weighted = 0;
 #pragma unroll
-    for (int i = 0; i < V::kPer / 2; ++i) {
-      const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, c));
-      z = add2(z, e);
-      if (kWeighted) s = fma2(e, d, s);
+    for (int u = 0; u < kN; ++u) {
+      pair_t v[V::kPer / 2];
+      V::get(y[u], floor, v);
+#pragma unroll
+      for (int i = 0; i < V::kPer / 2; ++i) {
+        const pair_t d = add2(v[i], minus_m), e = ex2_both(mul2(d, both(c)));
+        sum = u + i == 0 ? e : add2(sum, e);
+        if (kWeighted) weighted = u + i == 0 ? mul2(e, d) : fma2(e, d, weighted);
+      }
     }
+    z = add2(z, sum);
+    if (kWeighted) s = add2(s, weighted);
   }
-  // Some vectors.
+  // Any vectors.
   template <int kN>
   __device__ __forceinline__ void take(const uint4 (&y)[kN], float temperature, float c) {
     uint32_t w = V::kNegInf2;
 #pragma unroll
     for (int u = 0; u < kN; ++u) w = V::top(y[u], w);
     raise(V::finish(w), temperature, c);
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int u = 0; u < kN; ++u) add(y[u], both(c));
-    }
+    if (m > -INFINITY) add(y, c);
   }
   __device__ __forceinline__ void add_one(float v, float temperature, float c) {   // clean
     if (v > -INFINITY) {
@@ -300,7 +306,7 @@ __device__ __forceinline__ Stats warp_join(const Stats& part, float c) {
 // ------------------------------------------------------------------ a part of a row, read once from memory
 
 // Elements [lo, hi) of a row, whole vectors [full0, full1) of 16 bytes counted
-// from element `first`; thread t takes vectors full0 + t, full0 + t + kThreads,
+// from element `first`; thread t of kThr takes vectors full0 + t, full0 + t + kThr,
 // ... and the edge threads one element each outside them.
 template <typename T>
 struct Part {
@@ -323,28 +329,12 @@ struct Part {
   }
 };
 
-// A vector past the L1 cache; kConst: of memory that the kernel does not write.
-template <bool kConst>
+// A vector past the L1 cache, of memory that the kernel does not write.
 __device__ __forceinline__ uint4 load_vector(const uint4* p) {
   uint4 v;
-  if (kConst)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-  else
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-  return v;
-}
-// A vector that was read before and is not wanted again.
-__device__ __forceinline__ uint4 load_last(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
+               : "l"(p));
   return v;
 }
 
@@ -354,39 +344,35 @@ constexpr int kUnit = 4;     // vectors of a thread that are loaded and taken in
 // one unit is taken in, the next is on its way.  change(y, k) may alter vector k
 // (from the first whole one) first; seen(top) gets the largest element of each
 // unit, in order.
-template <bool kConst, typename T, bool kWeighted, typename Change, typename Seen>
+template <int kThr, typename T, bool kWeighted, typename Change, typename Seen>
 __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& run, float temperature,
                                        float c, Change&& change, Seen&& seen) {
   using V = RowVec<T>;
-  constexpr int kStep = kUnit * kThreads;
+  constexpr int kStep = kUnit * kThr;
   const int vecs = s.full1 - s.full0, pairs = vecs / (2 * kStep);
-  const pair_t c2 = both(c);
   uint4 x[2][kUnit];
   const uint4* p = s.vec() + s.full0 + threadIdx.x;
   auto load = [&](uint4 (&y)[kUnit], const uint4* from) {
 #pragma unroll
-    for (int u = 0; u < kUnit; ++u) y[u] = load_vector<kConst>(from + u * kThreads);
+    for (int u = 0; u < kUnit; ++u) y[u] = load_vector(from + u * kThr);
   };
   auto load_some = [&](uint4 (&y)[kUnit], int unit) {
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
       y[u] = make_uint4(V::kNegInf2, V::kNegInf2, V::kNegInf2, V::kNegInf2);
-      if (int(threadIdx.x) + unit * kStep + u * kThreads < vecs) y[u] = load_vector<kConst>(p + unit * kStep + u * kThreads);
+      if (int(threadIdx.x) + unit * kStep + u * kThr < vecs) y[u] = load_vector(p + unit * kStep + u * kThr);
     }
   };
   auto take = [&](uint4 (&y)[kUnit], int unit) {
     uint32_t w = V::kNegInf2;
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
-      change(y[u], int(threadIdx.x) + (unit * kUnit + u) * kThreads);
+      change(y[u], int(threadIdx.x) + (unit * kUnit + u) * kThr);
       w = V::top(y[u], w);
     }
     const float top = V::finish(w);
     run.raise(top, temperature, c);
-    if (run.m > -INFINITY) {
-#pragma unroll
-      for (int u = 0; u < kUnit; ++u) run.add(y[u], c2);
-    }
+    if (run.m > -INFINITY) run.add(y, c);
     seen(top);
   };
   if (pairs > 0) {
@@ -408,6 +394,24 @@ __device__ __forceinline__ void stream(const Part<T>& s, Running<T, kWeighted>& 
     take(x[0], 2 * pairs);
     if ((2 * pairs + 1) * kStep < vecs) take(x[1], 2 * pairs + 1);
   }
+}
+
+// Barrier of a CTA's first kThr threads, the ones that work on whole rows.
+template <int kThr>
+__device__ __forceinline__ void workers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThr) : "memory");
+}
+
+// The same, and whether the predicate holds for one of them.
+template <int kThr>
+__device__ __forceinline__ bool workers_any(bool pred) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(int(pred)), "n"(kThr)
+      : "memory");
+  return r != 0;
 }
 
 // What the CTAs of a cluster tell one another, and the room their warps meet in.
@@ -544,16 +548,30 @@ inline smp_status shape_parts(RowsArgs& r, int elem, int least, LaunchShape& ls)
 }
 
 // Launches `kernel` on every row; `a` is its argument, whose member `rows` is a
-// RowsArgs.
+// RowsArgs.  Without a cluster where one CTA has a row: as clusters of one, no more
+// than 16 small CTAs came to stand on an SM (8192 rows of 8191, CTAs of 32 threads:
+// 68 us, 39 this way).
 template <typename Args>
-smp_status launch_rows(const void* kernel, Args a, LaunchShape ls, cudaStream_t st, int threads = kThreads) {
+smp_status launch_rows(const void* kernel, Args a, LaunchShape ls, cudaStream_t st, int threads) {
   const int dev = current_device();
   if (dev < 0) return fail_cuda(cudaGetLastError());
   ls.pdl = true;
   a.rows.wait_limit = wait_limit_ns();
   cudaError_t err = prepare_kernel(kernel, dev, ls);
   if (err != cudaSuccess) return fail_cuda(err);
-  err = launch_cluster(kernel, dim3(unsigned(a.rows.rows) * unsigned(ls.cluster)), dim3(unsigned(threads)), ls, st, &a);
+  const dim3 grid(unsigned(a.rows.rows) * unsigned(ls.cluster)), block{unsigned(threads)};
+  if (ls.cluster > 1) {
+    err = launch_cluster(kernel, grid, block, ls, st, &a);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = ls.smem, cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    void* params[1] = {&a};
+    err = cudaLaunchKernelExC(&cfg, kernel, params);
+  }
   return err == cudaSuccess ? SMP_OK : fail_cuda(err);
 }
 

@@ -42,33 +42,38 @@ static_assert(kUnit == 4, "runs are counted in shifts");
 constexpr int kRuns = 16;
 
 // What slice_top works with, in shared memory.
+template <int kThr>
 struct TopRoom {
-  alignas(16) uint16_t keys[kThreads];
-  int hits[kCandidates];           // thread | run << 8
+  static constexpr int kCandidates = kThr == kThreads ? smp::kCandidates : smp::kCandidates / 2;
+  alignas(16) uint16_t keys[kThr];
+  uint16_t hits[kCandidates];      // thread | run << 8
   uint64_t cand[kCandidates];
-  uint64_t scratch[kWarps];
+  uint64_t scratch[kThr / 32];
   uint32_t bound;
   int hit_count, found;
 };
 
-// The largest value that `top` of the 256 keys reach, in one warp: bisection
-// between the smallest and the largest key, which are a few hundred apart in
-// ordinary rows (256 threads that count keys bit by bit behind a barrier each
-// took 1.1 to 2.4 us, this 0.3).
+// The largest value that `top` of the keys reach, in one warp: bisection between
+// the smallest and the largest key, which are a few hundred apart in ordinary rows
+// (256 threads that count keys bit by bit behind a barrier each took 1.1 to 2.4 us,
+// this 0.3).
+template <int kThr>
 __device__ __forceinline__ uint32_t nth_key(const uint16_t* keys, int top) {
-  const uint4 w = reinterpret_cast<const uint4*>(keys)[int(threadIdx.x) & 31];
-  const uint32_t k[8] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16, w.z & 0xFFFFu, w.z >> 16, w.w & 0xFFFFu, w.w >> 16};
+  constexpr int kEach = kThr / 32;
+  uint32_t k[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) k[i] = keys[(int(threadIdx.x) & 31) + 32 * i];
   uint32_t lo = k[0], hi = k[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) lo = min(lo, k[i]), hi = max(hi, k[i]);
+  for (int i = 1; i < kEach; ++i) lo = min(lo, k[i]), hi = max(hi, k[i]);
   lo = __reduce_min_sync(~0u, top <= 32 ? hi : lo), hi = __reduce_max_sync(~0u, hi);   // 32 keys reach the lanes' least maximum
   if (top == 1) return hi;
   while (lo < hi) {
     const uint32_t mid = (lo + hi + 1) >> 1;
-    uint32_t n = 0;
+    int n = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) n += k[i] >= mid;
-    if (int(__reduce_add_sync(~0u, n)) >= top) lo = mid;
+    for (int i = 0; i < kEach; ++i) n += kEach == 1 ? __popc(__ballot_sync(~0u, k[i] >= mid)) : int(k[i] >= mid);
+    if ((kEach == 1 ? n : __reduce_add_sync(~0u, n)) >= top) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -79,9 +84,10 @@ __device__ __forceinline__ uint32_t nth_key(const uint16_t* keys, int top) {
 // finite) among them.  `mine` is the largest of this thread's elements,
 // run_top[run][thread] of each run of 2^run_bits units, `edge` its edge element's
 // id.
-template <typename T>
+template <int kThr, typename T>
 __device__ __forceinline__ int slice_top(const Part<T>& s, float mine, const float* run_top, int runs, int run_bits, int edge,
-                                         int top, TopRoom& room) {
+                                         int top, TopRoom<kThr>& room) {
+  constexpr int kCandidates = TopRoom<kThr>::kCandidates;
   using V = RowVec<T>;
   constexpr int kPer = V::kPer;
   const int tid = int(threadIdx.x);
@@ -90,7 +96,7 @@ __device__ __forceinline__ int slice_top(const Part<T>& s, float mine, const flo
   if (tid == 0) room.hit_count = room.found = 0;
   __syncthreads();
   if (tid < 32) {
-    const uint32_t b = nth_key(room.keys, top);
+    const uint32_t b = nth_key<kThr>(room.keys, top);
     if (tid == 0) room.bound = b;
   }
   __syncthreads();
@@ -132,25 +138,25 @@ __device__ __forceinline__ int slice_top(const Part<T>& s, float mine, const flo
     }
     uint32_t mask = 0;
 #pragma unroll 4
-    for (int run = 0; run < runs; ++run) mask |= (run_top[run * kThreads + tid] >= limit ? 1u : 0u) << run;
+    for (int run = 0; run < runs; ++run) mask |= (run_top[run * kThr + tid] >= limit ? 1u : 0u) << run;
     int place = mask ? atomicAdd(&room.hit_count, __popc(mask)) : 0;
     for (; mask; mask &= mask - 1, ++place)
-      if (place < kCandidates) room.hits[place] = tid | (__ffs(mask) - 1) << 8;
+      if (place < kCandidates) room.hits[place] = uint16_t(tid | (__ffs(mask) - 1) << 8);
   }
   __syncthreads();
   // The vectors of the runs that reach the limit again, from L2, spread over the
   // threads (each thread its own runs: 3.0 us where this takes 1.9).
   const int vectors = min(room.hit_count, kCandidates) << (run_bits + 2);
-  for (int i0 = tid; i0 < vectors; i0 += kUnit * kThreads) {
+  for (int i0 = tid; i0 < vectors; i0 += kUnit * kThr) {
     uint4 y[kUnit];
     int at[kUnit];
 #pragma unroll
     for (int u = 0; u < kUnit; ++u) {
-      const int i = i0 + u * kThreads;
+      const int i = i0 + u * kThr;
       at[u] = -1;
       if (i < vectors) {
         const int hit = room.hits[i >> (run_bits + 2)], of = i & ((kUnit << run_bits) - 1);
-        const int k = (hit & 255) + (((hit >> 8) << (run_bits + 2)) + of) * kThreads;
+        const int k = (hit & 255) + (((hit >> 8) << (run_bits + 2)) + of) * kThr;
         if (k < vecs) at[u] = s.first + (s.full0 + k) * kPer, y[u] = s.vec()[s.full0 + k];
       }
     }
@@ -162,12 +168,18 @@ __device__ __forceinline__ int slice_top(const Part<T>& s, float mine, const flo
     uint64_t last = ~0ull;
     for (have = 0; have < top; ++have) {
       uint64_t best = 0;
-      for (int id = s.lo + tid; id < s.hi; id += kThreads) {
+      for (int id = s.lo + tid; id < s.hi; id += kThr) {
         const uint32_t k = key_of_bits(Elem<T>::bits(s.row[id]));
         const uint64_t v = k > kKeyNegInf ? pack_key_id(k, uint32_t(id)) : 0;
         if (v < last && v > best) best = v;
       }
-      best = block_max_u64(best, room.scratch);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) best = max(best, shfl_xor_u64(best, o));
+      __syncthreads();
+      if ((tid & 31) == 0) room.scratch[tid >> 5] = best;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThr / 32; ++w) best = max(best, room.scratch[w]);
       if (best == 0) break;
       if (tid == 0) room.cand[have] = best;
       last = best;
@@ -191,8 +203,11 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int count, uint
 // that some stream while others are at their alternatives (4093 x 152064: 200 us,
 // 207 with three); three, with more registers each, for few rows (160 x 32000 in
 // binary32: 10.4 us, 11.1 with four).
-template <typename T, bool kEntropy, bool kTop, int kOnSm>
-__global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
+// kThr: threads of a CTA, 256 for parts of rows.  Where rows are many, smaller CTAs,
+// of which more stand on an SM, overlap more of what follows a row's stream; kThr
+// is at least twice the alternatives wanted, so that the threads' maxima bound them.
+template <typename T, bool kEntropy, bool kTop, int kThr, int kOnSm>
+__global__ void __launch_bounds__(kThr, kOnSm) token_logprobs_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];   // with kTop: TopRoom, the runs' maxima, the lists
   __shared__ Meeting meet;
   const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
@@ -211,12 +226,12 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
     if (rank == 0 && tid < a.count) logprobs[tid] = 0.0f;
     return;
   }
-  TopRoom& room = *reinterpret_cast<TopRoom*>(dynamic);
-  float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom));
-  const int units_all = (s.full1 - s.full0 + kThreads * kUnit - 1) / (kThreads * kUnit);   // of a thread
+  TopRoom<kThr>& room = *reinterpret_cast<TopRoom<kThr>*>(dynamic);
+  float* run_top = reinterpret_cast<float*>(dynamic + sizeof(TopRoom<kThr>));
+  const int units_all = (s.full1 - s.full0 + kThr * kUnit - 1) / (kThr * kUnit);   // of a thread
   const int run_bits = units_all <= kRuns ? 0 : 32 - __clz((units_all - 1) / kRuns);   // 2^run_bits units in a run
   const int runs = (units_all + (1 << run_bits) - 1) >> run_bits;
-  uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThreads);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(run_top + a.run_room * kThr);
   int flags = temperature_fits(temperature) ? 0 : kRowBadParams;
   Stats all{-INFINITY, 0.0f, 0.0f};
   int have = 0, theirs = 0;   // candidates of this CTA, of the CTA of this lane's number
@@ -227,11 +242,11 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
     const float at_edge = edge >= 0 ? clean(load1(z + edge)) : -INFINITY;
     float best = -INFINITY, mine = at_edge;   // the largest of the run, of the thread
     int in_run = 0, r = 0;
-    stream<true>(s, run, temperature, c, [](uint4&, int) {}, [&](float top) {
+    stream<kThr>(s, run, temperature, c, [](uint4&, int) {}, [&](float top) {
       if (kTop) {
         best = fmaxf(best, top), mine = fmaxf(mine, top);
         if (++in_run == 1 << run_bits) {
-          run_top[r * kThreads + tid] = best;
+          run_top[r * kThr + tid] = best;
           best = -INFINITY, in_run = 0, ++r;
         }
       }
@@ -242,32 +257,32 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
     }
     run.add_one(at_edge, temperature, c);
     if (kTop) {
-      for (; r < runs; ++r, best = -INFINITY) run_top[r * kThreads + tid] = best;
+      for (; r < runs; ++r, best = -INFINITY) run_top[r * kThr + tid] = best;
     }
     const Stats part = warp_join<kEntropy>(run.stats(), c);
     if (lane == 0) meet.warp[warp] = part;
     cluster_all_run(ranks);
     if (kTop) {
-      have = slice_top(s, mine, run_top, runs, run_bits, edge, a.top, room);
+      have = slice_top<kThr>(s, mine, run_top, runs, run_bits, edge, a.top, room);
       if (ranks > 1) {
         const uint32_t to = map_rank(smem_addr(lists + rank * a.list_room), 0);
         if (have <= a.list_room && a.top <= kShortLists) {   // as they are: the first CTA puts them in order
-          for (int i = tid; i < have; i += kThreads) st_cluster_u64(to + uint32_t(i) * 8u, room.cand[i]);
+          for (int i = tid; i < have; i += kThr) st_cluster_u64(to + uint32_t(i) * 8u, room.cand[i]);
         } else {
-          for (int i0 = 0; i0 < have; i0 += kThreads / 4) {
+          for (int i0 = 0; i0 < have; i0 += kThr / 4) {
             const int i = i0 + (tid >> 2);
             const uint64_t v = i < have ? room.cand[i] : ~0ull;
             const int place = count_above(room.cand, have, v);
             if ((tid & 3) == 0 && i < have && place < a.top) st_cluster_u64(to + uint32_t(place) * 8u, v);
           }
           have = min(have, a.top);
-          for (int i = have + tid; i < a.top; i += kThreads) st_cluster_u64(to + uint32_t(i) * 8u, 0);
+          for (int i = have + tid; i < a.top; i += kThr) st_cluster_u64(to + uint32_t(i) * 8u, 0);
         }
       }
     }
     __syncthreads();
     if (warp == 0) {
-      const Stats cta = warp_join<kEntropy>(lane < kWarps ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
+      const Stats cta = warp_join<kEntropy>(lane < kThr / 32 ? meet.warp[lane] : Stats{-INFINITY, 0.0f, 0.0f}, c);
       post(meet, rank, ranks, cta.m, cta.z, cta.s, float(have));
     }
     cluster_meet(ranks);
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
     int32_t* top_ids = a.top_ids + int64_t(row) * a.top;
     float* top_logprobs = a.top_logprobs + int64_t(row) * a.top;
     if (flags) {
-      for (int i = tid; i < a.top; i += kThreads) top_ids[i] = -1, top_logprobs[i] = nan;
+      for (int i = tid; i < a.top; i += kThr) top_ids[i] = -1, top_logprobs[i] = nan;
       return;
     }
     auto emit = [&](int place, uint64_t v) {   // 0: no token
@@ -309,27 +324,27 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
       if (ranks > 1) {   // the lists one after the other in room.cand
         const int upto = int(warp_inclusive_scan<uint32_t>(uint32_t(theirs)));
         total = __shfl_sync(~0u, upto, 31);
-        for (int e = tid; e < ranks * a.list_room; e += kThreads) {   // a warp's words are of one list
+        for (int e = tid; e < ranks * a.list_room; e += kThr) {   // a warp's words are of one list
           const int from = e / (2 * kShortLists), i = e % (2 * kShortLists), n = __shfl_sync(~0u, theirs, from);
           const int at = __shfl_sync(~0u, upto, from) - n + i;
           if (i < n) room.cand[at] = lists[e];
         }
         __syncthreads();
       }
-      for (int e = tid; e < total; e += kThreads) {
+      for (int e = tid; e < total; e += kThr) {
         const uint64_t v = room.cand[e];
         int place = 0;
 #pragma unroll 8
         for (int j = 0; j < total; ++j) place += room.cand[j] > v;
         emit(place, v);
       }
-      for (int i = total + tid; i < a.top; i += kThreads) emit(i, 0);
+      for (int i = total + tid; i < a.top; i += kThr) emit(i, 0);
       return;
     }
     // A token's place is the number of larger ones in all lists, by bisection in
     // all of them at once.  An entry that is none finds all tokens larger: those of
     // list 0 fill the places that are left.
-    for (int e = tid; e < ranks * a.top; e += kThreads) {
+    for (int e = tid; e < ranks * a.top; e += kThr) {
       const uint64_t v = lists[e];
       int lo[kMaxParts], hi[kMaxParts];
 #pragma unroll
@@ -352,12 +367,21 @@ __global__ void __launch_bounds__(kThreads, kOnSm) token_logprobs_kernel(const _
   }
 }
 
-template <typename T, int kOnSm>
-static const void* score_kernel(bool entropy, bool top) {
-  return entropy ? (top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true, kOnSm>)
-                        : reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, false, kOnSm>))
-                 : (top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, true, kOnSm>)
-                        : reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, false, kOnSm>));
+template <typename T, int kThr, int kOnSm>
+static smp_status launch_scores_of(ScoreArgs a, LaunchShape ls, cudaStream_t st) {
+  const void* kernel =
+      a.entropy ? (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, true, kThr, kOnSm>)
+                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, true, false, kThr, kOnSm>))
+                : (a.top ? reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, true, kThr, kOnSm>)
+                         : reinterpret_cast<const void*>(&token_logprobs_kernel<T, false, false, kThr, kOnSm>));
+  a.ahead = std::max(1, device_sms(current_device()) * kOnSm / ls.cluster);
+  if (a.top) {
+    a.list_room = a.top <= kShortLists ? 2 * kShortLists : a.top;
+    const int unit = kThr * kUnit * RowVec<T>::kPer;
+    a.run_room = std::min(kRuns, (a.rows.slice + unit - 1) / unit);
+    ls.smem = sizeof(TopRoom<kThr>) + size_t(a.run_room) * kThr * 4 + (ls.cluster > 1 ? size_t(ls.cluster) * a.list_room * 8 : 0);
+  }
+  return launch_rows(kernel, a, ls, st, kThr);
 }
 
 template <typename T>
@@ -366,6 +390,16 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
   const smp_status ok = shape_parts(a.rows, int(sizeof(T)), 30 * 1024, ls);
   if (ok != SMP_OK) return ok;
   const int sms = device_sms(current_device());
+  // Small CTAs for rows that are many and not long, as many threads as leave no SM without work: 8192 rows of 32000 in
+  // bf16 with one alternative 99 us with 32 threads, 106 with 64, 114 with 128, 143 with 256; 1200 rows with eight 29,
+  // 22, 19, 24; 2048 rows of 128256 with twenty: 108 with 64, 101 with 128 and 256.
+  if (ls.cluster == 1 && !forced_cluster() && int64_t(a.rows.vocab) * int(sizeof(T)) < 200 * 1024) {
+    const int least = std::max(2 * a.top, a.count);
+    auto fills = [&](int threads) { return threads >= least && int64_t(a.rows.rows) * threads >= int64_t(sms) * 768; };
+    if (fills(32)) return launch_scores_of<T, 32, 32>(a, ls, st);
+    if (fills(64)) return launch_scores_of<T, 64, 16>(a, ls, st);
+    if (fills(128)) return launch_scores_of<T, 128, 8>(a, ls, st);
+  }
   // Halves of long rows where four on an SM hold them: 256 rows of 128256 in bf16 20.9 us, whole ones with three on an
   // SM 22.5; 300 rows of 32000 in binary32 12.2 and 11.9.
   if (ls.cluster == 1 && !forced_cluster() && a.rows.rows <= 2 * sms && int64_t(a.rows.vocab) * int(sizeof(T)) >= 200 * 1024) {
@@ -373,16 +407,8 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
     ls.cluster = 2;
     a.rows.slice = ((a.rows.vocab + kPer - 1 + 1) / 2 + kPer - 1) / kPer * kPer;
   }
-  const bool many = int64_t(a.rows.rows) * ls.cluster > int64_t(sms) * 3;
-  const void* kernel = many ? score_kernel<T, 4>(a.entropy != nullptr, a.top > 0) : score_kernel<T, 3>(a.entropy != nullptr, a.top > 0);
-  a.ahead = std::max(1, sms * 4 / ls.cluster);
-  if (a.top) {
-    a.list_room = a.top <= kShortLists ? 2 * kShortLists : a.top;
-    const int unit = kThreads * kUnit * RowVec<T>::kPer;
-    a.run_room = std::min(kRuns, (a.rows.slice + unit - 1) / unit);
-    ls.smem = sizeof(TopRoom) + size_t(a.run_room) * kThreads * 4 + (ls.cluster > 1 ? size_t(ls.cluster) * a.list_room * 8 : 0);
-  }
-  return launch_rows(kernel, a, ls, st);
+  return int64_t(a.rows.rows) * ls.cluster > int64_t(sms) * 3 ? launch_scores_of<T, kThreads, 4>(a, ls, st)
+                                                              : launch_scores_of<T, kThreads, 3>(a, ls, st);
 }
 }  // namespace smp
 

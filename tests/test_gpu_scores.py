@@ -4,11 +4,14 @@ Tolerances.  A weight 2^y is off by its argument's rounding (y = (z - m) c has
 a relative error of 3.5 steps of 2^-24, so the weight one of ln 2 |y| 3.5
 2^-24: 3e-6 at |y| = 20, beyond which weights no longer matter to sums) and by
 ex2.approx (1.7e-7).  A sum of them adds at most 100 roundings one after another
-(a thread's share of a slice, then trees): 6e-6.  So Z, and with it ln Z, p and
+(a unit of 32 elements, a thread's units, then trees): 6e-6.  So Z, and with it ln Z, p and
 mean values, are within 2^-16 relative; values are then off by a few steps of
 2^-24 of the numbers they are made from: 2^-21 of those.  A weight of its own
 (a gradient's p_j) has |y| up to 126 before it is flushed: ln 2 * 126 * 3.5 *
-2^-24 = 1.8e-5, together below 2^-15.  bf16 results: half a step, 2^-8."""
+2^-24 = 1.8e-5, together below 2^-15.  A gradient whose argument is one fused multiply-add, z c
+plus a constant below 128 + 150, has that constant's rounding instead, 278 * 2^-24 ln
+2 = 1.1e-5, with z c's 2^-24 ln 2 * 128 * 2 the same 2^-15.  bf16 results: half a
+step, 2^-8."""
 
 import numpy as np
 import pytest
@@ -346,6 +349,30 @@ def test_every_cluster_size(cluster, dtype, monkeypatch):
         check_grad(scores.token_logprobs_grad(view, up(ids, torch.int32), up(g), up(h)), want, reach, dtype)
         values = np.log(rng.dirichlet(np.ones(4), rows)[:, :3]).astype(np.float32)
         check_distill(view, z, ids, values, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab,count,top", [(3700, 2300, 1, 1), (3700, 301, 32, 16), (1900, 1203, 33, 5), (1900, 4100, 5, 32),
+                                                  (950, 8193, 20, 0), (950, 70, 65, 40), (950, 700, 128, 64), (60, 77003, 2, 1)])
+def test_many_rows_by_small_thread_blocks(rows, vocab, count, top, dtype):
+    rng = np.random.default_rng(rows + vocab)
+    view, z, _ = rows_of(rng, rows, vocab, dtype, masked=0.05, stride=vocab + 3, offset=1)
+    view[7], view[11, 5], view[13, ::2], z[7], z[11, 5], z[13, ::2] = -np.inf, np.inf, np.nan, -np.inf, np.inf, np.nan
+    view[17, 1:], z[17, 1:] = -np.inf, -np.inf
+    ids = ids_for(rng, rows, vocab, count)
+    ids[3:5] = -1                                         # padding
+    t = rng.uniform(0.3, 3.0, rows).astype(np.float32)
+    check_logprobs(view, z, ids, top, t, flags=2)
+    check_logprobs(view, z, ids, top, 1.0, entropy=False, flags=2)
+    g, h = rng.normal(0, 1, (rows, count)).astype(np.float32), rng.normal(0, 1, rows).astype(np.float32)
+    h[::3] = 0.0
+    want, reach, flag = oracle.token_logprobs_grad(z, ids, g, h, t)
+    st = status()
+    got = scores.token_logprobs_grad(view, up(ids, torch.int32), up(g), up(h), temperature=up(t), status=st)
+    check_grad(got, want, reach, dtype, t)
+    assert int(st) == flag == 2
+    values = np.log(rng.dirichlet(np.ones(count + 1), rows)[:, :count]).astype(np.float32)
+    check_distill(view, z, ids, values, dtype, temperature=t, weight=h, flags=2)
 
 
 def all_calls(view, ids, g, h, values, stream=None):
