@@ -85,7 +85,8 @@ smp_status smp_token_logprobs(const void* logits, int32_t rows, int32_t vocab, i
  *   grad_entropy   device, [rows] float, or NULL (none).
  *   out_grad     device, like logits with its own stride, written for every
  *                row; may be the logits themselves with the same stride (in
- *                place), and must not overlap them otherwise.
+ *                place).  Rows that overlap the logits otherwise are refused; two
+ *                blocks of columns of one tensor do not.
  * A row without a token and with h = 0 is not read: its gradient is 0.
  */
 smp_status smp_token_logprobs_grad(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype,

@@ -138,7 +138,7 @@ extern "C" smp_status smp_distill(const void* logits, int32_t rows, int32_t voca
   const smp_status ok = check_rows(logits, rows, vocab, stride, dtype, temperature, temperatures, status);
   if (ok != SMP_OK) return ok;
   if (count < 1 || count > SMP_MAX_ROW_IDS) return SMP_ERR_INVALID_ARG;
-  if (out_grad && !grad_fits(logits, rows, vocab, stride, out_grad, grad_stride)) return SMP_ERR_INVALID_ARG;
+  if (out_grad && !grad_fits(logits, rows, vocab, stride, dtype, out_grad, grad_stride)) return SMP_ERR_INVALID_ARG;
   if (rows > 0 && (!teacher_ids || !teacher_logprobs || !out_loss)) return SMP_ERR_INVALID_ARG;
   if (misaligned(teacher_ids, 4) || misaligned(teacher_logprobs, 4) || misaligned(weights, 4) || misaligned(out_loss, 4) ||
       misaligned(out_grad, dtype == SMP_F32 ? 4 : 2))

@@ -521,10 +521,20 @@ inline smp_status check_rows(const void* logits, int32_t rows, int32_t vocab, in
   return SMP_OK;
 }
 
-// A gradient's rows: beside the logits, or in their place.
-inline bool grad_fits(const void* logits, int32_t rows, int32_t vocab, int64_t stride, const void* grad, int64_t grad_stride) {
+// A gradient's rows: in the logits' place, or where they share no element with them
+// (as two halves of wider rows, of one stride, do not).
+inline bool grad_fits(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype, const void* grad,
+                      int64_t grad_stride) {
   if (grad_stride < vocab || grad_stride > (int64_t(1) << 40)) return false;
-  return grad != logits || rows <= 1 || grad_stride == stride;
+  if (rows <= 0) return true;
+  if (grad == logits) return rows == 1 || grad_stride == stride;
+  const int64_t elem = dtype == SMP_F32 ? 4 : 2;
+  const uintptr_t z = reinterpret_cast<uintptr_t>(logits), g = reinterpret_cast<uintptr_t>(grad);
+  const uintptr_t z_bytes = uintptr_t(((rows - 1) * stride + vocab) * elem), g_bytes = uintptr_t(((rows - 1) * grad_stride + vocab) * elem);
+  if (g >= z + z_bytes || z >= g + g_bytes) return true;
+  if (rows == 1 || grad_stride != stride) return false;
+  const int64_t apart = int64_t(g > z ? g - z : z - g) % (stride * elem);   // of a row and the other's last before it
+  return apart >= vocab * elem && apart <= (stride - vocab) * elem;
 }
 
 // The launch of a kernel whose CTAs read their parts of a row from memory once: a

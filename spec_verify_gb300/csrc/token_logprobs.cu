@@ -450,7 +450,7 @@ extern "C" smp_status smp_token_logprobs_grad(const void* logits, int32_t rows, 
   if (ok != SMP_OK) return ok;
   if (count < 0 || count > SMP_MAX_ROW_IDS) return SMP_ERR_INVALID_ARG;
   if (count == 0 && !grad_entropy) return SMP_ERR_INVALID_ARG;
-  if (!grad_fits(logits, rows, vocab, stride, out_grad, grad_stride)) return SMP_ERR_INVALID_ARG;
+  if (!grad_fits(logits, rows, vocab, stride, dtype, out_grad, grad_stride)) return SMP_ERR_INVALID_ARG;
   if (rows > 0 && (!out_grad || (count > 0 && (!ids || !grad_logprobs)))) return SMP_ERR_INVALID_ARG;
   if (misaligned(ids, 4) || misaligned(grad_logprobs, 4) || misaligned(grad_entropy, 4) ||
       misaligned(out_grad, dtype == SMP_F32 ? 4 : 2))

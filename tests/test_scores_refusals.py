@@ -66,6 +66,17 @@ def test_distill(lib):
         assert call(lib.smp_distill, good, **bad) == 1, bad
 
 
+def test_gradients_over_the_logits(lib):
+    """Rows lie in the logits' place or share no element with them."""
+    at = lambda elements: ctypes.c_void_p((1 << 20) + 2 * elements)  # noqa: E731
+    good = dict(ROWS, logits=at(0), vocab=100, stride=300, ids=P, count=2, g=P, h=P, grad=P, gs=300, status=NULL, stream=NULL)
+    for elements, gs in ((1, 300), (99, 300), (-1, 300), (-99, 300), (201, 300), (299, 300), (301, 300), (600, 300), (150, 301),
+                         (0, 301), (-500, 400), (900, 300 - 1)):
+        assert call(lib.smp_token_logprobs_grad, good, grad=at(elements), gs=gs) == 1, (elements, gs)
+    for elements in (1, 99, -99, 50):
+        assert call(lib.smp_token_logprobs_grad, dict(good, rows=1), grad=at(elements)) == 1, elements
+
+
 def test_no_rows_are_no_work(lib):
     assert lib.smp_token_logprobs(NULL, 0, 100, 100, 0, 1.0, NULL, NULL, 2, 0, NULL, NULL, NULL, NULL, NULL, NULL) == 0
     assert lib.smp_token_logprobs_grad(NULL, 0, 100, 100, 0, 1.0, NULL, NULL, 2, NULL, NULL, NULL, 100, NULL, NULL) == 0
