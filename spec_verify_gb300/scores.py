@@ -32,10 +32,13 @@ def _queue(stream):
 
 
 def _beside(logits, stream):
-    """A gradient's tensor, laid out as the logits are."""
+    """A gradient's tensor: its rows end where they begin, but for what lets them
+    lie to 16-byte boundaries as the logits' rows do (both then go by bulk copies)."""
     _needs(logits, "logits", 2)
+    rows, vocab = logits.shape
+    stride = vocab + (logits.stride(0) - vocab) % (16 // logits.element_size()) if rows > 1 else vocab
     with _on(stream):
-        return _torch().empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+        return _torch().empty((rows, stride), dtype=logits.dtype, device=logits.device)[:, :vocab]
 
 
 def token_logprobs(logits, ids=None, top=0, entropy=False, temperature=1.0, out=None, status=None, stream=None):
