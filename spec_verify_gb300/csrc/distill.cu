@@ -125,7 +125,8 @@ static smp_status launch_distill_loss(RowGradArgs a, cudaStream_t st) {
   if (ls.cluster == 1 && !forced_cluster() && int64_t(a.rows.vocab) * int(sizeof(T)) < 200 * 1024 &&
       a.rows.rows >= 6 * device_sms(current_device()))
     return launch_distill_loss_of<T, 64, 9>(a, ls, st);
-  return launch_distill_loss_of<T, kThreads, 3>(a, ls, st);
+  return four_on_sm(a.rows, ls) ? launch_distill_loss_of<T, kThreads, 4>(a, ls, st)
+                                : launch_distill_loss_of<T, kThreads, 3>(a, ls, st);
 }
 
 }  // namespace smp

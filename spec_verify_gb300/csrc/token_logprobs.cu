@@ -199,10 +199,7 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int count, uint
   return n + __shfl_xor_sync(~0u, n, 2);
 }
 
-// kOnSm: CTAs on an SM.  Four where there are more rows than three would hold, so
-// that some stream while others are at their alternatives (4093 x 152064: 200 us,
-// 207 with three); three, with more registers each, for few rows (160 x 32000 in
-// binary32: 10.4 us, 11.1 with four).
+// kOnSm: CTAs on an SM.
 // kThr: threads of a CTA, 256 for parts of rows.  Where rows are many, smaller CTAs,
 // of which more stand on an SM, overlap more of what follows a row's stream; kThr
 // is at least twice the alternatives wanted, so that the threads' maxima bound them.
@@ -407,9 +404,9 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
     ls.cluster = 2;
     a.rows.slice = ((a.rows.vocab + kPer - 1 + 1) / 2 + kPer - 1) / kPer * kPer;
   }
-  return int64_t(a.rows.rows) * ls.cluster > int64_t(sms) * 3 ? launch_scores_of<T, kThreads, 4>(a, ls, st)
-                                                              : launch_scores_of<T, kThreads, 3>(a, ls, st);
+  return four_on_sm(a.rows, ls) ? launch_scores_of<T, kThreads, 4>(a, ls, st) : launch_scores_of<T, kThreads, 3>(a, ls, st);
 }
+
 }  // namespace smp
 
 extern "C" smp_status smp_token_logprobs(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype,
