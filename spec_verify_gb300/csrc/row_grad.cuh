@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThr + 32, kOnSm) row_grad_kernel(const __grid
     mbar_init(&bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  ask_early(a.rows, reinterpret_cast<const uint4*>(z + s.first + s.full0 * Slice<T, kThr>::kPer), s.full1 - s.full0, 4096);
   grid_dependency_wait();
   cluster_arrive_early(ranks);
   const float temperature = row_temperature(a.rows, row);

@@ -217,11 +217,12 @@ __global__ void __launch_bounds__(kThr, kOnSm) token_logprobs_kernel(const __gri
   const int ranks = int(cluster_size()), rank = int(cluster_rank()), row = int(blockIdx.x) / ranks;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   allow_dependent_launch();
+  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
+  const Part<T> s(z, a.rows.vocab, a.rows.slice, rank);
+  ask_early(a.rows, s.vec() + s.full0, s.full1 - s.full0, 2048);
   grid_dependency_wait();
   cluster_arrive_early(ranks);
 
-  const T* z = static_cast<const T*>(a.rows.logits) + int64_t(row) * a.rows.stride;
-  const Part<T> s(z, a.rows.vocab, a.rows.slice, rank);
   const float temperature = row_temperature(a.rows, row), c = __fdiv_rn(kLog2e, temperature);
   const int id = tid < a.count ? a.ids[int64_t(row) * a.count + tid] : -1;
   float* logprobs = a.logprobs + int64_t(row) * a.count;
