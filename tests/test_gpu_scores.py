@@ -8,10 +8,10 @@ ex2.approx (1.7e-7).  A sum of them adds at most 100 roundings one after another
 mean values, are within 2^-16 relative; values are then off by a few steps of
 2^-24 of the numbers they are made from: 2^-21 of those.  A weight of its own
 (a gradient's p_j) has |y| up to 126 before it is flushed: ln 2 * 126 * 3.5 *
-2^-24 = 1.8e-5, together below 2^-15.  A gradient whose argument is one fused multiply-add, z c
-plus a constant below 128 + 150, has that constant's rounding instead, 278 * 2^-24 ln
-2 = 1.1e-5, with z c's 2^-24 ln 2 * 128 * 2 the same 2^-15.  bf16 results: half a
-step, 2^-8."""
+2^-24 = 1.8e-5, together below 2^-15.  A gradient
+whose argument is one fused multiply-add, z c plus a constant below 128 + 150,
+has that constant's rounding instead, 278 * 2^-24 ln 2 = 1.1e-5, and c's own of
+2^-24 ln 2 * 256 = 1.1e-5: the same 2^-15.  bf16 results: half a step, 2^-8."""
 
 import numpy as np
 import pytest
@@ -373,6 +373,17 @@ def test_many_rows_by_small_thread_blocks(rows, vocab, count, top, dtype):
     assert int(st) == flag == 2
     values = np.log(rng.dirichlet(np.ones(count + 1), rows)[:, :count]).astype(np.float32)
     check_distill(view, z, ids, values, dtype, temperature=t, weight=h, flags=2)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(240, 33001, "f32"), (130, 100003, "bf16"), (130, 50021, "f32")])
+@pytest.mark.parametrize("count", [20, 64, 65])
+def test_distillation_of_long_slices(rows, vocab, dtype, count):
+    rng = np.random.default_rng(vocab + count)
+    view, z, _ = rows_of(rng, rows, vocab, dtype, masked=0.05, stride=vocab + 5)
+    ids = ids_for(rng, rows, vocab, count)
+    ids[2], ids[3, 1] = -1, ids[3, 0]
+    values = np.log(rng.dirichlet(np.ones(count + 1), rows)[:, :count]).astype(np.float32)
+    check_distill(view, z, ids, values, dtype, weight=rng.normal(0, 1, rows).astype(np.float32), tails=(1,))
 
 
 def all_calls(view, ids, g, h, values, stream=None):
