@@ -5,17 +5,18 @@
 // A row belongs to the CTAs of one cluster, which each keep a slice of it in shared
 // memory: fetched by bulk copies, summed, turned into gradients in place once the
 // cluster's sums are known, and sent off by bulk copies.  Three CTAs stand on an
-// SM, so that one loads or stores while the others compute.  What the teacher's row
-// gives (or the gradients of the log probabilities) is worked up by a ninth warp
-// while the slice arrives and is summed.
+// SM (five where slices are small), so that one loads or stores while the others
+// compute.  What the teacher's row gives (or the gradients of the log probabilities)
+// is worked up by a warp beside the workers while the slice arrives and is summed.
 //
 // Bound: HBM, every logit read once and every gradient written once, where slices
-// hide one another's phases: 4096 rows of 128256 in bf16 with 64 ids 358 us (87 % of
-// a plain copy), 8192 of 32000, a quarter of them padding, 139 (98 %), 4096 of 128256
-// with entropies 356 (76 %: two more multiply-adds per element in either sweep).
-// Tried: the row read again from L2 for its gradient (490 us for the first case);
-// persistent CTAs with two slices and a barrier between them (630), sums sent warp by
-// warp (582), and sixteen workers with warps of their own for copies and joins (522).
+// hide one another's phases: 4096 rows of 128256 in bf16 with 64 ids 341 us (91 % of
+// a plain copy), 8192 of 32000, a quarter of them padding, 137 (99 %), 4096 of 128256
+// with entropies 354 (77 %: two more multiply-adds per element in either sweep).
+// Tried, against 358 us for the first case as it then stood: the row read again from
+// L2 for its gradient (490); persistent CTAs with two slices and a barrier between
+// them (630), sums sent warp by warp (582), and sixteen workers with warps of their
+// own for copies and joins (522).
 //
 // Mathematics (scores.cuh for the sums).  Distillation, with R the statistics
 // outside the teacher's ids (whose places hold -inf while the rest is summed, so
