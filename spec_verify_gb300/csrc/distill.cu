@@ -19,7 +19,7 @@ namespace smp {
 
 // The loss alone: nothing has to stay on chip, so a row streams through one CTA
 // (or the CTAs of a cluster, where rows are few), and a bit per element says
-// which are the teacher's.  A ninth warp of the cluster's first CTA works up the
+// which are the teacher's.  A warp beside the workers of the first CTA works up the
 // teacher's row meanwhile.
 template <typename T, int kEach, int kThr, int kOnSm>
 __global__ void __launch_bounds__(kThr + 32, kOnSm) distill_loss_kernel(const __grid_constant__ RowGradArgs a) {

@@ -459,6 +459,35 @@ def test_offsets_past_32_bits():
     check_grad(scores.token_logprobs_grad(view, up(ids, torch.int32), up(g), out=view), want, reach, "bf16")
 
 
+def test_more_rows_than_65535():
+    g = torch.Generator("cuda").manual_seed(4)
+    rows, vocab = 200003, 5
+    view = torch.randn(rows, vocab, generator=g, device="cuda") * 3
+    ids = torch.randint(-1, vocab, (rows, 2), generator=g, device="cuda").int()
+    got = scores.token_logprobs(view, ids, top=3, entropy=True)
+    logp = view.double().log_softmax(1)
+    live = ids >= 0
+    want = logp.gather(1, ids.clamp(min=0).long()) * live
+    assert bool(((got.logprobs - want).abs() <= 2.0 ** -16 + 2.0 ** -21 * want.abs()).all())
+    entropy = -(logp.exp() * logp).sum(1)
+    assert bool(((got.entropy - entropy).abs() <= 2.0 ** -15 * (1 + entropy)).all())
+    best, at = logp.sort(1, descending=True, stable=True)
+    assert torch.equal(got.top_ids.long(), at[:, :3])
+    assert bool(((got.top_logprobs - best[:, :3]).abs() <= 2.0 ** -16 + 2.0 ** -21 * best[:, :3].abs()).all())
+    up_g = torch.randn(rows, 2, generator=g, device="cuda")
+    hot = torch.zeros(rows, vocab, dtype=torch.float64, device="cuda")
+    hot.scatter_add_(1, ids.clamp(min=0).long(), up_g.double() * live)
+    total, reach = (up_g.double() * live).sum(1, keepdim=True), (up_g.double().abs() * live).sum(1, keepdim=True)
+    grad = hot - logp.exp() * total
+    bound = 2.0 ** -15 * (logp.exp() * reach + (hot.abs() + reach * (hot != 0))) + 2.0 ** -120
+    assert bool(((scores.token_logprobs_grad(view, ids, up_g) - grad).abs() <= bound).all())
+    loss, dz = scores.distill_grad(view, ids[:, :1].contiguous(), torch.zeros(rows, 1, device="cuda"))
+    sure = ids[:, 0] >= 0                                 # a teacher that is sure: the loss is -ln p, its gradient p - 1
+    assert bool(((loss + want[:, 0]).abs() <= 2.0 ** -16 * (1 + want[:, 0].abs())).all())
+    one = torch.nn.functional.one_hot(ids[:, 0].clamp(min=0).long(), vocab)
+    assert bool(((dz - (logp.exp() - one) * sure[:, None]).abs() <= 2.0 ** -15 * (logp.exp() + one)).all())
+
+
 def test_no_rows_and_no_status():
     empty = torch.empty(0, 500, device="cuda")
     ids = torch.empty(0, 3, dtype=torch.int32, device="cuda")
