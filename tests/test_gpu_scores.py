@@ -471,7 +471,7 @@ def test_more_rows_than_65535():
     assert bool(((got.logprobs - want).abs() <= 2.0 ** -16 + 2.0 ** -21 * want.abs()).all())
     entropy = -(logp.exp() * logp).sum(1)
     assert bool(((got.entropy - entropy).abs() <= 2.0 ** -15 * (1 + entropy)).all())
-    best, at = logp.sort(1, descending=True, stable=True)
+    best, at = logp.sort(dim=1, descending=True, stable=True)
     assert torch.equal(got.top_ids.long(), at[:, :3])
     assert bool(((got.top_logprobs - best[:, :3]).abs() <= 2.0 ** -16 + 2.0 ** -21 * best[:, :3].abs()).all())
     up_g = torch.randn(rows, 2, generator=g, device="cuda")
