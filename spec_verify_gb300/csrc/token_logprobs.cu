@@ -406,7 +406,7 @@ static smp_status launch_scores(ScoreArgs a, cudaStream_t st) {
     if (fills(128)) return launch_scores_of<T, 128, 8>(a, ls, st);
   }
   // Halves of long rows where four on an SM hold them: 256 rows of 128256 in bf16 20.9 us, whole ones with three on an
-  // SM 22.5; 300 rows of 32000 in binary32 12.2 and 11.9.
+  // SM 22.8; 300 rows of 32000 in binary32 12.2 and 11.9.
   if (ls.cluster == 1 && !forced_cluster() && a.rows.rows <= 2 * sms && int64_t(a.rows.vocab) * int(sizeof(T)) >= 200 * 1024) {
     constexpr int kPer = RowVec<T>::kPer;
     ls.cluster = 2;
