@@ -289,7 +289,10 @@ __device__ __forceinline__ void each_unit(const Slice<T, kThr>& s, Take&& take) 
 // weight), and with weights none is -inf, nothing has to be looked at before it
 // enters the sums: y = z c - m c in one fused multiply-add, m the largest of the
 // first unit.  The sums say whether that held (they are finite); otherwise the
-// share is summed again with care, and `plain` is false.
+// share is summed again with care, and `plain` is false.  A sum of 2^16 or more is
+// brought below that by a higher reference, so that sums of many threads, warps
+// and CTAs stay far from binary32's ends, and so do what they are divided into.
+// Weighted sums are means of distances from m: plain up to 2^64, 45 T of them.
 template <bool kWeighted, typename T, int kThr>
 __device__ __forceinline__ Stats slice_stats(const Slice<T, kThr>& s, float temperature, float c, bool& plain) {
   using V = RowVec<T>;
@@ -318,11 +321,13 @@ __device__ __forceinline__ Stats slice_stats(const Slice<T, kThr>& s, float temp
   });
   const float sum = sum_of(z), sum_y = kWeighted ? sum_of(zy) : 0.0f, at_m = __fmul_rn(m, c);
   const bool none = int(threadIdx.x) >= s.vecs;
-  plain = __all_sync(~0u, none || (sum < INFINITY && fabsf(sum_y) < INFINITY && fabsf(at_m) < 0x1p20f));
-  if (plain) {   // the sums are relative to the rounded m c: y = (z - m) c + off
-    const float off = __fmaf_rn(m, c, -at_m), back = ex2_approx(-off);
+  plain = __all_sync(~0u, none || (sum < (kWeighted ? 0x1p64f : INFINITY) && fabsf(sum_y) < INFINITY && fabsf(at_m) < 0x1p20f));
+  if (plain) {   // the sums are relative to the rounded m c: y = (z - ref) c + off
+    float ref = m;
+    if (sum >= 0x1p16f) ref = __fadd_rn(m, __fdiv_rn(float((__float_as_int(sum) >> 23) - 127 - 15), c));
+    const float off = __fmaf_rn(ref, c, -at_m), back = ex2_approx(-off);
     Stats part{-INFINITY, 0.0f, 0.0f};
-    if (!none) part = Stats{m, sum * back, kWeighted ? __fdiv_rn(__fmaf_rn(-off, sum, sum_y), c) * back : 0.0f};
+    if (!none) part = Stats{ref, sum * back, kWeighted ? __fdiv_rn(__fmaf_rn(-off, sum, sum_y) * back, c) : 0.0f};
     return warp_join<kWeighted>(part, c);
   }
   Running<T, kWeighted> run;

@@ -51,9 +51,9 @@ struct RowsArgs {
   int first_round;    // CTAs that may stand before the kernel ahead has ended
 };
 
-// The statistics of some elements: one of them that none exceeds by much, sum
-// 2^((z - m) c) and, where wanted, the same weighted by z - m.  No elements: -inf,
-// 0, 0; +inf among them: m is +inf.
+// The statistics of some elements: a reference that none exceeds by more than 2^16
+// of weight, sum 2^((z - m) c) and, where wanted, the same weighted by z - m.  No
+// elements: -inf, 0, 0; +inf among them: m is +inf.
 struct Stats {
   float m, z, s;
 };
