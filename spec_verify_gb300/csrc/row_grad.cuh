@@ -355,9 +355,16 @@ __device__ __forceinline__ void slice_grad(const Slice<T, kThr>& s, float m, flo
 #pragma unroll 1
     for (; j < s.vecs; j += kThr) p[j] = turn(p[j]);
   };
-  if (plain && fabsf(__fmul_rn(m, c)) < 128.0f) {
-    if (kWeighted) {   // 2^y (A + (B / c) y), y = z c - m c
-      const pair_t shift = both(-__fmul_rn(m, c)), ca2 = both(ca), cb2 = both(__fdiv_rn(cb, c));
+  // With weights, 2^y (A + b y) with b = B / c and y = z c - m c has to be 0 wherever 2^y is, at a mask of -1e38 say:
+  // b y is finite for any finite y while |b| is below 1/2, so a larger b gives n of its powers of two to the other
+  // factor, as 2^(y + n) (2^-n (A - b n) + 2^-n b (y + n)).  It is larger where h is above 0.7 T Z: sums of entropies of
+  // sharp rows, which the careful sweep would slow down (4096 rows of 128256: 430 us, 421 this way).
+  const float b = kWeighted ? __fdiv_rn(cb, c) : 0.0f;
+  const int n = max(0, int(__float_as_uint(b) >> 23 & 255u) - 125);
+  if (plain && fabsf(__fmul_rn(m, c)) < 128.0f && n <= 16) {
+    if (kWeighted) {
+      const float lift = float(n), down = __int_as_float((127 - n) << 23);
+      const pair_t shift = both(__fmaf_rn(-m, c, lift)), ca2 = both(__fmaf_rn(-lift, b * down, ca * down)), cb2 = both(b * down);
       turn_all([&](const uint4& x) {
         pair_t v[V::kPer / 2];
         float r[V::kPer];
