@@ -291,8 +291,8 @@ __device__ __forceinline__ void each_unit(const Slice<T, kThr>& s, Take&& take) 
 // first unit.  The sums say whether that held (they are finite); otherwise the
 // share is summed again with care, and `plain` is false.  A sum of 2^16 or more is
 // brought below that by a higher reference, so that sums of many threads, warps
-// and CTAs stay far from binary32's ends, and so do what they are divided into.
-// Weighted sums are means of distances from m: plain up to 2^64, 45 T of them.
+// and CTAs stay far from binary32's ends, and so do what they are divided into
+// (weighted ones too: where sum_y is finite, sum is below 2^122).
 template <bool kWeighted, typename T, int kThr>
 __device__ __forceinline__ Stats slice_stats(const Slice<T, kThr>& s, float temperature, float c, bool& plain) {
   using V = RowVec<T>;
@@ -321,7 +321,7 @@ __device__ __forceinline__ Stats slice_stats(const Slice<T, kThr>& s, float temp
   });
   const float sum = sum_of(z), sum_y = kWeighted ? sum_of(zy) : 0.0f, at_m = __fmul_rn(m, c);
   const bool none = int(threadIdx.x) >= s.vecs;
-  plain = __all_sync(~0u, none || (sum < (kWeighted ? 0x1p64f : INFINITY) && fabsf(sum_y) < INFINITY && fabsf(at_m) < 0x1p20f));
+  plain = __all_sync(~0u, none || (sum < INFINITY && fabsf(sum_y) < INFINITY && fabsf(at_m) < 0x1p20f));
   if (plain) {   // the sums are relative to the rounded m c: y = (z - ref) c + off
     float ref = m;
     if (sum >= 0x1p16f) ref = __fadd_rn(m, __fdiv_rn(float((__float_as_int(sum) >> 23) - 127 - 15), c));

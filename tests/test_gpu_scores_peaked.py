@@ -5,8 +5,8 @@ Tolerances are those of test_gpu_scores.py.  With entropies the gradient also ha
 p h / T times (ln p + H), whose two parts are distances D from a reference that
 may nearly cancel: the mean of D is within 2^-16 of itself (the sums it comes
 from), and D itself has the rounding of z c and m c, 128 * 2^-24 at most.  D is the
-leaders' height above the row's bulk where that is the reference, up to 2^64 of
-weight, and 2^16 of weight else.  A weight below 2^-126 is flushed, and with it
+leaders' height above the row's bulk where sums are relative to that: 84 at most,
+since 2^121 times 121 is no finite sum; 2^16 of weight else.  A weight below 2^-126 is flushed, and with it
 what the gradient multiplies it by: up to 2^-126 (|G| + |h| (|ln p| + H)) / T, of
 which |ln p| is 128 ln 2 here (2^-120 alone allows for 64); what is flushed of yet
 smaller weights is less, p |ln p| falling with p."""
@@ -23,7 +23,7 @@ pytestmark = pytest.mark.gpu
 
 def check_scores_grad(view, z, ids, g, h, dtype, temperature, height):
     t = np.float32(temperature)
-    far = height if height < 64 * np.log(2) else 16 * np.log(2)
+    far = height if height < 84 else 16 * np.log(2)
     for entropies in (None, h):
         want, reach, flags = oracle.token_logprobs_grad(z, ids, g, entropies, t)
         if entropies is not None:
