@@ -62,7 +62,9 @@ extern "C" {
  *                with top 0): the tokens with the largest logits, in descending
  *                order, the lower id first among equal ones.  Tokens of
  *                probability 0 (-inf or NaN logits) are none: where fewer than
- *                `top` are left, the rest is id -1 with -inf.
+ *                `top` are left, the rest is id -1 with -inf.  Rows with hundreds
+ *                of equal logits among these, as under a finite mask that leaves
+ *                fewer than `top`, are read `top` times: mask with -inf.
  * Something has to be asked for (count, top or out_entropy).  A row whose ids
  * are all padding is not read when only log probabilities are asked for.
  */
@@ -86,7 +88,9 @@ smp_status smp_token_logprobs(const void* logits, int32_t rows, int32_t vocab, i
  *   out_grad     device, like logits with its own stride, written for every
  *                row; may be the logits themselves with the same stride (in
  *                place).  Rows that overlap the logits otherwise are refused; two
- *                blocks of columns of one tensor do not.
+ *                blocks of columns of one tensor do not.  Rows that do not lie to
+ *                16-byte boundaries as the logits' do are written element by
+ *                element, which takes up to 1.4 times as long.
  * A row without a token and with h = 0 is not read: its gradient is 0.
  */
 smp_status smp_token_logprobs_grad(const void* logits, int32_t rows, int32_t vocab, int64_t stride, smp_dtype dtype,

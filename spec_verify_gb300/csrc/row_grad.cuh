@@ -11,8 +11,12 @@
 //
 // Bound: HBM, every logit read once and every gradient written once, where slices
 // hide one another's phases: 4096 rows of 128256 in bf16 with 64 ids 341 us (91 % of
-// a plain copy), 8192 of 32000, a quarter of them padding, 137 (99 %), 4096 of 128256
-// with entropies 354 (77 %: two more multiply-adds per element in either sweep).
+// a plain copy), 8192 of 32000, a quarter of them padding, 137 (99 %).  With
+// entropies 354 for 4096 of 128256, a quarter padding (77 %), and 422 without padding
+// where ids alone take 363: a unit that a slice's end cuts short is filled with -inf,
+// which weighted sums take for a masked element, so that 12 of a row's 32 warps sum
+// their share twice and turn it with care (all 32 of 152064 tokens: 170 and 136).
+// Slices of whole units go without: 4096 rows of 32768 in 85, with ids alone 84.
 // Tried, against 358 us for the first case as it then stood: the row read again from
 // L2 for its gradient (490); persistent CTAs with two slices and a barrier between
 // them (630), sums sent warp by warp (582), and sixteen workers with warps of their
@@ -95,7 +99,8 @@ struct Slice {
   }
 
   // All workers: writes the slice to a row of the output, by bulk copies where
-  // that is aligned as the slice is; returns once `buf` has been read.
+  // that is aligned as the slice is and element by element where it is not (4096
+  // rows of 50021 in bf16 193 us and not 141); returns once `buf` has been read.
   __device__ __forceinline__ void leave(T* row) const {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     workers_sync<kThr>();
@@ -289,7 +294,8 @@ __device__ __forceinline__ void each_unit(const Slice<T, kThr>& s, Take&& take) 
 // weight), and with weights none is -inf, nothing has to be looked at before it
 // enters the sums: y = z c - m c in one fused multiply-add, m the largest of the
 // first unit.  The sums say whether that held (they are finite); otherwise the
-// share is summed again with care, and `plain` is false.  A sum of 2^16 or more is
+// share is summed again with care, and `plain` is false: so for weighted sums of a
+// unit that the slice's end cuts short, too, filled with -inf as it is.  A sum of 2^16 or more is
 // brought below that by a higher reference, so that sums of many threads, warps
 // and CTAs stay far from binary32's ends, and so do what they are divided into
 // (weighted ones too: where sum_y is finite, sum is below 2^122).
@@ -589,7 +595,8 @@ smp_status launch_row_grad(RowGradArgs a, cudaStream_t st) {
   // which every CTA of a cluster works up: 4096 rows of 128256 in bf16 with 64 ids 341 us and not 358, of 50021 in
   // binary32 273 and not 284, of 32000 159 and not 163; but with 100 ids 408 and not 397, of 50021 in bf16 (a pair, 50
   // KB) 139 and not 133, of 128256 in binary32 (eight) 228 and not 213 for 1200; log probabilities with entropies 377
-  // and not 355.
+  // and not 355, with most of their warps in the careful sums (above).  Clusters of 16, binary32 from 147454 tokens on:
+  // 1200 rows of 152064 277, ids alone 279 (78 and 77 % of a plain copy).
   if (kDistill && a.count <= 64 && int64_t(a.rows.rows) * c > 3 * sms &&
       (c == 4 ? slice(c) * elem > 42 * 1024 : c == 2 && slice(c) * elem > 60 * 1024))
     c *= 2;

@@ -73,7 +73,9 @@ def token_logprobs_grad(logits, ids, grad_logprobs, grad_entropy=None, temperatu
     gradients in the log probabilities (float32 [rows, count], as ids; both
     None: no ids) and the entropies (float32 [rows], or None) are given.  out:
     a tensor like the logits (the logits themselves: in place), or None for a
-    new one.  Returns it."""
+    new one, whose rows lie to 16-byte boundaries as the logits' do: others, as
+    torch.empty_like makes them for logits cut from wider rows, take up to 1.4
+    times as long.  Returns it."""
     native = step_module()
     if out is None:
         out = _beside(logits, stream)
@@ -107,8 +109,7 @@ def distill_grad(logits, teacher_ids, teacher_logprobs, weight=None, tail=False,
                  out=None, status=None, stream=None):
     """smp_distill: distill_loss and, in the same pass, the gradient in the
     logits of sum(weight * loss); weight: float32 [rows], or None for ones.
-    out: a tensor like the logits (the logits themselves: in place), or None
-    for a new one.  Returns (loss, gradient)."""
+    out: as for token_logprobs_grad.  Returns (loss, gradient)."""
     native = step_module()
     out_loss = _losses(logits, out_loss, stream)
     if out is None:
