@@ -142,7 +142,8 @@ def distill(z, ids, values, tail, weights=None, temperature=1.0):
             log_rest = beyond.max() + np.log(np.exp(beyond - beyond.max()).sum())
             loss[r] += rest * (np.log(rest) - log_rest)
             loss_reach[r] += rest * (abs(np.log(rest)) + abs(log_rest)) + 2.0 ** -16 * (1 + abs(np.log(rest)) + abs(log_rest))
-            part = np.where(outside, np.exp(np.where(outside, logp, -np.inf) - log_rest), 0.0) * rest
+            part = np.where(outside, np.exp(np.where(outside, logp, -np.inf) - beyond.max()), 0.0)
+            part *= rest / part.sum()                       # log_rest may have lost the logarithm of the sum, at masks of -1e38 say
             grad[r] = grad[r] - part
             reach[r] = reach[r] + part
         for i, share, _ in places:
